@@ -12,6 +12,11 @@ Functions mirror the C ABI in ``include/moe.h``:
     unpermute          -> moe_unpermute
     grouped_mlp_fwd    -> moe_grouped_mlp_fwd
     grouped_mlp_bwd    -> moe_grouped_mlp_bwd
+    router_loss        -> moe_router_loss (and router_loss_bwd)
+    grouped_linear     -> moe_grouped_linear (and grouped_linear_bwd)
+    checkpoint_pack    -> moe_checkpoint_pack (and checkpoint_unpack,
+                          permute_checkpoint, grouped_mlp_fwd_ckpt,
+                          grouped_mlp_bwd_routed_ckpt)
 """
 from __future__ import annotations
 
@@ -32,9 +37,14 @@ __all__ = [
     "grouped_gemm", "activation", "activation_bwd", "grouped_mlp_fwd_gather",
     "grouped_mlp_bwd_routed_gather", "route_logits", "FLAG_MX_SEPARATE_DH_QUANT",
     "mx_bwd_workspace_layout", "set_pair_mma",
+    "LINEAR_ACT", "router_loss", "router_loss_bwd", "router_loss_workspace_size", "grouped_linear",
+    "grouped_linear_bwd", "grouped_linear_bwd_workspace_size", "checkpoint_pack",
+    "checkpoint_unpack", "permute_checkpoint", "grouped_mlp_fwd_ckpt",
+    "grouped_mlp_bwd_routed_ckpt",
 ]
 
 ACT = {"swiglu": 0, "geglu": 1, "srelu": 2}
+LINEAR_ACT = {**ACT, "none": 3, "relu": 4, "silu": 5, "gelu": 6}
 FLAG_SAVE_H = 1
 FLAG_MXFP8 = 2
 FLAG_ACCUMULATE_DW = 4
@@ -148,6 +158,35 @@ def lib():
         L.moe_activation_bwd.argtypes = [vp, vp, vp, i32, i32, i32, i32, vp, vp]
         L.moe_router_grad_rows.restype = i32
         L.moe_router_grad_rows.argtypes = [vp, i32, vp, i32, i32, i32, vp, vp]
+        L.moe_router_loss_workspace_size.restype = sz
+        L.moe_router_loss_workspace_size.argtypes = [i32, i32, i32]
+        L.moe_router_loss.restype = i32
+        L.moe_router_loss.argtypes = [vp, i32, vp, i32, i32, i32, vp, i32, vp, vp, vp, vp, vp, vp,
+                                      sz, vp, vp]
+        L.moe_router_loss_bwd.restype = i32
+        L.moe_router_loss_bwd.argtypes = [vp, i32, vp, i32, i32, i32, vp, i32, vp, vp, vp, vp, vp,
+                                          vp, vp, vp, i32, vp]
+        L.moe_grouped_linear.restype = i32
+        L.moe_grouped_linear.argtypes = [vp, vp, i32, i32, i32, i32, vp, i32, vp, i32, vp, vp, vp,
+                                         i32, vp, vp]
+        L.moe_grouped_linear_bwd_workspace_size.restype = sz
+        L.moe_grouped_linear_bwd_workspace_size.argtypes = [i32, i32, i32]
+        L.moe_grouped_linear_bwd.restype = i32
+        L.moe_grouped_linear_bwd.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, vp, i32, i32, i32,
+                                             vp, vp, vp, vp, vp, sz, vp, vp]
+        L.moe_checkpoint_pack.restype = i32
+        L.moe_checkpoint_pack.argtypes = [vp, i32, i32, vp, vp, vp]
+        L.moe_checkpoint_unpack.restype = i32
+        L.moe_checkpoint_unpack.argtypes = [vp, vp, i32, i32, vp, vp]
+        L.moe_permute_checkpoint.restype = i32
+        L.moe_permute_checkpoint.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, vp, vp]
+        L.moe_grouped_mlp_fwd_ckpt.restype = i32
+        L.moe_grouped_mlp_fwd_ckpt.argtypes = [vp, vp, i32, i32, i32, i32, vp, vp, i32, vp, vp, vp,
+                                               vp, vp, vp]
+        L.moe_grouped_mlp_bwd_routed_ckpt.restype = i32
+        L.moe_grouped_mlp_bwd_routed_ckpt.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32,
+                                                      i32, vp, vp, i32, i32, vp, vp, vp, vp, vp,
+                                                      vp, vp, vp]
         L.moe_selftest_bounded_wait.restype = i32
         L.moe_selftest_bounded_wait.argtypes = [i32, vp, vp, vp]
         _LIB = L
@@ -828,3 +867,335 @@ def activation_bwd(h, da, offsets, act: str = "swiglu", dh=None, stream=None):
                                   ACT[act], _ptr(dh), _stream(stream))
     _check(rc, "moe_activation_bwd")
     return dh
+
+
+# ----------------------------------------------------------------- router losses
+
+_TYPE = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _float_type(t, name):
+    if t not in _TYPE:
+        raise MoeError(f"{name} must be torch.float32 or torch.bfloat16, got {t}")
+    return _TYPE[t]
+
+
+def _same_shape(t, shape, name):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise MoeError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def router_loss_workspace_size(T: int, E: int, S: int = 1) -> int:
+    return int(lib().moe_router_loss_workspace_size(T, E, S))
+
+
+def _router_args(logits, topk_idx, seg_offsets, token_mask):
+    lt = _float_type(logits.dtype, "logits")
+    _need(logits, logits.dtype, "logits", 2)
+    _need(topk_idx, torch.int32, "topk_idx", 2)
+    _need(seg_offsets, torch.int32, "seg_offsets", 1)
+    _need(token_mask, torch.uint8, "token_mask", 1)
+    T, E = logits.shape
+    if topk_idx.shape[0] != T or (token_mask is not None and token_mask.numel() != T):
+        raise MoeError("logits, topk_idx and token_mask must have the same number of tokens")
+    S = 1 if seg_offsets is None else seg_offsets.numel() - 1
+    return lt, T, E, topk_idx.shape[1], S
+
+
+def router_loss(logits: torch.Tensor, topk_idx: torch.Tensor, seg_offsets=None, token_mask=None,
+                err=None, out: dict | None = None, workspace=None, stream=None) -> dict:
+    """The router's load-balance and z losses with the per-expert counts
+    (moe_router_loss).  logits [T, E] float32 or bf16, topk_idx [T, k] int32,
+    seg_offsets [S+1] int32 (None: one sequence), token_mask [T] uint8 (None:
+    every token).  Returns a dict of device tensors: loss [2] (balance, z),
+    counts [S, E], lse [T], n_valid [S], err."""
+    lt, T, E, k, S = _router_args(logits, topk_idx, seg_offsets, token_mask)
+    dev = logits.device
+    o = out if out is not None else {
+        "loss": torch.empty(2, dtype=torch.float32, device=dev),
+        "counts": torch.empty((S, E), dtype=torch.int32, device=dev),
+        "lse": torch.empty(T, dtype=torch.float32, device=dev),
+        "n_valid": torch.empty(S, dtype=torch.int32, device=dev),
+    }
+    o["err"] = _err_word(err if err is not None else o.get("err"), dev)
+    if workspace is None:
+        workspace = torch.empty(max(router_loss_workspace_size(T, E, S), 16), dtype=torch.uint8,
+                                device=dev)
+    rc = lib().moe_router_loss(_ptr(logits), lt, _ptr(topk_idx), T, E, k, _ptr(seg_offsets), S,
+                               _ptr(token_mask), _ptr(o["loss"]), _ptr(o["counts"]),
+                               _ptr(o["lse"]), _ptr(o["n_valid"]), _ptr(workspace),
+                               workspace.numel() * workspace.element_size(), _ptr(o["err"]),
+                               _stream(stream))
+    _check(rc, "moe_router_loss")
+    return o
+
+
+def router_loss_bwd(logits: torch.Tensor, topk_idx: torch.Tensor, fwd: dict, dloss: torch.Tensor,
+                    probs=None, dprobs=None, seg_offsets=None, token_mask=None, dtype=None,
+                    dlogits=None, stream=None) -> torch.Tensor:
+    """Gradient of the logits (moe_router_loss_bwd): of dloss [2] times the
+    two losses and, with the router's probs and their gradient dprobs
+    [T, k], of the softmax over the selected logits.  fwd: the dict that
+    ``router_loss`` returned; dtype: of dlogits (float32, or bf16 for the
+    gate's weight gradient)."""
+    lt, T, E, k, S = _router_args(logits, topk_idx, seg_offsets, token_mask)
+    if dlogits is None:
+        dlogits = torch.empty((T, E), dtype=dtype or torch.float32, device=logits.device)
+    ot = _float_type(dlogits.dtype, "dlogits")
+    _need(dlogits, dlogits.dtype, "dlogits", 2)
+    for t, ty, nm, shape in ((dlogits, dlogits.dtype, "dlogits", (T, E)),
+                             (dloss, torch.float32, "dloss", (2,)),
+                             (probs, torch.float32, "probs", (T, k)),
+                             (dprobs, torch.float32, "dprobs", (T, k)),
+                             (fwd["lse"], torch.float32, "lse", (T,)),
+                             (fwd["counts"], torch.int32, "counts", (S, E)),
+                             (fwd["n_valid"], torch.int32, "n_valid", (S,))):
+        _need(t, ty, nm)
+        _same_shape(t, shape, nm)
+    rc = lib().moe_router_loss_bwd(_ptr(logits), lt, _ptr(topk_idx), T, E, k, _ptr(seg_offsets), S,
+                                   _ptr(token_mask), _ptr(fwd["lse"]), _ptr(fwd["counts"]),
+                                   _ptr(fwd["n_valid"]), _ptr(dloss), _ptr(probs), _ptr(dprobs),
+                                   _ptr(dlogits), ot, _stream(stream))
+    _check(rc, "moe_router_loss_bwd")
+    return dlogits
+
+
+# ----------------------------------------------------------------- linear
+
+def _linear_args(a, offsets, B, act, b_layout):
+    _need(a, torch.bfloat16, "a", 2)
+    _need(offsets, torch.int32, "offsets", 1)
+    _need(B, torch.bfloat16, "B")
+    if act not in LINEAR_ACT:
+        raise MoeError(f"act must be one of {sorted(LINEAR_ACT)}, got {act!r}")
+    if b_layout not in ("kn", "nk"):
+        raise MoeError(f"b_layout must be 'kn' or 'nk', got {b_layout!r}")
+    if B.dim() not in (2, 3):
+        raise MoeError("B must have 2 or 3 dims")
+    layout = 0 if b_layout == "kn" else 1
+    E = B.shape[0] if B.dim() == 3 else 1
+    K, N = (B.shape[-2], B.shape[-1]) if layout == 0 else (B.shape[-1], B.shape[-2])
+    if a.shape[1] != K or (offsets is not None and offsets.numel() != E + 1):
+        raise MoeError("inconsistent shapes")
+    gated = act in ("swiglu", "geglu")
+    return E, a.shape[0], K, N, layout, (N // 2 if gated else N)
+
+
+def grouped_linear(a: torch.Tensor, offsets, B: torch.Tensor, act: str = "none", bias=None,
+                   residual=None, b_layout: str = "kn", save_z: bool = False, out=None, z=None,
+                   out_dtype=torch.bfloat16, err=None, stream=None):
+    """out = act(a B_e + bias_e) + residual over the experts' rows
+    (moe_grouped_linear).  offsets [E+1] int32, or None for a dense product
+    (B [K, N], or [1, K, N]; b_layout "nk": B stored [N, K]).  act: "none",
+    "relu", "silu", "gelu", "srelu", or the gated "swiglu", "geglu" (columns
+    2j gate, 2j+1 up).  bias bf16 [E, N], residual bf16 [M, n_out] (may be
+    ``out``).  Returns (out, z, err); z, the bf16 pre-activation that the
+    backward reads, is None unless save_z or z is given."""
+    E, M_cap, K, N, layout, n_out = _linear_args(a, offsets, B, act, b_layout)
+    _need(bias, torch.bfloat16, "bias")
+    _need(residual, torch.bfloat16, "residual")
+    if bias is not None and bias.numel() != E * N:
+        raise MoeError("bias must hold E*N values")
+    _same_shape(residual, (M_cap, n_out), "residual")
+    if out is None:
+        out = torch.empty((M_cap, n_out), dtype=out_dtype, device=a.device)
+    ot = _float_type(out.dtype, "out")
+    _need(out, out.dtype, "out")
+    _same_shape(out, (M_cap, n_out), "out")
+    if save_z and z is None:
+        z = torch.empty((M_cap, N), dtype=torch.bfloat16, device=a.device)
+    _need(z, torch.bfloat16, "z")
+    _same_shape(z, (M_cap, N), "z")
+    err = _err_word(err, a.device)
+    rc = lib().moe_grouped_linear(_ptr(a), _ptr(offsets), E, M_cap, K, N, _ptr(B), layout,
+                                  _ptr(bias), LINEAR_ACT[act], _ptr(residual), _ptr(z), _ptr(out),
+                                  ot, _ptr(err), _stream(stream))
+    _check(rc, "moe_grouped_linear")
+    return out, z, err
+
+
+def grouped_linear_bwd_workspace_size(E: int, M_cap: int, N: int) -> int:
+    return int(lib().moe_grouped_linear_bwd_workspace_size(E, M_cap, N))
+
+
+def grouped_linear_bwd(dout: torch.Tensor, a: torch.Tensor, offsets, B: torch.Tensor,
+                       act: str = "none", z=None, bias: bool = False, b_layout: str = "kn",
+                       dz=None, da=None, dB=None, dbias=None, accumulate_dw: bool = False,
+                       workspace=None, err=None, stream=None):
+    """Backward of ``grouped_linear`` (moe_grouped_linear_bwd).  z: the saved
+    pre-activation (not needed for act "none"); bias: also the bias gradient.
+    Returns (dz, da, dB, dbias, err): dz is dout itself for act "none", dbias
+    (float32 [E, N]) None without bias; the residual's gradient is dout.
+    accumulate_dw adds to the given dB (and dbias)."""
+    E, M_cap, K, N, layout, n_out = _linear_args(a, offsets, B, act, b_layout)
+    _need(dout, torch.bfloat16, "dout", 2)
+    _same_shape(dout, (M_cap, n_out), "dout")
+    _need(z, torch.bfloat16, "z")
+    _same_shape(z, (M_cap, N), "z")
+    if act != "none" and z is None:
+        raise MoeError("act needs the saved pre-activation z")
+    bias = bias or dbias is not None
+    if accumulate_dw and (dB is None or (bias and dbias is None)):
+        raise ValueError("accumulate_dw needs the dB (and dbias) to accumulate into")
+    dev = a.device
+    if act != "none" and dz is None:
+        dz = torch.empty((M_cap, N), dtype=torch.bfloat16, device=dev)
+    if da is None:
+        da = torch.empty((M_cap, K), dtype=torch.bfloat16, device=dev)
+    if dB is None:
+        dB = torch.empty_like(B)
+    if bias and dbias is None:
+        dbias = torch.empty((E, N), dtype=torch.float32, device=dev)
+    for t, ty, nm, shape in ((dz, torch.bfloat16, "dz", (M_cap, N)),
+                             (da, torch.bfloat16, "da", (M_cap, K)),
+                             (dB, torch.bfloat16, "dB", tuple(B.shape)),
+                             (dbias, torch.float32, "dbias", (E, N))):
+        _need(t, ty, nm)
+        _same_shape(t, shape, nm)
+    if bias and workspace is None:
+        workspace = torch.empty(max(grouped_linear_bwd_workspace_size(E, M_cap, N), 16),
+                                dtype=torch.uint8, device=dev)
+    err = _err_word(err, dev)
+    rc = lib().moe_grouped_linear_bwd(
+        _ptr(dout), _ptr(z), _ptr(a), _ptr(offsets), E, M_cap, K, N, _ptr(B), layout,
+        LINEAR_ACT[act], FLAG_ACCUMULATE_DW if accumulate_dw else 0, _ptr(dz), _ptr(da), _ptr(dB),
+        _ptr(dbias), _ptr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _ptr(err),
+        _stream(stream))
+    _check(rc, "moe_grouped_linear_bwd")
+    return (dout if act == "none" else dz), da, dB, dbias, err
+
+
+# ----------------------------------------------------------------- 8-bit checkpoints
+
+def checkpoint_pack(src: torch.Tensor, q=None, s=None, stream=None):
+    """Rows [rows, cols] bf16 in 8 bits (moe_checkpoint_pack): E4M3 codes q
+    [rows, cols] and one E8M0 scale per 32 values of a row, s [rows, cols/32]
+    (both uint8).  Returns (q, s)."""
+    _need(src, torch.bfloat16, "src", 2)
+    rows, cols = src.shape
+    if q is None:
+        q = torch.empty((rows, cols), dtype=torch.uint8, device=src.device)
+    if s is None:
+        s = torch.empty((rows, cols // 32), dtype=torch.uint8, device=src.device)
+    for t, nm, shape in ((q, "q", (rows, cols)), (s, "s", (rows, cols // 32))):
+        _need(t, torch.uint8, nm)
+        _same_shape(t, shape, nm)
+    rc = lib().moe_checkpoint_pack(_ptr(src), rows, cols, _ptr(q), _ptr(s), _stream(stream))
+    _check(rc, "moe_checkpoint_pack")
+    return q, s
+
+
+def _ckpt_args(q, s, name):
+    _need(q, torch.uint8, name + "_q", 2)
+    _need(s, torch.uint8, name + "_s", 2)
+    _same_shape(s, (q.shape[0], q.shape[1] // 32), name + "_s")
+    return q.shape
+
+
+def checkpoint_unpack(q: torch.Tensor, s: torch.Tensor, out=None, stream=None) -> torch.Tensor:
+    """The bf16 values of a checkpoint (moe_checkpoint_unpack), exact."""
+    rows, cols = _ckpt_args(q, s, "checkpoint")
+    if out is None:
+        out = torch.empty((rows, cols), dtype=torch.bfloat16, device=q.device)
+    _need(out, torch.bfloat16, "out", 2)
+    _same_shape(out, (rows, cols), "out")
+    rc = lib().moe_checkpoint_unpack(_ptr(q), _ptr(s), rows, cols, _ptr(out), _stream(stream))
+    _check(rc, "moe_checkpoint_unpack")
+    return out
+
+
+def permute_checkpoint(q: torch.Tensor, s: torch.Tensor, pair_of_row: torch.Tensor, k: int,
+                       row_of_pair=None, out=None, stream=None) -> torch.Tensor:
+    """``permute`` from packed token rows (moe_permute_checkpoint): expert-major
+    bf16 rows, zeros for pad rows; with row_of_pair in token order."""
+    T, d = _ckpt_args(q, s, "checkpoint")
+    _need(pair_of_row, torch.int32, "pair_of_row", 1)
+    _need(row_of_pair, torch.int32, "row_of_pair", 1)
+    if row_of_pair is not None and row_of_pair.numel() != T * k:
+        raise MoeError("row_of_pair must hold T*k entries")
+    M_cap = pair_of_row.numel()
+    if out is None:
+        out = torch.empty((M_cap, d), dtype=torch.bfloat16, device=q.device)
+    _need(out, torch.bfloat16, "out", 2)
+    _same_shape(out, (M_cap, d), "out")
+    rc = lib().moe_permute_checkpoint(_ptr(q), _ptr(s), _ptr(row_of_pair), _ptr(pair_of_row), T, k,
+                                      d, M_cap, _ptr(out), _stream(stream))
+    _check(rc, "moe_permute_checkpoint")
+    return out
+
+
+def grouped_mlp_fwd_ckpt(x_perm: torch.Tensor, offsets: torch.Tensor, W1: torch.Tensor,
+                         W2: torch.Tensor, act: str = "swiglu", h_q=None, h_s=None, a=None,
+                         y_perm=None, err=None, stream=None):
+    """Grouped expert MLP forward that keeps H in 8 bits
+    (moe_grouped_mlp_fwd_ckpt).  Returns (h_q, h_s, a, y_perm, err); a and
+    y_perm are ``grouped_mlp_fwd``'s bit for bit."""
+    _need(x_perm, torch.bfloat16, "x_perm", 2)
+    _need(offsets, torch.int32, "offsets", 1)
+    _need(W1, torch.bfloat16, "W1", 3)
+    _need(W2, torch.bfloat16, "W2", 3)
+    M_cap, d = x_perm.shape
+    E, n, d2 = W2.shape
+    n1 = n if act == "srelu" else 2 * n
+    if d2 != d or tuple(W1.shape) != (E, d, n1) or offsets.numel() != E + 1:
+        raise MoeError("inconsistent shapes")
+    dev = x_perm.device
+    if h_q is None:
+        h_q = torch.empty((M_cap, n1), dtype=torch.uint8, device=dev)
+    if h_s is None:
+        h_s = torch.empty((M_cap, n1 // 32), dtype=torch.uint8, device=dev)
+    if a is None:
+        a = torch.empty((M_cap, n), dtype=torch.bfloat16, device=dev)
+    if y_perm is None:
+        y_perm = torch.empty((M_cap, d), dtype=torch.bfloat16, device=dev)
+    _ckpt_args(h_q, h_s, "h")
+    _same_shape(h_q, (M_cap, n1), "h_q")
+    err = _err_word(err, dev)
+    rc = lib().moe_grouped_mlp_fwd_ckpt(_ptr(x_perm), _ptr(offsets), E, M_cap, d, n, _ptr(W1),
+                                        _ptr(W2), ACT[act], _ptr(h_q), _ptr(h_s), _ptr(a),
+                                        _ptr(y_perm), _ptr(err), _stream(stream))
+    _check(rc, "moe_grouped_mlp_fwd_ckpt")
+    return h_q, h_s, a, y_perm, err
+
+
+def grouped_mlp_bwd_routed_ckpt(x_perm, h_q, h_s, do_perm, pair_of_row, probs, offsets, W1, W2,
+                                act: str = "swiglu", dh=None, a_scaled=None, ds_part=None,
+                                dx_perm=None, dW1=None, dW2=None, err=None, stream=None,
+                                accumulate_dw: bool = False):
+    """Routed backward from the 8-bit H (moe_grouped_mlp_bwd_routed_ckpt).
+    Returns (dh, a_scaled, ds_part, dx_perm, dW1, dW2, err) like
+    ``grouped_mlp_bwd_routed``."""
+    flags = _bwd_flags(accumulate_dw, dW1, dW2)
+    for t, nm in ((x_perm, "x_perm"), (do_perm, "do_perm"), (W1, "W1"), (W2, "W2")):
+        _need(t, torch.bfloat16, nm)
+    _need(pair_of_row, torch.int32, "pair_of_row", 1)
+    _need(probs, torch.float32, "probs")
+    _need(offsets, torch.int32, "offsets", 1)
+    M_cap, d = x_perm.shape
+    E, n, _ = W2.shape
+    n1 = n if act == "srelu" else 2 * n
+    _ckpt_args(h_q, h_s, "h")
+    _same_shape(h_q, (M_cap, n1), "h_q")
+    dev = x_perm.device
+    bf = torch.bfloat16
+    if dh is None:
+        dh = torch.empty((M_cap, n1), dtype=bf, device=dev)
+    if a_scaled is None:
+        a_scaled = torch.empty((M_cap, n), dtype=bf, device=dev)
+    if ds_part is None:
+        ds_part = torch.empty((M_cap, (n + 127) // 128), dtype=torch.float32, device=dev)
+    if dx_perm is None:
+        dx_perm = torch.empty((M_cap, d), dtype=bf, device=dev)
+    if dW1 is None:
+        dW1 = torch.empty((E, d, n1), dtype=bf, device=dev)
+    if dW2 is None:
+        dW2 = torch.empty((E, n, d), dtype=bf, device=dev)
+    err = _err_word(err, dev)
+    rc = lib().moe_grouped_mlp_bwd_routed_ckpt(
+        _ptr(x_perm), _ptr(h_q), _ptr(h_s), _ptr(do_perm), _ptr(pair_of_row), _ptr(probs),
+        _ptr(offsets), E, M_cap, d, n, _ptr(W1), _ptr(W2), ACT[act], flags, _ptr(dh),
+        _ptr(a_scaled), _ptr(ds_part), _ptr(dx_perm), _ptr(dW1), _ptr(dW2), _ptr(err),
+        _stream(stream))
+    _check(rc, "moe_grouped_mlp_bwd_routed_ckpt")
+    return dh, a_scaled, ds_part, dx_perm, dW1, dW2, err

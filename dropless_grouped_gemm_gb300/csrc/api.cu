@@ -10,7 +10,10 @@
 #include <mutex>
 
 #include "../../include/moe.h"
+#include "ckpt.cuh"
 #include "gemm.cuh"
+#include "linear.cuh"
+#include "loss.cuh"
 #include "mxgemm.cuh"
 #include "route.cuh"
 
@@ -179,6 +182,14 @@ bool map_out2(CUtensorMap* m, const void* p, int rows, int cols) {
   return make_map(m, p, 2, dims, box, false, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
+// [rows, cols] 8-bit codes written by staged TMA stores of FC1: box 64 cols
+// x 32 rows, 64-byte swizzle
+bool map_codes_out(CUtensorMap* m, const void* p, int rows, int cols) {
+  const uint64_t dims[2] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows)};
+  const uint32_t box[2] = {64, 32};
+  return make_map(m, p, 2, dims, box, true, CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
 int cuda_rc(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_E_CUDA; }
 
 int check_mlp_sizes(int E, int M_cap, int d, int n) {
@@ -188,12 +199,34 @@ int check_mlp_sizes(int E, int M_cap, int d, int n) {
   return MOE_OK;
 }
 
+int check_loss(int T, int E, int k, const int32_t* seg, int S, int type) {
+  if (T < 0 || E < 1 || E > MOE_MAX_EXPERTS || k < 1 || k > E || S < 1 || S > moe::kMaxSegments)
+    return MOE_E_SIZE;
+  if (static_cast<long long>(T) * k >= (1LL << 31)) return MOE_E_SIZE;
+  if (!seg && S != 1) return MOE_E_SIZE;
+  if (type != MOE_TYPE_F32 && type != MOE_TYPE_BF16) return MOE_E_ARG;
+  return MOE_OK;
+}
+
+bool linear_gated(int act) { return act == MOE_ACT_SWIGLU || act == MOE_ACT_GEGLU; }
+
+int check_linear(const int32_t* offsets, int E, int M_cap, int K, int N, int b_layout, int act) {
+  const int rc = check_mlp_sizes(E, M_cap, K, N);
+  if (rc) return rc;
+  if (static_cast<long long>(M_cap) * K >= (1LL << 40)) return MOE_E_SIZE;
+  if (!offsets && E != 1) return MOE_E_SIZE;
+  if (b_layout != MOE_B_KN && b_layout != MOE_B_NK) return MOE_E_ARG;
+  if (act < MOE_ACT_SWIGLU || act > MOE_ACT_GELU) return MOE_E_ARG;
+  return MOE_OK;
+}
+
 // The four backward GEMMs.  dy is FC2-dgrad's A operand and FC2-wgrad's B
 // operand, a_w FC2-wgrad's A operand.  Routed (probs != NULL): dy is the
 // unscaled gathered dO; FC2-dgrad applies each row's router probability in
 // its epilogue, which also writes A' (= a_w) and the dS partials.  With
 // x_tok / do_tok (routed only) the token tensors x [T, d] and dO [T, d]
 // replace x_perm and dy: the GEMMs read their rows through pair_of_row.
+// With h_q / h_s, FC2-dgrad reads H from its 8-bit checkpoint.
 int bwd_gemms(const moe_bf16* x_perm, const moe_bf16* h_saved, const moe_bf16* a_w,
               const moe_bf16* dy, const int32_t* offsets, int E, int M_cap, int d, int n,
               const moe_bf16* W1, const moe_bf16* W2, int act, moe_bf16* dh, moe_bf16* dx_perm,
@@ -201,7 +234,7 @@ int bwd_gemms(const moe_bf16* x_perm, const moe_bf16* h_saved, const moe_bf16* a
               const int32_t* pair_of_row, const float* probs, moe_bf16* a_scaled,
               float* ds_part, float* amax_dh, bool accumulate,
               const moe_bf16* x_tok = nullptr, const moe_bf16* do_tok = nullptr, int T = 0,
-              int k = 1) {
+              int k = 1, const uint8_t* h_q = nullptr, const uint8_t* h_s = nullptr) {
   const bool gather = x_tok != nullptr;
   const int n1 = (act == MOE_ACT_SRELU) ? n : 2 * n;
   moe::GemmArgs probe{};
@@ -232,6 +265,8 @@ int bwd_gemms(const moe_bf16* x_perm, const moe_bf16* h_saved, const moe_bf16* a
   moe::GemmArgs g{};
   g.offsets = offsets; g.E = E; g.M_cap = M_cap; g.K = d; g.N = n;
   g.out = dh; g.ldo = n1; g.aux = h_saved; g.ld_aux = n1; g.err = err; g.amax = amax_dh;
+  g.h_q = const_cast<uint8_t*>(h_q);   // H in 8 bits (read only) instead of h_saved
+  g.h_s = const_cast<uint8_t*>(h_s);
   if (probs) {
     g.pair_of_row = pair_of_row; g.probs = probs; g.out3 = a_scaled; g.ldo3 = n;
     g.ds_part = ds_part; g.ds_parts = (n + 127) / 128;
@@ -1076,6 +1111,352 @@ int moe_mx_quantize_tiled(const moe_bf16* src, int rows, int cols, const int32_t
   ev_end(s);
   g_last_launches = 1 + g_split_extra;
   return cuda_rc(e);
+}
+
+// ------------------------------------------------ router losses
+
+size_t moe_router_loss_workspace_size(int T, int E, int S) {
+  if (T < 0 || E < 1 || E > MOE_MAX_EXPERTS || S < 1 || S > moe::kMaxSegments) return 0;
+  return moe::router_loss_workspace_bytes(T, E, S);
+}
+
+int moe_router_loss(const void* logits, int logits_type, const int32_t* topk_idx, int T, int E,
+                    int k, const int32_t* seg_offsets, int S, const uint8_t* token_mask,
+                    float* loss, int32_t* counts, float* lse, int32_t* n_valid, void* workspace,
+                    size_t ws_bytes, int32_t* err, void* stream) {
+  g_last_launches = 0;
+  g_split_extra = 0;
+  const int rc = check_loss(T, E, k, seg_offsets, S, logits_type);
+  if (rc) return rc;
+  if (!loss || !counts || !n_valid || !err) return MOE_E_NULL;
+  if (T > 0 && (!logits || !topk_idx || !lse)) return MOE_E_NULL;
+  if (misaligned(logits)) return MOE_E_ALIGN;
+  if (ws_bytes < moe::router_loss_workspace_bytes(T, E, S)) return MOE_E_WORKSPACE;
+  if (!workspace) return MOE_E_NULL;
+  if (misaligned(workspace)) return MOE_E_ALIGN;
+  const int sms = num_sms_current();
+  if (sms <= 0) return MOE_E_CUDA;
+  moe::RouterLossArgs a{};
+  a.logits = logits; a.logits_bf16 = logits_type == MOE_TYPE_BF16; a.idx = topk_idx;
+  a.T = T; a.E = E; a.k = k; a.seg = seg_offsets; a.S = S; a.mask = token_mask; a.err = err;
+  a.loss = loss; a.counts = counts; a.lse = lse; a.n_valid = n_valid; a.ws = workspace;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int launches = 0;
+  ev_begin(s);
+  const cudaError_t e = moe::launch_router_loss(a, sms, s, &launches);
+  ev_end(s);
+  g_last_launches = launches;
+  return cuda_rc(e);
+}
+
+int moe_router_loss_bwd(const void* logits, int logits_type, const int32_t* topk_idx, int T, int E,
+                        int k, const int32_t* seg_offsets, int S, const uint8_t* token_mask,
+                        const float* lse, const int32_t* counts, const int32_t* n_valid,
+                        const float* dloss, const float* probs, const float* dprobs,
+                        void* dlogits, int dlogits_type, void* stream) {
+  g_last_launches = 0;
+  g_split_extra = 0;
+  int rc = check_loss(T, E, k, seg_offsets, S, logits_type);
+  if (rc == MOE_OK) rc = check_loss(T, E, k, seg_offsets, S, dlogits_type);
+  if (rc) return rc;
+  if (T == 0) return MOE_OK;
+  if (!logits || !topk_idx || !lse || !counts || !n_valid || !dloss || !dlogits) return MOE_E_NULL;
+  if ((probs == nullptr) != (dprobs == nullptr)) return MOE_E_NULL;
+  if (misaligned(logits) || misaligned(dlogits)) return MOE_E_ALIGN;
+  const int sms = num_sms_current();
+  if (sms <= 0) return MOE_E_CUDA;
+  moe::RouterLossArgs a{};
+  a.logits = logits; a.logits_bf16 = logits_type == MOE_TYPE_BF16; a.idx = topk_idx;
+  a.T = T; a.E = E; a.k = k; a.seg = seg_offsets; a.S = S; a.mask = token_mask;
+  a.counts = const_cast<int32_t*>(counts); a.lse = const_cast<float*>(lse);
+  a.n_valid = const_cast<int32_t*>(n_valid);
+  a.dloss = dloss; a.probs = probs; a.dprobs = dprobs;
+  a.dlogits = dlogits; a.dlogits_bf16 = dlogits_type == MOE_TYPE_BF16;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  ev_begin(s);
+  const cudaError_t e = moe::launch_router_loss_bwd(a, sms, s);
+  ev_end(s);
+  g_last_launches = 1;
+  return cuda_rc(e);
+}
+
+// ------------------------------------------------ linear
+
+int moe_grouped_linear(const moe_bf16* a, const int32_t* offsets, int E, int M_cap, int K, int N,
+                       const moe_bf16* B, int b_layout, const moe_bf16* bias, int act,
+                       const moe_bf16* residual, moe_bf16* z, void* out, int out_type,
+                       int32_t* err, void* stream) {
+  g_last_launches = 0;
+  g_split_extra = 0;
+  const int rc = check_linear(offsets, E, M_cap, K, N, b_layout, act);
+  if (rc) return rc;
+  if (out_type != MOE_TYPE_F32 && out_type != MOE_TYPE_BF16) return MOE_E_ARG;
+  if (!B || !err) return MOE_E_NULL;
+  if (M_cap == 0) return MOE_OK;
+  if (!a || !out) return MOE_E_NULL;
+  if (misaligned(a) || misaligned(B) || misaligned(bias) || misaligned(residual) ||
+      misaligned(z) || misaligned(out))
+    return MOE_E_ALIGN;
+  const int sms = num_sms_current();
+  if (sms <= 0) return MOE_E_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool kn = b_layout == MOE_B_KN;
+  const int n_out = linear_gated(act) ? N / 2 : N;
+  const bool f32 = out_type == MOE_TYPE_F32;
+  CUtensorMap tb;
+  if (kn ? !map_w(&tb, B, E, K, N, 64) : !map_w(&tb, B, E, N, K, 128)) return MOE_E_CUDA;
+  const moe::FewPlan plan = moe::few_plan(E, M_cap, K, N, offsets != nullptr, sms);
+  CUtensorMap ta;
+  if (!map_act(&ta, a, M_cap, K, plan.tn ? plan.tn : moe::kBM)) return MOE_E_CUDA;
+  if (plan.tn) {
+    moe::FewArgs g{};
+    g.offsets = offsets; g.E = E; g.M_cap = M_cap; g.K = K; g.N = N; g.bias = bias; g.act = act;
+    g.residual = residual; g.z = z; g.ldo = n_out; g.err = err;
+    g.out = f32 ? nullptr : static_cast<uint16_t*>(out);
+    g.out_f32 = f32 ? static_cast<float*>(out) : nullptr;
+    ev_begin(s);
+    const cudaError_t e = moe::launch_few(tb, ta, kn, g, plan, sms, s);
+    ev_end(s);
+    g_last_launches = 1;
+    return cuda_rc(e);
+  }
+  moe::GemmArgs g{};
+  g.offsets = offsets; g.E = E; g.M_cap = M_cap; g.K = K; g.N = N; g.err = err;
+  g.act = act; g.bias = bias; g.residual = residual; g.out2 = z; g.ldo2 = N; g.ldo = n_out;
+  g.out = f32 ? nullptr : static_cast<uint16_t*>(out);
+  g.out_f32 = f32 ? static_cast<float*>(out) : nullptr;
+  CUtensorMap tz = ta, to = ta;
+  if ((z && !map_out2(&tz, z, M_cap, N)) || (!f32 && !map_out2(&to, out, M_cap, n_out)))
+    return MOE_E_CUDA;
+  g.tma_out = 1;
+  const cudaError_t e = gemm(kn ? moe::GemmKind::kLinearKN : moe::GemmKind::kLinearNK, act, ta, tb,
+                             tz, g, sms, s, &to);
+  if (e != cudaSuccess) return MOE_E_CUDA;
+  g_last_launches = 1 + g_split_extra;
+  return MOE_OK;
+}
+
+size_t moe_grouped_linear_bwd_workspace_size(int E, int M_cap, int N) {
+  if (E < 1 || E > MOE_MAX_EXPERTS || M_cap < 0 || N <= 0) return 0;
+  return moe::linear_dz_workspace_bytes(E, M_cap, N);
+}
+
+int moe_grouped_linear_bwd(const moe_bf16* dout, const moe_bf16* z, const moe_bf16* a,
+                           const int32_t* offsets, int E, int M_cap, int K, int N,
+                           const moe_bf16* B, int b_layout, int act, int flags, moe_bf16* dz,
+                           moe_bf16* da, moe_bf16* dB, float* dbias, void* workspace,
+                           size_t ws_bytes, int32_t* err, void* stream) {
+  g_last_launches = 0;
+  g_split_extra = 0;
+  const int rc = check_linear(offsets, E, M_cap, K, N, b_layout, act);
+  if (rc) return rc;
+  if (flags & ~MOE_FLAG_ACCUMULATE_DW) return MOE_E_ARG;
+  const bool accumulate = flags & MOE_FLAG_ACCUMULATE_DW;
+  if (!err || (da && !B)) return MOE_E_NULL;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (M_cap == 0) {
+    if (accumulate) return MOE_OK;
+    cudaError_t e = cudaSuccess;
+    if (dB) e = cudaMemsetAsync(dB, 0, static_cast<size_t>(E) * K * N * 2, s);
+    if (dbias && e == cudaSuccess) e = cudaMemsetAsync(dbias, 0, static_cast<size_t>(E) * N * 4, s);
+    return cuda_rc(e);
+  }
+  if (!dout || (dB && !a)) return MOE_E_NULL;
+  if (act != MOE_ACT_NONE && (!z || !dz)) return MOE_E_NULL;
+  if (misaligned(dout) || misaligned(z) || misaligned(a) || misaligned(B) || misaligned(dz) ||
+      misaligned(da) || misaligned(dB) || misaligned(dbias))
+    return MOE_E_ALIGN;
+  if (dbias) {
+    if (ws_bytes < moe::linear_dz_workspace_bytes(E, M_cap, N)) return MOE_E_WORKSPACE;
+    if (!workspace) return MOE_E_NULL;
+    if (misaligned(workspace)) return MOE_E_ALIGN;
+  }
+  const int sms = num_sms_current();
+  if (sms <= 0) return MOE_E_CUDA;
+  const bool kn = b_layout == MOE_B_KN;
+  int launches = 0;
+  // 1. dz and the bias gradient's column sums (act none without a bias
+  //    gradient: dz is dout, nothing to do)
+  if (act != MOE_ACT_NONE || dbias) {
+    moe::LinearDzArgs q{};
+    q.dout = dout; q.z = act == MOE_ACT_NONE ? nullptr : z; q.offsets = offsets; q.E = E;
+    q.M_cap = M_cap; q.N = N; q.act = act; q.dz = act == MOE_ACT_NONE ? nullptr : dz;
+    q.dbias = dbias; q.accumulate = accumulate; q.part = static_cast<float*>(workspace);
+    q.err = err;
+    ev_begin(s);
+    const cudaError_t e = moe::launch_linear_dz(q, s, &launches);
+    ev_end(s);
+    if (e != cudaSuccess) return MOE_E_CUDA;
+  }
+  const moe_bf16* gz = act == MOE_ACT_NONE ? dout : dz;
+  // 2. da = dz B^T
+  if (da) {
+    CUtensorMap ta, tb, to;
+    if (!map_act(&ta, gz, M_cap, N, moe::kBM) || !map_out2(&to, da, M_cap, K) ||
+        (kn ? !map_w(&tb, B, E, K, N, 128) : !map_w(&tb, B, E, N, K, 64)))
+      return MOE_E_CUDA;
+    moe::GemmArgs g{};
+    g.offsets = offsets; g.E = E; g.M_cap = M_cap; g.K = N; g.N = K;
+    g.out = da; g.ldo = K; g.err = err; g.tma_out = 1;
+    if (gemm(kn ? moe::GemmKind::kDgrad : moe::GemmKind::kFc2, 0, ta, tb, to, g, sms, s) !=
+        cudaSuccess)
+      return MOE_E_CUDA;
+    ++launches;
+  }
+  // 3. dB_e = a_e^T dz_e, or its transpose for B stored [E, N, K]
+  if (dB) {
+    const int R = kn ? K : N, C = kn ? N : K;
+    moe::GemmArgs g{};
+    g.offsets = offsets; g.E = E; g.M_cap = M_cap; g.N = C; g.R = R;
+    g.out = dB; g.ldo = C; g.out_estride = static_cast<long long>(R) * C; g.err = err;
+    g.accumulate = accumulate;
+    const bool skinny = moe::wgrad_skinny(g);
+    CUtensorMap tl, tr, to, to_l;
+    if (!map_act(&tl, kn ? a : gz, M_cap, R, 64) || !map_act(&tr, kn ? gz : a, M_cap, C, 64) ||
+        !map_out3(&to, dB, E, R, C, skinny) || (skinny && !map_out3(&to_l, dB, E, R, C, false)))
+      return MOE_E_CUDA;
+    if (gemm(moe::GemmKind::kWgrad, 0, tl, tr, to, g, sms, s, skinny ? &to_l : nullptr) !=
+        cudaSuccess)
+      return MOE_E_CUDA;
+    ++launches;
+  }
+  g_last_launches = launches + g_split_extra;
+  return MOE_OK;
+}
+
+// ------------------------------------------------ 8-bit checkpoints
+int moe_checkpoint_pack(const moe_bf16* src, int rows, int cols, uint8_t* q, uint8_t* s,
+                        void* stream) {
+  g_last_launches = 0;
+  g_split_extra = 0;
+  if (rows < 0 || cols <= 0 || cols % 64) return MOE_E_SIZE;
+  const long long n = static_cast<long long>(rows) * cols;
+  if (n >= (1LL << 40)) return MOE_E_SIZE;
+  if (rows == 0) return MOE_OK;
+  if (!src || !q || !s) return MOE_E_NULL;
+  if (misaligned(src) || misaligned(q)) return MOE_E_ALIGN;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  ev_begin(st);
+  const cudaError_t e = moe::launch_ckpt_pack(src, n, q, s, st);
+  ev_end(st);
+  g_last_launches = 1;
+  return cuda_rc(e);
+}
+
+int moe_checkpoint_unpack(const uint8_t* q, const uint8_t* s, int rows, int cols, moe_bf16* dst,
+                          void* stream) {
+  g_last_launches = 0;
+  g_split_extra = 0;
+  if (rows < 0 || cols <= 0 || cols % 64) return MOE_E_SIZE;
+  const long long n = static_cast<long long>(rows) * cols;
+  if (n >= (1LL << 40)) return MOE_E_SIZE;
+  if (rows == 0) return MOE_OK;
+  if (!q || !s || !dst) return MOE_E_NULL;
+  if (misaligned(q) || misaligned(dst)) return MOE_E_ALIGN;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  ev_begin(st);
+  const cudaError_t e = moe::launch_ckpt_unpack(q, s, n, dst, st);
+  ev_end(st);
+  g_last_launches = 1;
+  return cuda_rc(e);
+}
+
+int moe_permute_checkpoint(const uint8_t* q, const uint8_t* s, const int32_t* row_of_pair,
+                           const int32_t* pair_of_row, int T, int k, int d, int M_cap,
+                           moe_bf16* dst, void* stream) {
+  g_last_launches = 0;
+  g_split_extra = 0;
+  if (T < 0 || k < 1 || d <= 0 || d % 64 || M_cap < 0) return MOE_E_SIZE;
+  if (static_cast<long long>(T) * k >= (1LL << 31)) return MOE_E_SIZE;
+  if (M_cap == 0) return MOE_OK;
+  if (!pair_of_row || !dst || (T > 0 && (!q || !s))) return MOE_E_NULL;
+  if (misaligned(q) || misaligned(dst)) return MOE_E_ALIGN;
+  const int sms = num_sms_current();
+  if (sms <= 0) return MOE_E_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  ev_begin(st);
+  const cudaError_t e = moe::launch_ckpt_gather(q, s, row_of_pair, pair_of_row, T, k, d, M_cap,
+                                                dst, sms, st);
+  ev_end(st);
+  g_last_launches = 1;
+  return cuda_rc(e);
+}
+
+int moe_grouped_mlp_fwd_ckpt(const moe_bf16* x_perm, const int32_t* offsets, int E, int M_cap,
+                             int d, int n, const moe_bf16* W1, const moe_bf16* W2, int act,
+                             uint8_t* h_q, uint8_t* h_s, moe_bf16* a, moe_bf16* y_perm,
+                             int32_t* err, void* stream) {
+  g_last_launches = 0;
+  g_split_extra = 0;
+  const int rc = check_mlp_sizes(E, M_cap, d, n);
+  if (rc) return rc;
+  if (act < MOE_ACT_SWIGLU || act > MOE_ACT_SRELU) return MOE_E_ARG;
+  if (!offsets || !W1 || !W2 || !err) return MOE_E_NULL;
+  if (M_cap == 0) return MOE_OK;
+  if (!x_perm || !h_q || !h_s || !a || !y_perm) return MOE_E_NULL;
+  if (misaligned(x_perm) || misaligned(W1) || misaligned(W2) || misaligned(h_q) ||
+      misaligned(h_s) || misaligned(a) || misaligned(y_perm))
+    return MOE_E_ALIGN;
+  const int n1 = (act == MOE_ACT_SRELU) ? n : 2 * n;
+  const int sms = num_sms_current();
+  if (sms <= 0) return MOE_E_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  CUtensorMap tx, tw1, ta, tw2, th, tao, ty;
+  if (!map_act(&tx, x_perm, M_cap, d, moe::kBM) || !map_w(&tw1, W1, E, d, n1, 64) ||
+      !map_act(&ta, a, M_cap, n, moe::kBM) || !map_w(&tw2, W2, E, n, d, 64) ||
+      !map_codes_out(&th, h_q, M_cap, n1) || !map_out2(&tao, a, M_cap, n) ||
+      !map_out2(&ty, y_perm, M_cap, d))
+    return MOE_E_CUDA;
+  moe::GemmArgs g1{};
+  g1.offsets = offsets; g1.E = E; g1.M_cap = M_cap; g1.K = d; g1.N = n1;
+  g1.out = a; g1.ldo = n; g1.ldo2 = n1; g1.err = err; g1.tma_out = 1;
+  g1.h_q = h_q; g1.h_s = h_s;
+  cudaError_t e = gemm(moe::GemmKind::kFc1Act, act, tx, tw1, th, g1, sms, s, &tao);
+  if (e != cudaSuccess) return MOE_E_CUDA;
+  moe::GemmArgs g2{};
+  g2.offsets = offsets; g2.E = E; g2.M_cap = M_cap; g2.K = n; g2.N = d;
+  g2.out = y_perm; g2.ldo = d; g2.err = err; g2.tma_out = 1;
+  e = gemm(moe::GemmKind::kFc2, 0, ta, tw2, ty, g2, sms, s);
+  if (e != cudaSuccess) return MOE_E_CUDA;
+  g_last_launches = 2 + g_split_extra;
+  return MOE_OK;
+}
+
+int moe_grouped_mlp_bwd_routed_ckpt(const moe_bf16* x_perm, const uint8_t* h_q, const uint8_t* h_s,
+                                    const moe_bf16* do_perm, const int32_t* pair_of_row,
+                                    const float* probs, const int32_t* offsets, int E, int M_cap,
+                                    int d, int n, const moe_bf16* W1, const moe_bf16* W2, int act,
+                                    int flags, moe_bf16* dh, moe_bf16* a_scaled, float* ds_part,
+                                    moe_bf16* dx_perm, moe_bf16* dW1, moe_bf16* dW2, int32_t* err,
+                                    void* stream) {
+  g_last_launches = 0;
+  g_split_extra = 0;
+  const int rc = check_mlp_sizes(E, M_cap, d, n);
+  if (rc) return rc;
+  if (act < MOE_ACT_SWIGLU || act > MOE_ACT_SRELU || (flags & ~MOE_FLAG_ACCUMULATE_DW))
+    return MOE_E_ARG;
+  const bool accumulate = flags & MOE_FLAG_ACCUMULATE_DW;
+  if (!offsets || !W1 || !W2 || !dW1 || !dW2 || !err) return MOE_E_NULL;
+  const int n1 = (act == MOE_ACT_SRELU) ? n : 2 * n;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (M_cap == 0) {
+    if (accumulate) return MOE_OK;
+    cudaError_t e = cudaMemsetAsync(dW1, 0, static_cast<size_t>(E) * d * n1 * 2, s);
+    if (e == cudaSuccess) e = cudaMemsetAsync(dW2, 0, static_cast<size_t>(E) * n * d * 2, s);
+    return cuda_rc(e);
+  }
+  if (!x_perm || !h_q || !h_s || !do_perm || !pair_of_row || !probs || !dh || !a_scaled ||
+      !ds_part || !dx_perm)
+    return MOE_E_NULL;
+  if (misaligned(x_perm) || misaligned(h_q) || misaligned(h_s) || misaligned(do_perm) ||
+      misaligned(dh) || misaligned(a_scaled) || misaligned(dx_perm) || misaligned(dW1) ||
+      misaligned(dW2) || misaligned(W1) || misaligned(W2))
+    return MOE_E_ALIGN;
+  const int sms = num_sms_current();
+  if (sms <= 0) return MOE_E_CUDA;
+  return bwd_gemms(x_perm, nullptr, a_scaled, do_perm, offsets, E, M_cap, d, n, W1, W2, act, dh,
+                   dx_perm, dW1, dW2, err, s, sms, pair_of_row, probs, a_scaled, ds_part, nullptr,
+                   accumulate, nullptr, nullptr, 0, 1, h_q, h_s);
 }
 
 }  // extern "C"

@@ -16,10 +16,12 @@ enum class GemmKind : int {
   kDgradAct = 2,  // A = dy_perm (K-major), B = W2^T (K-major, 3-D); dAct epilogue
   kDgrad = 3,     // A = dh (K-major),     B = W1^T (K-major, 3-D); store
   kWgrad = 4,     // A = act^T (M-major),  B = grad (N-major); ragged K
+  kLinearKN = 5,  // A = a (K-major),      B [E, K, N]; bias, act, residual epilogue
+  kLinearNK = 6,  // as kLinearKN with B stored [E, N, K]
 };
 
 struct GemmArgs {
-  const int32_t* offsets;  // [E+1] device
+  const int32_t* offsets;  // [E+1] device; NULL (E = 1): all M_cap rows
   int E;
   int M_cap;
   int K;                   // reduction length (ragged-row kinds)
@@ -84,6 +86,18 @@ struct GemmArgs {
   int gather_operand;
   const uint16_t* gather_src;
   long long gather_ld;
+  // H in 8 bits (E4M3 codes [M_cap, n1] and E8M0 scales [M_cap, n1 / 32], 32
+  // values of a row to a scale) in place of the bf16 H: kFc1Act writes h_q /
+  // h_s (tmC maps h_q: 64 columns x 32 rows, 64-byte swizzle), kDgradAct
+  // reads them
+  uint8_t* h_q;
+  uint8_t* h_s;
+  // kLinear*: out = act(a B + bias_e) + residual; out2 (optional) the
+  // pre-activation in bf16 (tmC with tma_out; tmD maps the bf16 out)
+  int act;                     // MOE_ACT_*
+  const uint16_t* bias;        // [E, N] bf16 or NULL
+  const uint16_t* residual;    // [M_cap, ldo] bf16 or NULL
+  float* out_f32;              // [M_cap, ldo]: float32 output in place of out
 };
 
 // Launches the persistent grouped GEMM of `kind` (act: MOE_ACT_*) on `s`.
@@ -105,6 +119,12 @@ cudaError_t launch_grouped_gemm(GemmKind kind, int act, const CUtensorMap& ta,
                                 const GemmArgs& args, int num_sms, cudaStream_t s,
                                 bool mx = false, const CUtensorMap* td = nullptr,
                                 int* launched = nullptr);
+
+// the kinds and variants that gemm_ext.cu instantiates (called by
+// launch_grouped_gemm with the unit order set)
+cudaError_t launch_gemm_ext(GemmKind kind, int act, const CUtensorMap& ta, const CUtensorMap& tb,
+                            const CUtensorMap& tc, const CUtensorMap& td, const GemmArgs& g,
+                            int num_sms, cudaStream_t s, bool pair);
 
 // Weight gradients use the skinny-expert configuration when the average
 // rows per expert (M_cap / E, known on the host without reading counts) is

@@ -1,0 +1,630 @@
+// linear.cu - the linear operator where it has few rows, and the elementwise
+// part of its backward.
+//
+// out_e = act(a_e B_e + bias_e) + residual.  With few rows per expert (a
+// token or a small batch in decoding, a router's gate) the product reads
+// every weight once for little arithmetic: it is bound by the weights' bytes
+// and by how many SMs stream them.  Tiles of 128 rows x 256 columns would
+// leave most SMs idle (a dense K x 4096 layer has 16) and load 128 rows of
+// `a` for one.  So the tile is turned: the weights are the MMA's M operand
+// (128 output columns x 64 of K, 16 KB) and TN = 16..128 tokens its N
+// operand, D[column, token] in TMEM; and `split` CTAs of a cluster share one
+// tile's reduction, each streaming its part of K into its own TMEM.  They
+// join through distributed shared memory: each CTA leaves its float32
+// partials in its own buffer, and token t's sum is formed by CTA t % split
+// in the order of the ranks, so reruns are bitwise identical and no
+// workspace, atomic or second launch is needed.
+//
+// Roles (192 threads): warp 0 TMA producer, warp 1 TMEM owner and MMA
+// issuer, warps 2-5 epilogue (a thread per output column).  Up to two CTAs
+// an SM keep one tile's loads running under another's epilogue.
+#include <cuda_runtime.h>
+
+#include "act.cuh"
+#include "linear.cuh"
+#include "ptx.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int FT = 192;               // threads
+constexpr int FM = 128;               // output columns per tile
+constexpr int FK = 64;                // reduction elements per stage
+constexpr int W_BYTES = FM * FK * 2;  // 16 KB
+constexpr int W_BOX = 64 * FK * 2;    // a 64 (columns) x 64 (K) box
+constexpr int MAX_SPLIT = 8;
+
+template <int TN>
+struct FC {
+  static constexpr int x_bytes = TN * FK * 2;
+  static constexpr int stage_bytes = W_BYTES + x_bytes;
+  static constexpr int red_bytes = TN * FM * 4;
+  // two CTAs an SM up to TN = 64, one at 128
+  static constexpr int stages = TN == 16 ? 5 : TN == 32 ? 4 : TN == 64 ? 3 : 4;
+  static constexpr int ctas = TN <= 64 ? 2 : 1;
+  static constexpr int tmem_cols = 2 * TN;   // two accumulators; a power of two >= 32
+  static constexpr size_t smem(int E) {
+    return 1024 + static_cast<size_t>(stages) * stage_bytes + red_bytes + (2 * stages + 7) * 8 +
+           16 + 2 * (E + 1) * 4;
+  }
+};
+
+struct FTile {
+  int e, row0, rows, n0;
+};
+
+// unit u -> tile: an expert's units run over its token tiles first, so that
+// consecutive units share their weights through L2
+template <int TN>
+__device__ __forceinline__ FTile few_tile(const FewArgs& g, const int* s_off, const int* s_ts,
+                                          int u) {
+  int lo = 0, hi = g.E - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (s_ts[mid + 1] <= u) lo = mid + 1;
+    else hi = mid;
+  }
+  const int rows = s_off[lo + 1] - s_off[lo];
+  const int tt = (rows + TN - 1) / TN;
+  const int local = u - s_ts[lo];
+  const int ni = local / tt;
+  const int ti = local - ni * tt;
+  FTile t;
+  t.e = lo;
+  t.row0 = s_off[lo] + ti * TN;
+  t.rows = min(TN, rows - ti * TN);
+  t.n0 = ni * FM;
+  return t;
+}
+
+// one output value: thread's column c of row `row`, z = the full sum
+template <bool GATED>
+__device__ __forceinline__ void few_out(const FewArgs& g, long long row, int c, float z,
+                                        float bias) {
+  z += bias;
+  const bool ok = c < g.N;
+  if (g.z != nullptr && ok)
+    g.z[row * g.N + c] = static_cast<uint16_t>(pack_bf16x2(z, 0.f) & 0xffffu);
+  int oc = c;
+  bool mine = ok;
+  float v;
+  if constexpr (GATED) {
+    const float up = __shfl_down_sync(0xffffffffu, z, 1);   // column c + 1
+    v = (g.act == MOE_ACT_SWIGLU ? gate_phi<MOE_ACT_SWIGLU>(z) : gate_phi<MOE_ACT_GEGLU>(z)) * up;
+    mine = ok && !(c & 1);
+    oc = c >> 1;
+  } else {
+    v = linear_act1(g.act, z);
+  }
+  if (!mine) return;
+  const long long at = row * g.ldo + oc;
+  if (g.residual != nullptr) v += __uint_as_float(static_cast<uint32_t>(g.residual[at]) << 16);
+  if (g.out_f32 != nullptr) g.out_f32[at] = v;
+  else g.out[at] = static_cast<uint16_t>(pack_bf16x2(v, 0.f) & 0xffffu);
+}
+
+template <bool KN, int TN, bool GATED>
+__global__ void __launch_bounds__(FT, FC<TN>::ctas)
+    few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+               const FewArgs g) {
+  using C = FC<TN>;
+  constexpr int NST = C::stages;
+  constexpr uint32_t IDESC = idesc_bf16(FM, TN, KN, false);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  float* red = reinterpret_cast<float*>(smem + NST * C::stage_bytes);   // [TN][FM]
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(red) + C::red_bytes);
+  uint64_t* empty_bar = full_bar + NST;
+  uint64_t* tfull_bar = empty_bar + NST;
+  uint64_t* tempty_bar = tfull_bar + 2;
+  uint64_t* rfull_bar = tempty_bar + 2;    // every CTA's partials are in its buffer
+  uint64_t* rempty_bar = rfull_bar + 1;    // every CTA has read this CTA's partials
+  uint64_t* drain_bar = rempty_bar + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* s_off = reinterpret_cast<int*>(tmem_slot + 4);
+  int* s_ts = s_off + (g.E + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int split = static_cast<int>(cluster_nctarank());
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int unit0 = blockIdx.x / split;
+  const int unit_step = gridDim.x / split;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NST; ++i) {
+      mbar_init(&full_bar[i], 1);
+      mbar_init(&empty_bar[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tfull_bar[i], 1);
+      mbar_init(&tempty_bar[i], 4);
+    }
+    mbar_init(rfull_bar, 4 * split);
+    mbar_init(rempty_bar, 4 * split);
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&tmW);
+    prefetch_tmap(&tmX);
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, C::tmem_cols);
+  if (warp == 2) {
+    // offsets made safe and the units' prefix, as in the grouped GEMM
+    bool bad = false;
+    for (int i = lane; i <= g.E; i += 32) {
+      const int v = g.offsets != nullptr ? g.offsets[i] : (i == 0 ? 0 : g.M_cap);
+      if (v < 0 || v > g.M_cap) bad = true;
+      s_off[i] = min(max(v, 0), g.M_cap);
+    }
+    __syncwarp();
+    if (lane == 0) {
+      int prev = 0;
+      for (int i = 0; i <= g.E; ++i) {
+        if (s_off[i] < prev) { bad = true; s_off[i] = prev; }
+        prev = s_off[i];
+      }
+      if (s_off[0] != 0) bad = true;
+    }
+    if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0) set_err(g.err, MOE_DEV_BAD_OFFSETS);
+    __syncwarp();
+    const int nt = (g.N + FM - 1) / FM;
+    int carry = 0;
+    for (int base = 0; base < g.E; base += 32) {
+      const int e = base + lane;
+      const int t = (e < g.E) ? (s_off[e + 1] - s_off[e] + TN - 1) / TN * nt : 0;
+      int v = t;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
+      }
+      if (e < g.E) s_ts[e] = carry + v - t;
+      carry += __shfl_sync(0xffffffffu, v, 31);
+    }
+    if (lane == 0) s_ts[g.E] = carry;
+  }
+  tc_fence_before();
+  // the peers' barriers are initialised before any CTA arrives on them
+  cluster_sync();
+  tc_fence_after();
+
+  const uint32_t tmem_base = *tmem_slot;
+  const int units = s_ts[g.E];
+  const int kblocks = g.K / FK;
+  const int kb0 = static_cast<int>(static_cast<long long>(kblocks) * rank / split);
+  const int kb1 = static_cast<int>(static_cast<long long>(kblocks) * (rank + 1) / split);
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool issued[NST];
+      uint32_t issued_parity[NST];
+      for (int i = 0; i < NST; ++i) { issued[i] = false; issued_parity[i] = 0; }
+      bool ok = true;
+      for (int u = unit0; u < units && ok; u += unit_step) {
+        const FTile t = few_tile<TN>(g, s_off, s_ts, u);
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!mbar_wait(&empty_bar[stage], phase ^ 1, abort_flag)) { ok = false; break; }
+          uint8_t* sw = smem + stage * C::stage_bytes;
+          uint64_t* fb = &full_bar[stage];
+          mbar_arrive_expect_tx(fb, C::stage_bytes);
+          if constexpr (KN) {
+            tma_load_3d(sw, &tmW, fb, t.n0, kb * FK, t.e);
+            tma_load_3d(sw + W_BOX, &tmW, fb, t.n0 + 64, kb * FK, t.e);
+          } else {
+            tma_load_3d(sw, &tmW, fb, kb * FK, t.n0, t.e);
+          }
+          tma_load_2d(sw + W_BYTES, &tmX, fb, kb * FK, t.row0);
+          issued[stage] = true;
+          issued_parity[stage] = phase;
+          if (++stage == NST) { stage = 0; phase ^= 1; }
+        }
+      }
+      if (!ok) {
+        // give up: wait (bounded) for the copies in flight
+        for (int i = 0; i < NST; ++i)
+          if (issued[i]) {
+            const uint32_t a = smem_u32(&full_bar[i]);
+            const uint64_t t0 = globaltimer_ns();
+            while (!mbar_try_wait(a, issued_parity[i]) && globaltimer_ns() - t0 < kWaitLimitNs) {}
+          }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int local = 0;
+      bool ok = true;
+      for (int u = unit0; u < units && ok; u += unit_step, ++local) {
+        const int buf = local & 1;
+        const uint32_t aph = (local >> 1) & 1;
+        if (!mbar_wait(&tempty_bar[buf], aph ^ 1, abort_flag)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t d = tmem_base + buf * TN;
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!mbar_wait(&full_bar[stage], phase, abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t w0 = smem_u32(smem + stage * C::stage_bytes);
+          const uint32_t x0 = w0 + W_BYTES;
+#pragma unroll
+          for (int kk = 0; kk < FK / 16; ++kk) {
+            const uint64_t wd = KN ? sdesc_sw128(w0 + kk * 2048, W_BOX, 1024)
+                                   : sdesc_sw128(w0 + kk * 32, 16, 1024);
+            const uint64_t xd = sdesc_sw128(x0 + kk * 32, 16, 1024);
+            umma_bf16(d, wd, xd, IDESC, (kb > kb0 || kk > 0) ? 1u : 0u);
+          }
+          umma_commit(&empty_bar[stage]);
+          if (++stage == NST) { stage = 0; phase ^= 1; }
+        }
+        if (ok) umma_commit(&tfull_bar[buf]);
+      }
+      if (!ok) {
+        // give up: the MMAs already issued finish before TMEM is freed
+        umma_commit(drain_bar);
+        const uint32_t a = smem_u32(drain_bar);
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(a, 0) && globaltimer_ns() - t0 < kWaitLimitNs) {}
+      }
+    }
+    __syncwarp();
+  } else {
+    const int q = warp & 3;                 // TMEM lane quadrant
+    const int n = q * 32 + lane;            // output column within the tile
+    int local = 0;
+    for (int u = unit0; u < units; u += unit_step, ++local) {
+      const FTile t = few_tile<TN>(g, s_off, s_ts, u);
+      const int buf = local & 1;
+      const uint32_t aph = (local >> 1) & 1;
+      const int c = t.n0 + n;
+      const float bias = (g.bias != nullptr && c < g.N)
+          ? __uint_as_float(static_cast<uint32_t>(g.bias[static_cast<long long>(t.e) * g.N + c]) << 16)
+          : 0.f;
+      bool ok = true;
+      if (lane == 0) {
+        ok = mbar_wait(&tfull_bar[buf], aph, abort_flag);
+        // the peers have read the previous unit's partials
+        if (ok && split > 1 && local > 0)
+          ok = mbar_wait_cluster(rempty_bar, (local - 1) & 1, abort_flag);
+      }
+      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+      tc_fence_after();
+      const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * TN;
+      // the accumulators, 16 tokens at a time
+      for (int t0 = 0; t0 < TN; t0 += 16) {
+        if (t0 >= t.rows) break;            // uniform: the rest are other rows
+        uint32_t r[16];
+        tmem_ld16(tb + t0, r);
+        tmem_wait_ld();
+        if (split > 1) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) red[(t0 + i) * FM + n] = __uint_as_float(r[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (t0 + i < t.rows)
+              few_out<GATED>(g, static_cast<long long>(t.row0) + t0 + i, c, __uint_as_float(r[i]), bias);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tempty_bar[buf]);
+      if (split > 1) {
+        // this warp's partials are written: tell every CTA of the cluster
+        if (lane < split) mbar_arrive_cluster(mapa_shared(smem_u32(rfull_bar), lane));
+        if (lane == 0) ok = mbar_wait_cluster(rfull_bar, local & 1, abort_flag);
+        if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+        // every lane reads the peers' buffers, so every lane acquires (the
+        // phase is complete and the next one needs this warp: no waiting)
+        while (!mbar_try_wait_cluster(smem_u32(rfull_bar), local & 1) && !*abort_flag) {}
+        for (int k = rank; k < t.rows; k += split) {
+          const uint32_t at = smem_u32(&red[k * FM + n]);
+          float z = 0.f;
+          for (int p = 0; p < split; ++p) z += ld_cluster_f32(mapa_shared(at, p));
+          few_out<GATED>(g, static_cast<long long>(t.row0) + k, c, z, bias);
+        }
+        __syncwarp();
+        if (lane < split) mbar_arrive_cluster(mapa_shared(smem_u32(rempty_bar), lane));
+      }
+    }
+  }
+
+  tc_fence_before();
+  // no CTA leaves while a peer may still read its partials or arrive on it
+  cluster_sync();
+  if (*abort_flag && threadIdx.x == 0) set_err(g.err, MOE_DEV_TIMEOUT);
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, C::tmem_cols);
+  }
+}
+
+constexpr int kMaxDevices = 64;
+
+template <bool KN, int TN, bool GATED>
+cudaError_t few_t(const CUtensorMap& tw, const CUtensorMap& tx, const FewArgs& g, int split,
+                  int num_sms, cudaStream_t s) {
+  auto kern = few_kernel<KN, TN, GATED>;
+  static_assert(FC<TN>::smem(MOE_MAX_EXPERTS) <= 227 * 1024, "shared memory of a CTA");
+  const size_t smem = FC<TN>::smem(g.E);
+  // clusters that fit at once with this shared memory, kept per device and
+  // split (it only sizes the grid: no cluster waits for another)
+  struct Fit {
+    size_t smem;
+    int clusters;
+  };
+  static Fit fit_of[kMaxDevices][4] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(FT);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = split;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  Fit& known = fit_of[dev][split == 1 ? 0 : split == 2 ? 1 : split == 4 ? 2 : 3];
+  int fit = known.clusters;
+  if (known.smem != smem) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(FC<TN>::smem(MOE_MAX_EXPERTS)));
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(num_sms / split * split);
+    cfg.dynamicSmemBytes = smem;
+    e = cudaOccupancyMaxActiveClusters(&fit, kern, &cfg);
+    if (e != cudaSuccess) return e;
+    if (fit < 1) fit = 1;
+    known = Fit{smem, fit};
+  }
+  const long long nt = (g.N + FM - 1) / FM;
+  const long long tiles = static_cast<long long>(g.M_cap) / TN + (g.E < g.M_cap ? g.E : g.M_cap);
+  const long long units = nt * (g.E == 1 ? (static_cast<long long>(g.M_cap) + TN - 1) / TN : tiles);
+  const long long clusters = units < fit ? units : fit;
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters * split));
+  cfg.dynamicSmemBytes = smem;
+  return cudaLaunchKernelEx(&cfg, kern, tw, tx, g);
+}
+
+template <bool KN, bool GATED>
+cudaError_t few_tn(const CUtensorMap& tw, const CUtensorMap& tx, const FewArgs& g,
+                   const FewPlan& p, int num_sms, cudaStream_t s) {
+  switch (p.tn) {
+    case 16: return few_t<KN, 16, GATED>(tw, tx, g, p.split, num_sms, s);
+    case 32: return few_t<KN, 32, GATED>(tw, tx, g, p.split, num_sms, s);
+    case 64: return few_t<KN, 64, GATED>(tw, tx, g, p.split, num_sms, s);
+    case 128: return few_t<KN, 128, GATED>(tw, tx, g, p.split, num_sms, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+// ------------------------------------------------------------- backward
+// dz = act'(z) dout and the bias gradient.  A block takes kDzRows rows of
+// one expert and 256 columns of dz; a thread 8 columns (one 16-byte load
+// of z) of every eighth row, its column sums in registers; the block adds
+// its eight row lanes in order and writes one partial row per (block of
+// rows, columns), which dbias_sum adds in order.
+constexpr int kDzRows = 128;
+constexpr int kDzThreads = 256;
+
+__device__ __forceinline__ int safe_off(const LinearDzArgs& g, int e) {
+  if (g.offsets == nullptr) return e == 0 ? 0 : g.M_cap;
+  return min(max(g.offsets[e], 0), g.M_cap);
+}
+
+// the row block `b` of the ragged rows: expert e and rows [r0, r1); experts
+// are walked by one warp, 32 at a time
+__device__ __forceinline__ bool dz_block(const LinearDzArgs& g, int b, int& e, int& r0, int& r1) {
+  const int lane = threadIdx.x & 31;
+  int carry = 0;
+  for (int base = 0; base < g.E; base += 32) {
+    const int x = base + lane;
+    const int lo = x < g.E ? safe_off(g, x) : 0;
+    const int hi = x < g.E ? max(safe_off(g, x + 1), lo) : 0;
+    // the grid's last block is past every row block, so it sees all experts
+    if (b == g.blocks - 1 && g.offsets != nullptr && x < g.E &&
+        (g.offsets[x] != lo || g.offsets[x + 1] != hi || (x == 0 && lo != 0)))
+      set_err(g.err, MOE_DEV_BAD_OFFSETS);
+    const int c = (hi - lo + kDzRows - 1) / kDzRows;
+    int incl = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const int first = carry + incl - c;
+    const bool hit = b >= first && b < first + c;
+    const unsigned m = __ballot_sync(0xffffffffu, hit);
+    if (m != 0) {
+      const int l = __ffs(m) - 1;
+      e = base + l;
+      r0 = __shfl_sync(0xffffffffu, lo + (b - first) * kDzRows, l);
+      r1 = min(r0 + kDzRows, __shfl_sync(0xffffffffu, hi, l));
+      return true;
+    }
+    carry += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return false;
+}
+
+// 8 dz values from 8 of z and 8 (gated: 4) of dout
+template <int ACT>
+__device__ __forceinline__ void dz8(const uint4& z, const uint32_t* d, float (&o)[8]) {
+  const uint32_t zw[4] = {z.x, z.y, z.z, z.w};
+  if constexpr (ACT == MOE_ACT_SWIGLU || ACT == MOE_ACT_GEGLU) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float gr = (i & 1) ? bf16_hi(d[i >> 1]) : bf16_lo(d[i >> 1]);
+      float p, dp;
+      gate_phi_dphi<ACT>(bf16_lo(zw[i]), p, dp);
+      o[2 * i] = gr * bf16_hi(zw[i]) * dp;
+      o[2 * i + 1] = gr * p;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      o[2 * i] = linear_dact<ACT>(bf16_lo(zw[i]), bf16_lo(d[i]));
+      o[2 * i + 1] = linear_dact<ACT>(bf16_hi(zw[i]), bf16_hi(d[i]));
+    }
+  }
+}
+
+template <int ACT>
+__global__ void __launch_bounds__(kDzThreads) dz_kernel(const LinearDzArgs g) {
+  constexpr bool GATED = (ACT == MOE_ACT_SWIGLU || ACT == MOE_ACT_GEGLU);
+  __shared__ int s_e, s_r0, s_r1, s_have;
+  __shared__ float s_sum[8][256];
+  if (threadIdx.x < 32) {
+    int e = 0, r0 = 0, r1 = 0;
+    const bool have = dz_block(g, blockIdx.x, e, r0, r1);
+    if (threadIdx.x == 0) { s_e = e; s_r0 = r0; s_r1 = r1; s_have = have; }
+  }
+  __syncthreads();
+  if (!s_have) return;
+  const int c8 = threadIdx.x & 31, rl = threadIdx.x >> 5;
+  const int col = blockIdx.y * 256 + c8 * 8;
+  float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (col < g.N) {
+    const int ldd = GATED ? g.N / 2 : g.N;
+    for (int r = s_r0 + rl; r < s_r1; r += 8) {
+      const long long row = r;
+      float o[8];
+      if constexpr (GATED) {
+        const uint2 d = *reinterpret_cast<const uint2*>(g.dout + row * ldd + col / 2);
+        const uint32_t dw[2] = {d.x, d.y};
+        dz8<ACT>(*reinterpret_cast<const uint4*>(g.z + row * g.N + col), dw, o);
+      } else {
+        const uint4 d = *reinterpret_cast<const uint4*>(g.dout + row * ldd + col);
+        const uint32_t dw[4] = {d.x, d.y, d.z, d.w};
+        const uint4 z = ACT == MOE_ACT_NONE ? d : *reinterpret_cast<const uint4*>(g.z + row * g.N + col);
+        dz8<ACT>(z, dw, o);
+      }
+      if (g.dz != nullptr)
+        *reinterpret_cast<uint4*>(g.dz + row * g.N + col) =
+            make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
+                       pack_bf16x2(o[6], o[7]));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] += o[i];
+    }
+  }
+  if (g.dbias == nullptr) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s_sum[rl][c8 * 8 + i] = sum[i];
+  __syncthreads();
+  const int c = blockIdx.y * 256 + threadIdx.x;
+  if (c < g.N) {
+    float t = s_sum[0][threadIdx.x];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) t += s_sum[i][threadIdx.x];
+    g.part[static_cast<long long>(blockIdx.x) * g.N + c] = t;
+  }
+}
+
+// dbias[e][c] (+)= the sum of e's row blocks, in order: 32 columns x 8 lanes
+// of blocks
+__global__ void __launch_bounds__(kDzThreads) dbias_sum(const LinearDzArgs g) {
+  __shared__ float s_sum[8][33];
+  __shared__ int s_b0, s_b1;
+  const int lane = threadIdx.x & 31, q = threadIdx.x >> 5;
+  const int e = blockIdx.y, c = blockIdx.x * 32 + lane;
+  if (q == 0) {
+    int n = 0, mine = 0;
+    for (int x = lane; x <= e; x += 32) {
+      const int lo = safe_off(g, x);
+      const int k = (max(safe_off(g, x + 1), lo) - lo + kDzRows - 1) / kDzRows;
+      if (x < e) n += k;
+      else mine = k;
+    }
+    n = __reduce_add_sync(0xffffffffu, n);
+    mine = __reduce_add_sync(0xffffffffu, mine);
+    if (lane == 0) { s_b0 = n; s_b1 = min(n + mine, g.blocks); }
+  }
+  __syncthreads();
+  float t = 0.f;
+  if (c < g.N)
+    for (int b = s_b0 + q; b < s_b1; b += 8) t += g.part[static_cast<long long>(b) * g.N + c];
+  s_sum[q][lane] = t;
+  __syncthreads();
+  if (q == 0 && c < g.N) {
+    t = s_sum[0][lane];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) t += s_sum[i][lane];
+    float* o = g.dbias + static_cast<long long>(e) * g.N + c;
+    *o = g.accumulate ? *o + t : t;
+  }
+}
+
+int dz_blocks_cap(int E, int M_cap) {
+  return M_cap / kDzRows + (E < M_cap ? E : M_cap) + 1;
+}
+
+}  // namespace
+
+FewPlan few_plan(int E, int M_cap, int K, int N, bool ragged, int num_sms) {
+  const long long active = ragged ? (E < M_cap ? E : M_cap) : 1;
+  const long long avg = (M_cap + active - 1) / active;
+  // 128 x 256 tiles of the grouped GEMM, when the rows are spread evenly
+  const long long big = (avg + 127) / 128 * active * ((N + 255) / 256);
+  if (avg > 64 && big >= num_sms) return FewPlan{0, 0};
+  FewPlan p;
+  const long long r = ragged ? 2 * avg : avg;
+  p.tn = r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128;
+  const long long slots = static_cast<long long>(num_sms) * (p.tn <= 64 ? 2 : 1);
+  const long long units = (avg + p.tn - 1) / p.tn * active * ((N + FM - 1) / FM);
+  p.split = 1;
+  while (p.split < MAX_SPLIT && units * p.split * 2 <= slots && K / FK >= 4 * p.split * 2)
+    p.split *= 2;
+  return p;
+}
+
+cudaError_t launch_few(const CUtensorMap& tw, const CUtensorMap& tx, bool kn, const FewArgs& g,
+                       const FewPlan& plan, int num_sms, cudaStream_t s) {
+  const bool gated = g.act == MOE_ACT_SWIGLU || g.act == MOE_ACT_GEGLU;
+  if (kn)
+    return gated ? few_tn<true, true>(tw, tx, g, plan, num_sms, s)
+                 : few_tn<true, false>(tw, tx, g, plan, num_sms, s);
+  return gated ? few_tn<false, true>(tw, tx, g, plan, num_sms, s)
+               : few_tn<false, false>(tw, tx, g, plan, num_sms, s);
+}
+
+size_t linear_dz_workspace_bytes(int E, int M_cap, int N) {
+  return static_cast<size_t>(dz_blocks_cap(E, M_cap)) * N * sizeof(float);
+}
+
+cudaError_t launch_linear_dz(const LinearDzArgs& in, cudaStream_t s, int* launches) {
+  *launches = 0;
+  LinearDzArgs g = in;
+  g.blocks = dz_blocks_cap(g.E, g.M_cap);
+  const dim3 grid(g.blocks, (g.N + 255) / 256);
+  if (g.M_cap > 0) {
+    switch (g.act) {
+      case MOE_ACT_SWIGLU: dz_kernel<MOE_ACT_SWIGLU><<<grid, kDzThreads, 0, s>>>(g); break;
+      case MOE_ACT_GEGLU: dz_kernel<MOE_ACT_GEGLU><<<grid, kDzThreads, 0, s>>>(g); break;
+      case MOE_ACT_SRELU: dz_kernel<MOE_ACT_SRELU><<<grid, kDzThreads, 0, s>>>(g); break;
+      case MOE_ACT_NONE: dz_kernel<MOE_ACT_NONE><<<grid, kDzThreads, 0, s>>>(g); break;
+      case MOE_ACT_RELU: dz_kernel<MOE_ACT_RELU><<<grid, kDzThreads, 0, s>>>(g); break;
+      case MOE_ACT_SILU: dz_kernel<MOE_ACT_SILU><<<grid, kDzThreads, 0, s>>>(g); break;
+      case MOE_ACT_GELU: dz_kernel<MOE_ACT_GELU><<<grid, kDzThreads, 0, s>>>(g); break;
+      default: return cudaErrorInvalidValue;
+    }
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    ++*launches;
+  }
+  if (g.dbias != nullptr) {
+    dbias_sum<<<dim3((g.N + 31) / 32, g.E), kDzThreads, 0, s>>>(g);
+    ++*launches;
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace moe

@@ -13,7 +13,11 @@
 // one chunk into 4 TMEM columns of every lane quadrant.
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include <cstdint>
+
+#include "ptx.cuh"
 
 namespace moe {
 
@@ -35,6 +39,27 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+// 2^(code - 127) for a scale byte (0: 2^-127)
+__device__ __forceinline__ float mx_scale(uint32_t code) {
+  return __uint_as_float(code != 0u ? code << 23 : 0x00400000u);
+}
+
+// 8 codes (two words) times the block's scale -> 4 words of bf16 pairs.  An
+// E4M3 value has 4 significant bits, so the product is exact in bf16 (down
+// to bf16's subnormals).
+__device__ __forceinline__ void mx_decode8(uint32_t lo, uint32_t hi, float scale,
+                                           uint32_t (&out)[4]) {
+  const uint32_t w[2] = {lo, hi};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint16_t c = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
+    const float2 f = __half22float2(*reinterpret_cast<__half2*>(&h));
+    out[i] = pack_bf16x2(f.x * scale, f.y * scale);
+  }
 }
 
 // 32 values (already bf16-representable) -> 32 codes in 8 words, scale code

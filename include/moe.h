@@ -66,6 +66,15 @@ typedef uint16_t moe_bf16;
 #define MOE_ACT_SWIGLU 0       /* A_j = silu(H_2j) * H_2j+1                    */
 #define MOE_ACT_GEGLU 1        /* A_j = gelu_tanh(H_2j) * H_2j+1               */
 #define MOE_ACT_SRELU 2        /* A_j = max(H_j, 0)^2  (not gated)             */
+/* further ones of moe_grouped_linear (not gated, elementwise) */
+#define MOE_ACT_NONE 3         /* z                                            */
+#define MOE_ACT_RELU 4         /* max(z, 0)                                    */
+#define MOE_ACT_SILU 5         /* z sigmoid(z)                                 */
+#define MOE_ACT_GELU 6         /* gelu_tanh(z)                                 */
+
+/* element types of the operators that take more than one */
+#define MOE_TYPE_F32 0
+#define MOE_TYPE_BF16 1
 
 /* flags */
 #define MOE_FLAG_SAVE_H 1      /* forward also stores H (needed by backward)   */
@@ -685,6 +694,163 @@ int moe_mx_quantize(const moe_bf16* src, int rows, int cols,
 int moe_mx_quantize_tiled(const moe_bf16* src, int rows, int cols,
                           const int32_t* offsets, int E, uint8_t* q, uint8_t* s,
                           uint8_t* qT, uint8_t* sT, int32_t* err, void* stream);
+
+/*
+ * moe_router_loss - the router's load-balance and z losses with the
+ * per-expert counts behind them ([TE] "용량 기반 MoE와 드롭리스 MoE": without a
+ * capacity nothing but training keeps the experts' loads even; the losses
+ * themselves are the common ones, the pages do not fix them).
+ *   logits      [T, E] float32 or bf16 (logits_type MOE_TYPE_*)
+ *   topk_idx    [T, k] int32, as moe_router_topk writes it (-1: no route;
+ *               other ids outside [0, E) are skipped and set
+ *               MOE_DEV_BAD_EXPERT)
+ *   seg_offsets [S+1] int32 (device): sequence s is tokens
+ *               [seg_offsets[s], seg_offsets[s+1]); starts at 0,
+ *               non-decreasing, at most T (else corrected, and
+ *               MOE_DEV_BAD_OFFSETS).  NULL with S = 1: one sequence of all T.
+ *   token_mask  [T] uint8 or NULL: 0 takes the token out.
+ * A token is valid if it lies in a sequence, is not masked and has a logit
+ * above the lowest finite value of its type (a row that -inf or that value
+ * masks throughout is empty: its lse is -inf).  With P_t = softmax of all E
+ * logits, lse_t their log-sum-exp,
+ * c_se the pairs of s's valid tokens that chose e, N_s its valid tokens and
+ * N their sum:
+ *   loss[0] = E / (k N) sum_s 1 / N_s sum_e c_se sum_{t in s} P_te
+ *             (1 when every sequence is balanced)
+ *   loss[1] = 1 / N sum_t lse_t^2
+ * (both 0 if N = 0), and counts [S, E], n_valid [S], lse [T] (every token's)
+ * for the backward.  Sums in float32, in an order that the sizes and
+ * seg_offsets alone fix: reruns are bitwise identical.  NaN logits of a
+ * valid token reach the losses.
+ *   workspace: moe_router_loss_workspace_size(T, E, S) bytes, 16-byte
+ *   aligned, not initialised.  1 <= S <= 4096.  Two launches.
+ */
+size_t moe_router_loss_workspace_size(int T, int E, int S);
+int moe_router_loss(const void* logits, int logits_type, const int32_t* topk_idx, int T, int E,
+                    int k, const int32_t* seg_offsets, int S, const uint8_t* token_mask,
+                    float* loss, int32_t* counts, float* lse, int32_t* n_valid, void* workspace,
+                    size_t ws_bytes, int32_t* err, void* stream);
+
+/*
+ * moe_router_loss_bwd - gradient of the logits: of dloss[0] loss[0] +
+ * dloss[1] loss[1] (the counts are constants), plus, if probs and dprobs are
+ * given, of the router's own softmax over the k selected logits
+ * ([Sonic] "역전파 계산 그래프 재작성하기": dS is what the experts' backward
+ * hands to the router).  With w_se = dloss[0] E c_se / (k N N_s):
+ *   dlogits_te = P_te (w_se - sum_e' P_te' w_se' + 2 dloss[1] lse_t / N)
+ *                                                 (valid tokens; else 0)
+ *              + sum_{j: idx_tj = e} p_tj (dp_tj - sum_i p_ti dp_ti)
+ * (the second line for every token; pairs without a valid id are left out
+ * of both of its sums).  An expert chosen twice by a token gets both terms.
+ *   lse, counts, n_valid: as moe_router_loss wrote them; dloss [2] float32
+ *   (device); probs, dprobs [T, k] float32 or both NULL; dlogits [T, E]
+ *   float32 or bf16.  One launch.
+ */
+int moe_router_loss_bwd(const void* logits, int logits_type, const int32_t* topk_idx, int T, int E,
+                        int k, const int32_t* seg_offsets, int S, const uint8_t* token_mask,
+                        const float* lse, const int32_t* counts, const int32_t* n_valid,
+                        const float* dloss, const float* probs, const float* dprobs,
+                        void* dlogits, int dlogits_type, void* stream);
+
+/*
+ * moe_grouped_linear - a product with bias, activation and residual in its
+ * epilogue, over the experts' ragged rows or dense (E = 1): the router's
+ * gate, a shared expert, experts with biases ([TE] "최적화 1: grouped GEMM";
+ * [CuTe] "핵심 아이디어 / 구조 / 동작 방식": work on the output belongs in the
+ * GEMM's epilogue).  For the rows of each expert:
+ *   z = a B_e + bias_e          (float32)
+ *   out = act(z) + residual     (float32, rounded once)
+ *   a [M_cap, K] bf16; offsets [E+1] as moe_grouped_gemm, or NULL with E = 1:
+ *   all M_cap rows; B as moe_grouped_gemm (b_layout MOE_B_*); bias [E, N]
+ *   bf16 or NULL; act any MOE_ACT_* (SWIGLU, GEGLU: columns 2j = gate,
+ *   2j+1 = up, n_out = N / 2; the others: n_out = N); residual [M_cap, n_out]
+ *   bf16 or NULL, may be `out` itself; z [M_cap, N] bf16 or NULL: the
+ *   pre-activation, for the backward; out [M_cap, n_out], bf16 or float32
+ *   (out_type).  Rows outside every expert are not written.  K, N multiples
+ *   of 64; pointers 16-byte aligned.
+ * Few rows (decoding: a token, or a few per expert; a gate's few columns)
+ * run a kernel of their own that splits the reduction over a cluster of
+ * CTAs; reruns are bitwise identical.  One launch (two where automatic pair
+ * mode splits a skinny layer, moe_set_pair_mma).
+ */
+int moe_grouped_linear(const moe_bf16* a, const int32_t* offsets, int E, int M_cap, int K, int N,
+                       const moe_bf16* B, int b_layout, const moe_bf16* bias, int act,
+                       const moe_bf16* residual, moe_bf16* z, void* out, int out_type,
+                       int32_t* err, void* stream);
+
+/*
+ * moe_grouped_linear_bwd - its backward ([CuTe] kernel family "GroupGemm +
+ * dActivation").
+ *   dz = act'(z) dout           (bf16; act NONE: dout itself, dz unused)
+ *   da = dz B_e^T               bf16 [M_cap, K], or NULL: not wanted
+ *   dB_e = a_e^T dz_e           bf16 in B's layout (zero for experts with no
+ *                               rows), or NULL
+ *   dbias_e = sum of e's rows   float32 [E, N], from dz before its rounding,
+ *                               added in an order fixed by the offsets; or NULL
+ * The residual's gradient is dout.  z (as moe_grouped_linear stored it) and
+ * dz [M_cap, N] may be NULL for act NONE.  relu's derivative at 0 is 0.
+ * flags: 0 or MOE_FLAG_ACCUMULATE_DW (dB and dbias += theirs; experts with
+ * no rows untouched).  workspace: moe_grouped_linear_bwd_workspace_size bytes,
+ * 16-byte aligned, needed with dbias only.  Up to four launches, and one
+ * more for each GEMM that automatic pair mode splits.
+ */
+size_t moe_grouped_linear_bwd_workspace_size(int E, int M_cap, int N);
+int moe_grouped_linear_bwd(const moe_bf16* dout, const moe_bf16* z, const moe_bf16* a,
+                           const int32_t* offsets, int E, int M_cap, int K, int N,
+                           const moe_bf16* B, int b_layout, int act, int flags, moe_bf16* dz,
+                           moe_bf16* da, moe_bf16* dB, float* dbias, void* workspace,
+                           size_t ws_bytes, int32_t* err, void* stream);
+
+/*
+ * Activation checkpoints in 8 bits: what the backward needs of the forward
+ * (the layer's input rows and H), kept as E4M3 codes with one E8M0 scale per
+ * 32 consecutive values of a row (the block rule above), 1.03 bytes a value
+ * against bf16's 2 ([Sonic] "역전파 계산 그래프 재작성하기": the activations that
+ * the backward keeps are what limits the layer).  An E4M3 value times a power
+ * of two is exact in bf16, so reading a checkpoint back loses nothing more.
+ * A value's error is at most 2^-4 of it (half a code step; below 2^-6 scale
+ * units 2^-10 units), and 2^-3 where it lies above 448 scale units and
+ * saturates.  NaN stays NaN; an infinity comes back as one, and the other
+ * finite values of its block as 0 or what is left of them at that scale.
+ *
+ * moe_checkpoint_pack   src [rows, cols] bf16 -> q [rows, cols] codes and
+ *                       s [rows, cols / 32] scales
+ * moe_checkpoint_unpack the bf16 values they stand for
+ * moe_permute_checkpoint moe_permute's / moe_permute_tokens' expert-major
+ *                       gather from the packed rows [T, d] into bf16 dst
+ *                       [M_cap, d]; with row_of_pair (may be NULL) each
+ *                       packed row is read once, in token order
+ * cols, d multiples of 64; q, src, dst 16-byte aligned.  One launch each.
+ */
+int moe_checkpoint_pack(const moe_bf16* src, int rows, int cols, uint8_t* q, uint8_t* s,
+                        void* stream);
+int moe_checkpoint_unpack(const uint8_t* q, const uint8_t* s, int rows, int cols, moe_bf16* dst,
+                          void* stream);
+int moe_permute_checkpoint(const uint8_t* q, const uint8_t* s, const int32_t* row_of_pair,
+                           const int32_t* pair_of_row, int T, int k, int d, int M_cap,
+                           moe_bf16* dst, void* stream);
+
+/*
+ * moe_grouped_mlp_fwd_ckpt - moe_grouped_mlp_fwd with H kept in 8 bits: FC1's
+ * epilogue quantises its float32 accumulators (one rounding) into h_q
+ * [M_cap, n1] and h_s [M_cap, n1 / 32]; A (from the unrounded H) and Y are
+ * moe_grouped_mlp_fwd's bit for bit.  No bf16 H exists.
+ * moe_grouped_mlp_bwd_routed_ckpt - moe_grouped_mlp_bwd_routed from that
+ * checkpoint: FC2-dgrad's epilogue reads h_q / h_s, and every result equals
+ * moe_grouped_mlp_bwd_routed's on the unpacked H bit for bit.
+ * Arguments, sizes and errors as there; all pointers 16-byte aligned.
+ */
+int moe_grouped_mlp_fwd_ckpt(const moe_bf16* x_perm, const int32_t* offsets, int E, int M_cap,
+                             int d, int n, const moe_bf16* W1, const moe_bf16* W2, int act,
+                             uint8_t* h_q, uint8_t* h_s, moe_bf16* a, moe_bf16* y_perm,
+                             int32_t* err, void* stream);
+int moe_grouped_mlp_bwd_routed_ckpt(const moe_bf16* x_perm, const uint8_t* h_q, const uint8_t* h_s,
+                                    const moe_bf16* do_perm, const int32_t* pair_of_row,
+                                    const float* probs, const int32_t* offsets, int E, int M_cap,
+                                    int d, int n, const moe_bf16* W1, const moe_bf16* W2, int act,
+                                    int flags, moe_bf16* dh, moe_bf16* a_scaled, float* ds_part,
+                                    moe_bf16* dx_perm, moe_bf16* dW1, moe_bf16* dW2, int32_t* err,
+                                    void* stream);
 
 /*
  * Measurement hook (per host thread; no counterpart on the pages).

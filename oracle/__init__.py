@@ -22,3 +22,4 @@ the pages' worked examples (``tests/golden/``).
 """
 from .moe import *  # noqa: F401,F403
 from .mx import *  # noqa: F401,F403
+from .ops import *  # noqa: F401,F403
