@@ -13,15 +13,16 @@
 // moe_router_topk writes.
 //
 // Forward, two kernels.  loss_rows: a block takes one unit, up to `chunk`
-// consecutive tokens of one segment, a warp per token; each lane keeps the
-// sums of P of its experts in registers over the warp's tokens, the block
-// adds its warps' sums in warp order and writes one partial row per unit, so
-// that no order depends on timing.  loss_finish: adds the units of each
-// segment in order (32 experts x 32 unit lanes per block); the block that
-// finishes last adds the blocks' terms in order.  Backward: one kernel, a
-// warp per token, which reads each logit once and writes its gradient.
-// All three are bound by HBM on long batches and by launch latency on short
-// ones.
+// consecutive tokens of one segment.  A group of L lanes (4 to 32, so that
+// each holds about 8 logits) takes a token, the next token's row loading
+// meanwhile, and keeps the sums of P of its experts in registers over its
+// tokens; the block adds its groups' sums in a fixed order and writes one
+// partial row per unit, so that no order depends on timing.  loss_finish,
+// launched programmatically behind it: adds the units of each segment in
+// order (a block per segment and slice of experts); the block that finishes last
+// adds the blocks' terms in order.  Backward: one kernel, a group of lanes
+// per token, which reads each logit once and writes its gradient.
+// All are bound by HBM on long batches and by launch latency on short ones.
 #include <cuda_bf16.h>
 
 #include "loss.cuh"
@@ -30,9 +31,7 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kFinishThreads = 1024;
+constexpr int kBwdThreads = 256;
 
 struct Ws {
   float* psum;     // [units, E] sums of P
@@ -40,23 +39,29 @@ struct Ws {
   float* pz;       // [units] sums of lse^2
   int32_t* pn;     // [units] valid tokens
   float* term;     // [S, slices] sum_e c S / N_s of a slice of experts
+  float* zseg;     // [S] sums of lse^2
   int32_t* ticket;
 };
 
-// Tokens per unit: whole rounds of the block's warps, about two units for
-// each of a GB300's 152 SMs (a constant, so that the workspace size and the
-// order of the sums do not depend on the device queried).
-constexpr int kUnits = 304;
+// Tokens per unit: about one unit (a block of 16 warps) for each of the 456
+// places that 152 SMs have at three blocks each, a few left for segments that
+// end inside a unit (a constant, so that the workspace size and the order of
+// the sums do not depend on the device queried).  65,536 tokens x 256 experts
+// in 16 sequences, forward as a whole: 26.2 us, against 28.9 with 608 units,
+// 31.5 with 1780 of 8 warps.
+constexpr int kUnits = 440;
 int chunk_of(int T) {
   const int per = (T + kUnits - 1) / kUnits;
-  const int c = (per + kWarps - 1) / kWarps * kWarps;
-  return c < kWarps ? kWarps : c;
+  const int c = (per + 15) / 16 * 16;
+  return c < 16 ? 16 : c;
 }
 int units_cap(int T, int S) {
   const int c = chunk_of(T);
   return (T + c - 1) / c + S + 1;
 }
-int slices_of(int E) { return (E + 31) / 32; }
+// experts per block of loss_finish
+int finish_experts(int S) { return S < 4 ? 8 : 32; }
+int slices_of(int E, int S) { return (E + finish_experts(S) - 1) / finish_experts(S); }
 
 size_t up16(size_t b) { return (b + 15) & ~static_cast<size_t>(15); }
 
@@ -74,7 +79,8 @@ Ws carve(void* base, int T, int E, int S, size_t* bytes) {
   w.pcnt = reinterpret_cast<int32_t*>(take(U * E * 4));
   w.pz = reinterpret_cast<float*>(take(U * 4));
   w.pn = reinterpret_cast<int32_t*>(take(U * 4));
-  w.term = reinterpret_cast<float*>(take(static_cast<size_t>(S) * slices_of(E) * 4));
+  w.term = reinterpret_cast<float*>(take(static_cast<size_t>(S) * slices_of(E, S) * 4));
+  w.zseg = reinterpret_cast<float*>(take(static_cast<size_t>(S) * 4));
   w.ticket = reinterpret_cast<int32_t*>(take(4));
   *bytes = at;
   return w;
@@ -151,33 +157,41 @@ __device__ __forceinline__ float warp_sum(float v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-__device__ __forceinline__ float warp_max(float v) {
+// sums and maxima over the L lanes of a group
+template <int L>
+__device__ __forceinline__ float group_sum(float v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+template <int L>
+__device__ __forceinline__ float group_max(float v) {
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
 }
 
 // A lane's logits of one row: NV values in groups of VEC consecutive ones;
-// value i is expert (lane + 32 (i / VEC)) * VEC + i % VEC.  Missing ones are
-// -inf.
-template <int VEC>
-__device__ __forceinline__ int expert_of(int lane, int i) {
-  return (lane + 32 * (i / VEC)) * VEC + i % VEC;
+// value i of lane l of its group is expert (l + L (i / VEC)) * VEC + i % VEC.
+// Missing ones are -inf.
+template <int VEC, int L>
+__device__ __forceinline__ int expert_of(int l, int i) {
+  return (l + L * (i / VEC)) * VEC + i % VEC;
 }
-template <class T, int VEC, int NV>
-__device__ __forceinline__ void load_row(const T* __restrict__ row, int E, int lane,
+template <class T, int VEC, int NV, int L>
+__device__ __forceinline__ void load_row(const T* __restrict__ row, int E, int l, bool ok,
                                          float (&v)[NV]) {
 #pragma unroll
   for (int g = 0; g < NV / VEC; ++g) {
-    const int e0 = (lane + 32 * g) * VEC;
+    const int e0 = (l + L * g) * VEC;
     if constexpr (VEC == 1) {
       v[g] = -INFINITY;
-      if (e0 < E) {
-        if constexpr (sizeof(T) == 4) v[g] = row[e0];
-        else v[g] = __uint_as_float(static_cast<uint32_t>(row[e0]) << 16);
+      if (ok && e0 < E) {
+        if constexpr (sizeof(T) == 4) v[g] = __ldcs(row + e0);
+        else v[g] = __uint_as_float(static_cast<uint32_t>(__ldcs(row + e0)) << 16);
       }
-    } else if (e0 < E) {   // E is a multiple of VEC here
-      const uint4 w = *reinterpret_cast<const uint4*>(row + e0);
+    } else if (ok && e0 < E) {   // E is a multiple of VEC here
+      const uint4 w = __ldcs(reinterpret_cast<const uint4*>(row + e0));
       const uint32_t u[4] = {w.x, w.y, w.z, w.w};
       if constexpr (sizeof(T) == 4) {
 #pragma unroll
@@ -196,24 +210,34 @@ __device__ __forceinline__ void load_row(const T* __restrict__ row, int E, int l
   }
 }
 
-// the lowest finite value of the logits' type
-template <class T>
-__device__ __forceinline__ float lowest() {
-  return __uint_as_float(sizeof(T) == 4 ? 0xFF7FFFFFu : 0xFF7F0000u);
+// The softmax in base 2: e^(z - m) = 2^(z log2 e - m2) with m2 = m log2 e,
+// one fused multiply-add and one exponential per logit, and
+// lse = (m2 + log2 sum) ln 2, in which m2's rounding cancels.
+constexpr float kLog2E = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+__device__ __forceinline__ float exp2_(float x) {
+  float y;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-template <class T, int VEC, int NV>
-__global__ void __launch_bounds__(kThreads) loss_rows(const RouterLossArgs a, const Ws w,
-                                                      int chunk) {
-  extern __shared__ float sm[];             // [kWarps][E] sums, then [E] counts
-  int32_t* hist = reinterpret_cast<int32_t*>(sm + kWarps * a.E);
+// Nothing at or below bf16's lowest finite value counts as a logit (float32's
+// lowest is below it): masks use either, on rows of either type.
+constexpr float kLowest = -3.3895313892515355e38f;
+
+template <class T, int VEC, int NV, int L, int W>
+__global__ void __launch_bounds__(32 * W, NV <= 8 ? 3 : 1) loss_rows(const RouterLossArgs a, const Ws w, int chunk) {
+  constexpr int G = 32 / L;                 // tokens of a warp at a time
+  extern __shared__ float sm[];             // [W][E] sums, then [E] counts
+  int32_t* hist = reinterpret_cast<int32_t*>(sm + W * a.E);
   __shared__ Span s_span;
   __shared__ int s_have;
-  __shared__ float s_z[kWarps];
-  __shared__ int s_n[kWarps];
+  __shared__ float s_z[W];
+  __shared__ int s_n[W];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int l = lane % L, grp = lane / L;
   if (blockIdx.x == 0 && threadIdx.x == 0) *w.ticket = 0;
-  for (int e = threadIdx.x; e < a.E; e += kThreads) hist[e] = 0;
+  for (int e = threadIdx.x; e < a.E; e += 32 * W) hist[e] = 0;
   if (warp == 0) {
     Span sp{0, 0, 0, 0};
     bool bad = false;
@@ -241,62 +265,91 @@ __global__ void __launch_bounds__(kThreads) loss_rows(const RouterLossArgs a, co
   int nval = 0;
   bool bad_id = false;
   const T* logits = static_cast<const T*>(a.logits);
-  for (int t = t0 + warp; t < t1; t += kWarps) {
+  // a round is G tokens of each warp.  Loads are not staged ahead: with 48
+  // warps an SM, one warp's wait is covered by the others' arithmetic
+  for (int tw = t0 + warp * G; tw < t1; tw += W * G) {
+    const int t = tw + grp;
+    const bool have = t < t1;
     float v[NV];
-    load_row<T, VEC, NV>(logits + static_cast<long long>(t) * a.E, a.E, lane, v);
+    load_row<T, VEC, NV, L>(logits + static_cast<long long>(t) * a.E, a.E, l, have, v);
+    const long long p0 = static_cast<long long>(t) * a.k;
+    int e0 = -1;
+    if (have && l < a.k) e0 = a.idx[p0 + l];
+    bool on = have && seg_ok;
+    if (on && a.mask != nullptr) on = a.mask[t] != 0;
     float m = v[0];
 #pragma unroll
     for (int i = 1; i < NV; ++i) m = fmaxf(m, v[i]);
-    m = warp_max(m);
+    m = group_max<L>(m);
+    // a row that a mask of -inf or of a type's lowest value has emptied
+    // has no weight at all (its lse^2 would overflow): with m = 0 every term
+    // is 0 and lse = log 0; NaN goes through
+    if (m <= kLowest) m = 0.f;
+    const float m2 = m * kLog2E;
     float tot = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      v[i] = (v[i] == -INFINITY) ? 0.f : expf(v[i] - m);
+      v[i] = exp2_(fmaf(v[i], kLog2E, -m2));
       tot += v[i];
     }
-    tot = warp_sum(tot);
-    // a row that a mask of -inf or of the type's lowest value has emptied
-    // has no weight at all (its lse^2 would overflow); NaN goes through
-    const float lse = (m <= lowest<T>() && tot == tot) ? -INFINITY : m + logf(tot);
-    if (lane == 0) a.lse[t] = lse;
-    const bool valid = seg_ok && (a.mask == nullptr || a.mask[t] != 0) && !(lse == -INFINITY);
-    if (valid) {
-      const float inv = 1.0f / tot;
+    tot = group_sum<L>(tot);
+    const float lse = (m2 + log2f(tot)) * kLn2;
+    if (have && l == 0) a.lse[t] = lse;
+    if (on && !(lse == -INFINITY)) {
+      const float inv = __fdividef(1.0f, tot);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) acc[i] += v[i] * inv;
-      zsum += lse * lse;
-      ++nval;
-      for (int j = lane; j < a.k; j += 32) {
-        const int e = a.idx[static_cast<long long>(t) * a.k + j];
+      for (int i = 0; i < NV; ++i) acc[i] = fmaf(v[i], inv, acc[i]);
+      if (l == 0) {
+        zsum = fmaf(lse, lse, zsum);
+        ++nval;
+      }
+      if (e0 >= 0 && e0 < a.E) atomicAdd(&hist[e0], 1);
+      else if (e0 != -1) bad_id = true;
+      for (int j = l + L; j < a.k; j += L) {
+        const int e = a.idx[p0 + j];
         if (e >= 0 && e < a.E) atomicAdd(&hist[e], 1);
         else if (e != -1) bad_id = true;
       }
     }
   }
+  // loss_finish may come in once every block is here (it waits for this grid
+  // to end; earlier its blocks would take the place of this grid's)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (__any_sync(0xffffffffu, bad_id) && lane == 0) set_err(a.err, MOE_DEV_BAD_EXPERT);
   if (!seg_ok) return;    // the tail's tokens count nowhere
+  // the warp's groups, by a tree
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = expert_of<VEC>(lane, i);
-    if (e < a.E) sm[warp * a.E + e] = acc[i];
+  for (int o = L; o < 32; o <<= 1) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+    zsum += __shfl_xor_sync(0xffffffffu, zsum, o);
+    nval += __shfl_xor_sync(0xffffffffu, nval, o);
   }
-  if (lane == 0) {
-    s_z[warp] = zsum;
-    s_n[warp] = nval;
+  if (grp == 0) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int e = expert_of<VEC, L>(l, i);
+      if (e < a.E) sm[warp * a.E + e] = acc[i];
+    }
+    if (l == 0) {
+      s_z[warp] = zsum;
+      s_n[warp] = nval;
+    }
   }
   __syncthreads();
   const long long row = static_cast<long long>(blockIdx.x) * a.E;
-  for (int e = threadIdx.x; e < a.E; e += kThreads) {
+  for (int e = threadIdx.x; e < a.E; e += 32 * W) {
     float x = sm[e];
 #pragma unroll
-    for (int q = 1; q < kWarps; ++q) x += sm[q * a.E + e];
+    for (int q = 1; q < W; ++q) x += sm[q * a.E + e];
     w.psum[row + e] = x;
     w.pcnt[row + e] = hist[e];
   }
   if (threadIdx.x == 0) {
     float z = 0.f;
     int n = 0;
-    for (int q = 0; q < kWarps; ++q) {
+#pragma unroll
+    for (int q = 0; q < W; ++q) {
       z += s_z[q];
       n += s_n[q];
     }
@@ -305,57 +358,92 @@ __global__ void __launch_bounds__(kThreads) loss_rows(const RouterLossArgs a, co
   }
 }
 
-// block (slice, segment): 32 experts x 32 unit lanes
-__global__ void __launch_bounds__(kFinishThreads) loss_finish(const RouterLossArgs a, const Ws w,
-                                                              int chunk) {
+// block (slice of EB experts, segment), blockDim / EB unit lanes: EB = 8 with
+// 1024 threads where a segment has many units, 32 with 256 threads where
+// there are many segments (a 1024-thread block for each of 16 segments took
+// 21 us, as long as loss_rows)
+template <int EB, int TH>
+__global__ void __launch_bounds__(TH) loss_finish(const RouterLossArgs a, const Ws w, int chunk) {
+  constexpr int LANES = TH / EB;      // unit lanes
+  constexpr int NW = TH / 32;
   __shared__ Span s_span;
-  __shared__ float s_sum[32][33];
-  __shared__ int s_cnt[32][33];
-  __shared__ int s_last, s_nseg;
-  const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
+  __shared__ float s_sum[NW][EB];
+  __shared__ int s_cnt[NW][EB];
+  __shared__ float s_red[2][NW];
+  __shared__ int s_num[NW];
+  __shared__ int s_last;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int xe = threadIdx.x % EB, ul = threadIdx.x / EB;
   const int s = blockIdx.y;
-  const int e = blockIdx.x * 32 + lane;
-  if (grp == 0) {
+  const int e = blockIdx.x * EB + xe;
+  if (warp == 0) {     // the segment's place, from the caller's offsets alone
     Span sp{0, 0, 0, 0};
     bool bad = false;
     walk_segments(a.seg, a.S, a.T, chunk, bad, sp, [&](const Span& x, int) { return x.s == s; });
-    const int n_units = (sp.hi - sp.lo + chunk - 1) / chunk;
-    int n = 0;
-    for (int u = lane; u < n_units; u += 32) n += w.pn[sp.unit0 + u];
-    n = __reduce_add_sync(0xffffffffu, n);
-    if (lane == 0) {
-      s_span = sp;
-      s_nseg = n;
-      if (blockIdx.x == 0) a.n_valid[s] = n;
-    }
+    if (lane == 0) s_span = sp;
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // loss_rows has ended
   __syncthreads();
   const Span sp = s_span;
   const int n_units = (sp.hi - sp.lo + chunk - 1) / chunk;
+  int n = 0;
+  float z = 0.f;
+  for (int u = threadIdx.x; u < n_units; u += TH) {
+    n += w.pn[sp.unit0 + u];
+    z += w.pz[sp.unit0 + u];
+  }
   float x = 0.f;
   int c = 0;
   if (e < a.E) {
-    for (int u = grp; u < n_units; u += 32) {
-      const long long at = static_cast<long long>(sp.unit0 + u) * a.E + e;
-      x += w.psum[at];
-      c += w.pcnt[at];
+    const float* ps = w.psum + static_cast<long long>(sp.unit0) * a.E + e;
+    const int32_t* pc = w.pcnt + static_cast<long long>(sp.unit0) * a.E + e;
+#pragma unroll 4
+    for (int u = ul; u < n_units; u += LANES) {
+      x += ps[static_cast<long long>(u) * a.E];
+      c += pc[static_cast<long long>(u) * a.E];
     }
   }
-  s_sum[grp][lane] = x;
-  s_cnt[grp][lane] = c;
+  // the warp's unit lanes by a tree, then the warps in order
+#pragma unroll
+  for (int o = EB; o < 32; o <<= 1) {
+    x += __shfl_xor_sync(0xffffffffu, x, o);
+    c += __shfl_xor_sync(0xffffffffu, c, o);
+  }
+  n = __reduce_add_sync(0xffffffffu, n);
+  z = warp_sum(z);
+  if (lane < EB) {
+    s_sum[warp][xe] = x;
+    s_cnt[warp][xe] = c;
+  }
+  if (lane == 0) {
+    s_num[warp] = n;
+    s_red[0][warp] = z;
+  }
   __syncthreads();
-  if (grp == 0) {
+  if (warp == 0) {
+    const int nseg = __reduce_add_sync(0xffffffffu, lane < NW ? s_num[lane] : 0);
+    z = warp_sum(lane < NW ? s_red[0][lane] : 0.f);
     float y = 0.f;
     int d = 0;
 #pragma unroll
-    for (int q = 0; q < 32; ++q) {
-      y += s_sum[q][lane];
-      d += s_cnt[q][lane];
+    for (int q = lane / EB; q < NW; q += 32 / EB) {
+      y += s_sum[q][xe];
+      d += s_cnt[q][xe];
     }
-    if (e < a.E) a.counts[static_cast<long long>(s) * a.E + e] = d;
-    float t = (e < a.E && s_nseg > 0) ? static_cast<float>(d) * (y / static_cast<float>(s_nseg)) : 0.f;
+#pragma unroll
+    for (int o = EB; o < 32; o <<= 1) {
+      y += __shfl_xor_sync(0xffffffffu, y, o);
+      d += __shfl_xor_sync(0xffffffffu, d, o);
+    }
+    const bool mine = lane < EB && e < a.E;
+    if (mine) a.counts[static_cast<long long>(s) * a.E + e] = d;
+    float t = (mine && nseg > 0) ? static_cast<float>(d) * (y / static_cast<float>(nseg)) : 0.f;
     t = warp_sum(t);
     if (lane == 0) {
+      if (blockIdx.x == 0) {
+        a.n_valid[s] = nseg;
+        w.zseg[s] = z;
+      }
       w.term[static_cast<long long>(s) * gridDim.x + blockIdx.x] = t;
       __threadfence();
       s_last = atomicAdd(w.ticket, 1) == static_cast<int>(gridDim.x * gridDim.y) - 1;
@@ -366,36 +454,31 @@ __global__ void __launch_bounds__(kFinishThreads) loss_finish(const RouterLossAr
   __threadfence();
   // the last block: every thread adds a strided part, then a tree
   const int terms = gridDim.x * gridDim.y;
-  // units of the segments come first; the tail's, after them, count nowhere
-  if (grp == 0) {
-    Span tail{0, 0, 0, 0};
-    bool bad = false;
-    walk_segments(a.seg, a.S, a.T, chunk, bad, tail, [&](const Span& q, int) { return q.s == a.S; });
-    if (lane == 0) s_span = tail;
-  }
-  __syncthreads();
-  const int units = s_span.unit0;
-  float b = 0.f, z = 0.f;
-  int n = 0;
+  float b = 0.f;
+  n = 0;
+  z = 0.f;
   const volatile float* term = w.term;
-  for (int i = threadIdx.x; i < terms; i += kFinishThreads) b += term[i];
-  for (int i = threadIdx.x; i < units; i += kFinishThreads) {
-    z += w.pz[i];
-    n += w.pn[i];
+  const volatile float* zseg = w.zseg;
+  const volatile int32_t* nv = a.n_valid;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < terms; i += TH) b += term[i];
+  for (int i = threadIdx.x; i < a.S; i += TH) {
+    z += zseg[i];
+    n += nv[i];
   }
   b = warp_sum(b);
   z = warp_sum(z);
   n = __reduce_add_sync(0xffffffffu, n);
   if (lane == 0) {
-    s_sum[0][grp] = b;
-    s_sum[1][grp] = z;
-    s_cnt[0][grp] = n;
+    s_red[0][warp] = b;
+    s_red[1][warp] = z;
+    s_num[warp] = n;
   }
   __syncthreads();
-  if (grp == 0) {
-    b = warp_sum(s_sum[0][lane]);
-    z = warp_sum(s_sum[1][lane]);
-    n = __reduce_add_sync(0xffffffffu, s_cnt[0][lane]);
+  if (warp == 0) {
+    b = warp_sum(lane < NW ? s_red[0][lane] : 0.f);
+    z = warp_sum(lane < NW ? s_red[1][lane] : 0.f);
+    n = __reduce_add_sync(0xffffffffu, lane < NW ? s_num[lane] : 0);
     if (lane == 0) {
       const float N = static_cast<float>(n);
       a.loss[0] = n > 0 ? b * (static_cast<float>(a.E) / (static_cast<float>(a.k) * N)) : 0.f;
@@ -417,27 +500,50 @@ __device__ __forceinline__ int segment_of(const int32_t* __restrict__ seg, int S
   return lo;
 }
 
-template <class T, int VEC, int NV>
-__global__ void __launch_bounds__(kThreads) loss_bwd(const RouterLossArgs a, int per_warp) {
-  __shared__ int s_part[kWarps];
+template <class T, int VEC, int NV, int L, bool ROUTER>
+__global__ void __launch_bounds__(kBwdThreads) loss_bwd(const RouterLossArgs a, int per_warp) {
+  constexpr int G = 32 / L;
+  constexpr int W = kBwdThreads / 32;
+  extern __shared__ float s_add[];    // ROUTER: a row of E zeros for each group of lanes
+  __shared__ int s_part[W];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int l = lane % L, grp = lane / L;
+  if constexpr (ROUTER)
+    for (int i = threadIdx.x; i < W * G * a.E; i += kBwdThreads) s_add[i] = 0.f;
+  // this warp's tokens: G at a time, per_warp rounds
+  const long long first = (static_cast<long long>(blockIdx.x) * W + warp) * per_warp * G;
+  const T* logits = static_cast<const T*>(a.logits);
   int n = 0;
-  for (int s = threadIdx.x; s < a.S; s += kThreads) n += a.n_valid[s];
+  for (int s = threadIdx.x; s < a.S; s += kBwdThreads) n += a.n_valid[s];
   n = __reduce_add_sync(0xffffffffu, n);
   if (lane == 0) s_part[warp] = n;
   __syncthreads();
   n = 0;
 #pragma unroll
-  for (int q = 0; q < kWarps; ++q) n += s_part[q];
+  for (int q = 0; q < W; ++q) n += s_part[q];
   const float inv_n = n > 0 ? 1.0f / static_cast<float>(n) : 0.f;
   const float gz = 2.f * a.dloss[1] * inv_n;
   const float gb = a.dloss[0] * static_cast<float>(a.E) / static_cast<float>(a.k) * inv_n;
-  const long long first = (static_cast<long long>(blockIdx.x) * kWarps + warp) * per_warp;
-  const int t1 = static_cast<int>(min(first + per_warp, static_cast<long long>(a.T)));
-  const T* logits = static_cast<const T*>(a.logits);
   float wv[NV];
   int cur = -1;
-  for (int t = static_cast<int>(min(first, static_cast<long long>(a.T))); t < t1; ++t) {
+  for (int r = 0; r < per_warp; ++r) {
+    const long long tl = first + static_cast<long long>(r) * G;
+    if (tl >= a.T) break;                       // the same for the whole warp
+    const bool have = tl + grp < a.T;
+    const int t = static_cast<int>(have ? tl + grp : a.T - 1);
+    float v[NV];
+    load_row<T, VEC, NV, L>(logits + static_cast<long long>(t) * a.E, a.E, l, have, v);
+    const float lse = a.lse[t];
+    // the router's own part: lane j of the group has the token's pair j
+    const long long p0 = static_cast<long long>(t) * a.k;
+    int e0 = -1;
+    float pr = 0.f, dp = 0.f;
+    if (ROUTER && l < a.k) {
+      e0 = a.idx[p0 + l];
+      pr = a.probs[p0 + l];
+      dp = a.dprobs[p0 + l];
+    }
+    bool valid = !(lse == -INFINITY) && (a.mask == nullptr || a.mask[t] != 0);
     const int s = segment_of(a.seg, a.S, t);
     if (s != cur) {
       cur = s;
@@ -445,61 +551,85 @@ __global__ void __launch_bounds__(kThreads) loss_bwd(const RouterLossArgs a, int
       const float f = ns > 0 ? gb / static_cast<float>(ns) : 0.f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int e = expert_of<VEC>(lane, i);
+        const int e = expert_of<VEC, L>(l, i);
         wv[i] = (s < a.S && e < a.E)
                     ? f * static_cast<float>(a.counts[static_cast<long long>(s) * a.E + e]) : 0.f;
       }
     }
-    const long long row = static_cast<long long>(t) * a.E;
-    float v[NV];
-    load_row<T, VEC, NV>(logits + row, a.E, lane, v);
-    const float lse = a.lse[t];
-    const bool valid = s < a.S && (a.mask == nullptr || a.mask[t] != 0) && !(lse == -INFINITY);
-    if (valid) {
-      float dot = 0.f;
+    valid = valid && s < a.S;
+    float dot = 0.f;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        v[i] = (v[i] == -INFINITY) ? 0.f : expf(v[i] - lse);
-        dot += v[i] * wv[i];
-      }
-      dot = warp_sum(dot) - gz * lse;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) v[i] *= wv[i] - dot;
-    } else {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) v[i] = 0.f;
+    for (int i = 0; i < NV; ++i) {
+      // (an empty or masked token's values are dropped below, whatever they are)
+      v[i] = exp2_((v[i] - lse) * kLog2E);
+      dot += v[i] * wv[i];
     }
-    if (a.probs != nullptr) {
-      const long long p0 = static_cast<long long>(t) * a.k;
-      float pd = 0.f;
-      for (int j = lane; j < a.k; j += 32) {
+    dot = group_sum<L>(dot) - gz * lse;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] = valid ? v[i] * (wv[i] - dot) : 0.f;
+    if constexpr (ROUTER) {
+      const bool ok0 = e0 >= 0 && e0 < a.E;
+      float pd = ok0 ? pr * dp : 0.f;
+      for (int j = l + L; j < a.k; j += L) {
         const int e = a.idx[p0 + j];
         if (e >= 0 && e < a.E) pd += a.probs[p0 + j] * a.dprobs[p0 + j];
       }
-      pd = warp_sum(pd);
-      for (int j0 = 0; j0 < a.k; j0 += 32) {
-        int e = -1;
-        float r = 0.f;
-        if (j0 + lane < a.k) {
-          e = a.idx[p0 + j0 + lane];
-          r = a.probs[p0 + j0 + lane] * (a.dprobs[p0 + j0 + lane] - pd);
+      pd = group_sum<L>(pd);
+      // The pairs' terms reach the lanes that hold their experts through
+      // the group's row in shared memory: each pair leaves its number at its
+      // expert and reads it back, so that an expert chosen twice shows; such
+      // tokens (no router makes them) take their pairs one after another.
+      float* add = s_add + (warp * G + grp) * a.E;
+      int* tag = reinterpret_cast<int*>(add);
+      for (int j0 = 0; j0 < a.k; j0 += L) {
+        int e = e0;
+        float rr = pr * (dp - pd);
+        if (j0 > 0) {
+          e = -1;
+          if (j0 + l < a.k) {
+            e = a.idx[p0 + j0 + l];
+            rr = a.probs[p0 + j0 + l] * (a.dprobs[p0 + j0 + l] - pd);
+          }
         }
-        const int jn = min(32, a.k - j0);
-        for (int j = 0; j < jn; ++j) {
-          const int ej = __shfl_sync(0xffffffffu, e, j);
-          const float rj = __shfl_sync(0xffffffffu, r, j);
+        const bool in = e >= 0 && e < a.E;
+        if (in) tag[e] = l;
+        __syncwarp();
+        const bool twice = in && tag[e] != l;
+        const bool any_twice = __any_sync(0xffffffffu, twice);
+        __syncwarp();
+        if (!any_twice) {
+          if (in) add[e] = rr;
+        } else {
+          if (in) add[e] = 0.f;
+          __syncwarp();
+          for (int j = 0; j < L; ++j) {
+            if (in && l == j) add[e] += rr;
+            __syncwarp();
+          }
+        }
+        __syncwarp();
+        // every lane takes its experts' terms (zero where there is none) ...
 #pragma unroll
-          for (int i = 0; i < NV; ++i)
-            if (expert_of<VEC>(lane, i) == ej) v[i] += rj;
+        for (int g = 0; g < NV / VEC; ++g) {
+          const int c0 = (l + L * g) * VEC;
+          if (c0 < a.E) {
+#pragma unroll
+            for (int q = 0; q < VEC; ++q) v[g * VEC + q] += add[c0 + q];
+          }
         }
+        __syncwarp();
+        if (in) add[e] = 0.f;    // ... and the row is zero again
+        __syncwarp();
       }
     }
+    if (!have) continue;
+    const long long row = static_cast<long long>(t) * a.E;
 #pragma unroll
     for (int g = 0; g < NV / VEC; ++g) {
-      const int e0 = (lane + 32 * g) * VEC;
-      if (e0 >= a.E) continue;
+      const int c0 = (l + L * g) * VEC;
+      if (c0 >= a.E) continue;
       if (a.dlogits_bf16) {
-        uint16_t* o = static_cast<uint16_t*>(a.dlogits) + row + e0;
+        uint16_t* o = static_cast<uint16_t*>(a.dlogits) + row + c0;
         if constexpr (VEC == 8) {
           *reinterpret_cast<uint4*>(o) =
               make_uint4(pack_bf16x2(v[g * 8], v[g * 8 + 1]), pack_bf16x2(v[g * 8 + 2], v[g * 8 + 3]),
@@ -511,7 +641,7 @@ __global__ void __launch_bounds__(kThreads) loss_bwd(const RouterLossArgs a, int
           *o = static_cast<uint16_t>(pack_bf16x2(v[g], 0.f) & 0xffffu);
         }
       } else {
-        float* o = static_cast<float*>(a.dlogits) + row + e0;
+        float* o = static_cast<float*>(a.dlogits) + row + c0;
         if constexpr (VEC == 1) {
           *o = v[g];
         } else {
@@ -526,41 +656,41 @@ __global__ void __launch_bounds__(kThreads) loss_bwd(const RouterLossArgs a, int
   }
 }
 
-template <class T, int VEC, int NV>
+template <class T, int VEC, int NV, int L>
 cudaError_t go(const RouterLossArgs& a, int num_sms, cudaStream_t s, bool bwd, int chunk,
                const Ws& w) {
   if (bwd) {
-    // consecutive tokens of a warp share their segment's weights: eight at
-    // most, fewer while the SMs are not full
-    int per = (a.T + num_sms * 4 * kWarps - 1) / (num_sms * 4 * kWarps);
+    // rounds of a warp: one while the SMs' 2048 threads are not full, then
+    // up to eight, whose tokens mostly share their segment's weights
+    constexpr int G = 32 / L, W = kBwdThreads / 32;
+    const long long waves = static_cast<long long>(num_sms) * 64 * G;
+    long long per = (a.T + waves - 1) / waves;
     per = per < 1 ? 1 : (per > 8 ? 8 : per);
-    const long long blocks = (static_cast<long long>(a.T) + per * kWarps - 1) / (per * kWarps);
-    loss_bwd<T, VEC, NV><<<static_cast<int>(blocks), kThreads, 0, s>>>(a, per);
+    const long long blocks = (a.T + per * G * W - 1) / (per * G * W);
+    if (a.probs != nullptr)
+      loss_bwd<T, VEC, NV, L, true>
+          <<<static_cast<int>(blocks), kBwdThreads, static_cast<size_t>(W) * G * a.E * 4, s>>>(
+              a, static_cast<int>(per));   // at most 32 KB
+    else
+      loss_bwd<T, VEC, NV, L, false><<<static_cast<int>(blocks), kBwdThreads, 0, s>>>(a, static_cast<int>(per));
   } else {
-    const size_t smem = static_cast<size_t>(kWarps + 1) * a.E * 4;   // at most 36 KB
-    loss_rows<T, VEC, NV><<<units_cap(a.T, a.S), kThreads, smem, s>>>(a, w, chunk);
+    constexpr int W = NV <= 16 ? 16 : 8;    // [W][E] sums: at most 37 KB
+    const size_t smem = static_cast<size_t>(W + 1) * a.E * 4;
+    loss_rows<T, VEC, NV, L, W><<<units_cap(a.T, a.S), 32 * W, smem, s>>>(a, w, chunk);
   }
   return cudaGetLastError();
 }
 
-// values per lane: the smallest instance that covers E
+// lanes and values per lane: the smallest instance that covers E
 template <class T, int VEC>
 cudaError_t pick(const RouterLossArgs& a, int num_sms, cudaStream_t s, bool bwd, int chunk,
                  const Ws& w) {
-  const int groups = (a.E + 32 * VEC - 1) / (32 * VEC);
-  if constexpr (VEC == 1) {
-    if (groups <= 1) return go<T, VEC, 1>(a, num_sms, s, bwd, chunk, w);
-    if (groups <= 2) return go<T, VEC, 2>(a, num_sms, s, bwd, chunk, w);
-    if (groups <= 4) return go<T, VEC, 4>(a, num_sms, s, bwd, chunk, w);
-    if (groups <= 8) return go<T, VEC, 8>(a, num_sms, s, bwd, chunk, w);
-    if (groups <= 16) return go<T, VEC, 16>(a, num_sms, s, bwd, chunk, w);
-    return go<T, VEC, 32>(a, num_sms, s, bwd, chunk, w);
-  } else {
-    if (groups * VEC <= 4) return go<T, VEC, VEC>(a, num_sms, s, bwd, chunk, w);
-    if (groups * VEC <= 8) return go<T, VEC, 8>(a, num_sms, s, bwd, chunk, w);
-    if (groups * VEC <= 16) return go<T, VEC, 16>(a, num_sms, s, bwd, chunk, w);
-    return go<T, VEC, 32>(a, num_sms, s, bwd, chunk, w);
-  }
+  if (a.E <= 32) return go<T, VEC, 8, 4>(a, num_sms, s, bwd, chunk, w);
+  if (a.E <= 64) return go<T, VEC, 8, 8>(a, num_sms, s, bwd, chunk, w);
+  if (a.E <= 128) return go<T, VEC, 8, 16>(a, num_sms, s, bwd, chunk, w);
+  if (a.E <= 256) return go<T, VEC, 8, 32>(a, num_sms, s, bwd, chunk, w);
+  if (a.E <= 512) return go<T, VEC, 16, 32>(a, num_sms, s, bwd, chunk, w);
+  return go<T, VEC, 32, 32>(a, num_sms, s, bwd, chunk, w);
 }
 
 cudaError_t dispatch(const RouterLossArgs& a, int num_sms, cudaStream_t s, bool bwd, int chunk,
@@ -589,9 +719,21 @@ cudaError_t launch_router_loss(const RouterLossArgs& a, int num_sms, cudaStream_
   *launches = 0;
   const cudaError_t e = dispatch(a, num_sms, s, false, chunk, w);
   if (e != cudaSuccess) return e;
-  loss_finish<<<dim3(slices_of(a.E), a.S), kFinishThreads, 0, s>>>(a, w, chunk);
+  // programmatic launch: loss_finish's blocks come in behind loss_rows and
+  // wait on the device for it to end
+  cudaLaunchConfig_t cfg = {};
+  const bool few = finish_experts(a.S) == 8;
+  cfg.gridDim = dim3(slices_of(a.E, a.S), a.S);
+  cfg.blockDim = dim3(few ? 1024 : 256);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
   *launches = 2;
-  return cudaGetLastError();
+  return few ? cudaLaunchKernelEx(&cfg, loss_finish<8, 1024>, a, w, chunk)
+             : cudaLaunchKernelEx(&cfg, loss_finish<32, 256>, a, w, chunk);
 }
 
 cudaError_t launch_router_loss_bwd(const RouterLossArgs& a, int num_sms, cudaStream_t s) {

@@ -710,9 +710,9 @@ int moe_mx_quantize_tiled(const moe_bf16* src, int rows, int cols,
  *               MOE_DEV_BAD_OFFSETS).  NULL with S = 1: one sequence of all T.
  *   token_mask  [T] uint8 or NULL: 0 takes the token out.
  * A token is valid if it lies in a sequence, is not masked and has a logit
- * above the lowest finite value of its type (a row that -inf or that value
- * masks throughout is empty: its lse is -inf).  With P_t = softmax of all E
- * logits, lse_t their log-sum-exp,
+ * above bf16's lowest finite value (a row masked throughout by -inf or by
+ * float32's or bf16's lowest value is empty: its lse is -inf).  With P_t =
+ * softmax of all E logits, lse_t their log-sum-exp,
  * c_se the pairs of s's valid tokens that chose e, N_s its valid tokens and
  * N their sum:
  *   loss[0] = E / (k N) sum_s 1 / N_s sum_e c_se sum_{t in s} P_te

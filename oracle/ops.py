@@ -22,17 +22,16 @@ __all__ = ["router_loss", "router_loss_bwd", "linear_act", "linear_dact", "linea
 # the common training terms)
 # ---------------------------------------------------------------------------
 
-LOWEST_F32 = -3.4028234663852886e38
-LOWEST_BF16 = -3.3895313892515355e38
+LOWEST = -3.3895313892515355e38     # bf16's lowest finite value
 
 
-def _softmax(logits, lowest=LOWEST_F32):
-    """P [T, E] and lse [T]; a row with nothing above ``lowest`` (a mask of
-    -inf or of the type's lowest value) is empty: P = 0 and lse = -inf."""
+def _softmax(logits):
+    """P [T, E] and lse [T]; a row with nothing above bf16's lowest value (a
+    mask of -inf or of a type's lowest) is empty: P = 0 and lse = -inf."""
     z = np.asarray(logits, np.float64)
     m = z.max(axis=1)
-    z = np.where((m <= lowest)[:, None], -np.inf, z)
-    m = np.where(m <= lowest, -np.inf, m)
+    z = np.where((m <= LOWEST)[:, None], -np.inf, z)
+    m = np.where(m <= LOWEST, -np.inf, m)
     safe = np.where(np.isneginf(m), 0.0, m)
     with np.errstate(invalid="ignore", divide="ignore", over="ignore"):
         e = np.where(np.isneginf(z), 0.0, np.exp(z - safe[:, None]))
@@ -50,13 +49,13 @@ def _segments(T, seg):
     return len(seg) - 1, owner
 
 
-def router_loss(logits, topk_idx, seg_offsets=None, token_mask=None, lowest=LOWEST_F32):
+def router_loss(logits, topk_idx, seg_offsets=None, token_mask=None):
     """loss [2] (balance, z), counts [S, E], lse [T], n_valid [S]: see
     ``moe_router_loss``.  Balance E/(kN) sum_s 1/N_s sum_e c_se sum_t P_te;
     z the mean squared log-partition of the valid tokens."""
     T, E = np.shape(logits)
     k = np.shape(topk_idx)[1]
-    P, lse = _softmax(logits, lowest)
+    P, lse = _softmax(logits)
     S, owner = _segments(T, seg_offsets)
     valid = (owner >= 0) & ~np.isneginf(lse)
     if token_mask is not None:
@@ -79,15 +78,15 @@ def router_loss(logits, topk_idx, seg_offsets=None, token_mask=None, lowest=LOWE
 
 
 def router_loss_bwd(logits, topk_idx, dloss, probs=None, dprobs=None, seg_offsets=None,
-                    token_mask=None, lowest=LOWEST_F32):
+                    token_mask=None):
     """dlogits [T, E] of dloss . loss (counts held constant) and, with probs
     and dprobs, of the softmax over the selected logits ([Sonic] "역전파 계산
     그래프 재작성하기": dS reaches the router)."""
     T, E = np.shape(logits)
     idx = np.asarray(topk_idx)
     k = idx.shape[1]
-    f = router_loss(logits, topk_idx, seg_offsets, token_mask, lowest)
-    P, lse = _softmax(logits, lowest)
+    f = router_loss(logits, topk_idx, seg_offsets, token_mask)
+    P, lse = _softmax(logits)
     S, owner = _segments(T, seg_offsets)
     N = int(f["n_valid"].sum())
     d = np.zeros((T, E))

@@ -128,16 +128,17 @@ def test_rows_without_a_finite_logit_and_special_values():
     gg = g.cpu().numpy()
     assert np.isfinite(gg).all() and np.all(gg[[3, 6, 9]] == 0)
     assert np.isneginf(r["lse"][3].item()) and np.isneginf(r["lse"][6].item())
-    # the same masks in bf16, whose lowest value is another one
+    # the same masks in bf16, whose lowest value is another one, and that in float32
     zb = torch.from_numpy(z).bfloat16()
     zb[5, :6] = torch.finfo(torch.bfloat16).min
     zb[6] = torch.finfo(torch.bfloat16).min
-    r = M.router_loss(zb.cuda(), cuda_i32(idx), token_mask=_cuda(mask))
-    torch.cuda.synchronize()
-    ref = O.router_loss(zb.double().numpy(), idx, None, mask, O.ops.LOWEST_BF16)
-    assert int(r["n_valid"].item()) == T - 3
-    got = r["loss"].cpu().numpy()
-    assert np.all(np.abs(got - ref["loss"]) <= 256 * U * np.abs(ref["loss"]))
+    ref = O.router_loss(zb.double().numpy(), idx, None, mask)
+    for zz in (zb, zb.float()):
+        r = M.router_loss(zz.cuda(), cuda_i32(idx), token_mask=_cuda(mask))
+        torch.cuda.synchronize()
+        assert int(r["n_valid"].item()) == T - 3
+        got = r["loss"].cpu().numpy()
+        assert np.all(np.abs(got - ref["loss"]) <= 256 * U * np.abs(ref["loss"]))
     # NaN in a valid row reaches the losses, and only that row's gradient
     z[2, 3] = np.nan
     r = M.router_loss(_cuda(z), cuda_i32(idx))
