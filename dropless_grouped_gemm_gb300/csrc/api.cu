@@ -1205,7 +1205,7 @@ int moe_grouped_linear(const moe_bf16* a, const int32_t* offsets, int E, int M_c
   const bool f32 = out_type == MOE_TYPE_F32;
   CUtensorMap tb;
   if (kn ? !map_w(&tb, B, E, K, N, 64) : !map_w(&tb, B, E, N, K, 128)) return MOE_E_CUDA;
-  const moe::FewPlan plan = moe::few_plan(E, M_cap, K, N, offsets != nullptr, sms);
+  const moe::FewPlan plan = moe::few_plan(E, M_cap, K, N, offsets != nullptr, f32, sms);
   CUtensorMap ta;
   if (!map_act(&ta, a, M_cap, K, plan.tn ? plan.tn : moe::kBM)) return MOE_E_CUDA;
   if (plan.tn) {
@@ -1223,11 +1223,9 @@ int moe_grouped_linear(const moe_bf16* a, const int32_t* offsets, int E, int M_c
   moe::GemmArgs g{};
   g.offsets = offsets; g.E = E; g.M_cap = M_cap; g.K = K; g.N = N; g.err = err;
   g.act = act; g.bias = bias; g.residual = residual; g.out2 = z; g.ldo2 = N; g.ldo = n_out;
-  g.out = f32 ? nullptr : static_cast<uint16_t*>(out);
-  g.out_f32 = f32 ? static_cast<float*>(out) : nullptr;
-  CUtensorMap tz = ta, to = ta;
-  if ((z && !map_out2(&tz, z, M_cap, N)) || (!f32 && !map_out2(&to, out, M_cap, n_out)))
-    return MOE_E_CUDA;
+  g.out = static_cast<uint16_t*>(out);
+  CUtensorMap tz = ta, to;
+  if ((z && !map_out2(&tz, z, M_cap, N)) || !map_out2(&to, out, M_cap, n_out)) return MOE_E_CUDA;
   g.tma_out = 1;
   const cudaError_t e = gemm(kn ? moe::GemmKind::kLinearKN : moe::GemmKind::kLinearNK, act, ta, tb,
                              tz, g, sms, s, &to);

@@ -97,7 +97,6 @@ struct GemmArgs {
   int act;                     // MOE_ACT_*
   const uint16_t* bias;        // [E, N] bf16 or NULL
   const uint16_t* residual;    // [M_cap, ldo] bf16 or NULL
-  float* out_f32;              // [M_cap, ldo]: float32 output in place of out
 };
 
 // Launches the persistent grouped GEMM of `kind` (act: MOE_ACT_*) on `s`.

@@ -466,7 +466,7 @@ __device__ __forceinline__ void linear_chunk(const GemmArgs& g, const Tile& tl, 
   float v[32];
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-  if (g.bias != nullptr) add_bf16x32(g.bias + static_cast<long long>(tl.e) * g.N + col, v);
+  if (g.bias != nullptr) add_bf16<32>(g.bias + static_cast<long long>(tl.e) * g.N + col, v);
   if (g.out2 != nullptr) {
     uint32_t p[16];
 #pragma unroll
@@ -475,32 +475,16 @@ __device__ __forceinline__ void linear_chunk(const GemmArgs& g, const Tile& tl, 
     else if (valid) store_pairs<4>(g.out2 + grow * g.ldo2 + col, p);
   }
   if constexpr (!GATED) {
-    linear_act32(g.act, v);
-    if (g.residual != nullptr && valid) add_bf16x32(g.residual + grow * g.ldo + col, v);
-    if (g.out_f32 != nullptr) {
-      if (valid) {
-        float4* o = reinterpret_cast<float4*>(g.out_f32 + grow * g.ldo + col);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-      }
-      return;
-    }
+    linear_act(g.act, v);
+    if (g.residual != nullptr && valid) add_bf16<32>(g.residual + grow * g.ldo + col, v);
 #pragma unroll
     for (int i = 0; i < 16; ++i) av[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
     if (box != nullptr) put_box32(box, av, to, col, y0);
     else if (valid) store_pairs<4>(g.out + grow * g.ldo + col, av);
   } else {
     float u[16];
-    glu16(g.act, v, u);
-    if (g.residual != nullptr && valid) add_bf16x16(g.residual + grow * g.ldo + col / 2, u);
-    if (g.out_f32 != nullptr) {
-      if (valid) {
-        float4* o = reinterpret_cast<float4*>(g.out_f32 + grow * g.ldo + col / 2);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = make_float4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
-      }
-      return;
-    }
+    linear_glu(g.act, v, u);
+    if (g.residual != nullptr && valid) add_bf16<16>(g.residual + grow * g.ldo + col / 2, u);
     const int h = (cc & 1) * 8;
 #pragma unroll
     for (int i = 0; i < 8; ++i) av[h + i] = pack_bf16x2(u[2 * i], u[2 * i + 1]);

@@ -11,13 +11,20 @@
 // operand, D[column, token] in TMEM; and `split` CTAs of a cluster share one
 // tile's reduction, each streaming its part of K into its own TMEM.  They
 // join through distributed shared memory: each CTA leaves its float32
-// partials in its own buffer, and token t's sum is formed by CTA t % split
+// partials in its own buffer, and token t's sum is formed by one of the CTAs
 // in the order of the ranks, so reruns are bitwise identical and no
 // workspace, atomic or second launch is needed.
 //
-// Roles (192 threads): warp 0 TMA producer, warp 1 TMEM owner and MMA
-// issuer, warps 2-5 epilogue (a thread per output column).  Up to two CTAs
-// an SM keep one tile's loads running under another's epilogue.
+// The tensor cores add into their float32 accumulator with less than a
+// float32 addition's rounding, an error that grows with the number of
+// additions (K = 7168 in one chain: 3.7e-6 of the result, against 8e-7 for a
+// float32 product).  A float32 output therefore ends its chains after 1024
+// of K and adds them in shared memory.
+//
+// Roles (192 threads, one CTA an SM, so that the stages can hold 130 to 200
+// KB of loads in flight): warp 0 TMA producer, warp 1 TMEM owner and MMA
+// issuer, warps 2-5 epilogue.  (Eight epilogue warps shorten a single tile's
+// output pass, and slowed the streaming of many tiles by 4 to 6%.)
 #include <cuda_runtime.h>
 
 #include "act.cuh"
@@ -28,20 +35,20 @@ namespace moe {
 namespace {
 
 constexpr int FT = 192;               // threads
+constexpr int FE = 4;                 // epilogue warps, one for each TMEM lane quadrant
 constexpr int FM = 128;               // output columns per tile
 constexpr int FK = 64;                // reduction elements per stage
 constexpr int W_BYTES = FM * FK * 2;  // 16 KB
 constexpr int W_BOX = 64 * FK * 2;    // a 64 (columns) x 64 (K) box
 constexpr int MAX_SPLIT = 8;
+constexpr int CHAIN = 1024 / FK;      // stages per accumulation chain, float32 output
 
 template <int TN>
 struct FC {
   static constexpr int x_bytes = TN * FK * 2;
   static constexpr int stage_bytes = W_BYTES + x_bytes;
-  static constexpr int red_bytes = TN * FM * 4;
-  // two CTAs an SM up to TN = 64, one at 128
-  static constexpr int stages = TN == 16 ? 5 : TN == 32 ? 4 : TN == 64 ? 3 : 4;
-  static constexpr int ctas = TN <= 64 ? 2 : 1;
+  static constexpr int stages = TN == 16 ? 11 : TN == 32 ? 9 : TN == 64 ? 7 : 4;
+  static constexpr int red_bytes = TN * FM * 4;   // the tile's float32 sums
   static constexpr int tmem_cols = 2 * TN;   // two accumulators; a power of two >= 32
   static constexpr size_t smem(int E) {
     return 1024 + static_cast<size_t>(stages) * stage_bytes + red_bytes + (2 * stages + 7) * 8 +
@@ -54,57 +61,128 @@ struct FTile {
 };
 
 // unit u -> tile: an expert's units run over its token tiles first, so that
-// consecutive units share their weights through L2
+// consecutive units share their weights through L2.  Dense (no offsets): by
+// arithmetic alone.
 template <int TN>
 __device__ __forceinline__ FTile few_tile(const FewArgs& g, const int* s_off, const int* s_ts,
                                           int u) {
-  int lo = 0, hi = g.E - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (s_ts[mid + 1] <= u) lo = mid + 1;
-    else hi = mid;
+  int lo = 0, first = 0, rows = g.M_cap, at = 0;
+  if (g.offsets != nullptr) {
+    int hi = g.E - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (s_ts[mid + 1] <= u) lo = mid + 1;
+      else hi = mid;
+    }
+    rows = s_off[lo + 1] - s_off[lo];
+    first = s_off[lo];
+    at = s_ts[lo];
   }
-  const int rows = s_off[lo + 1] - s_off[lo];
   const int tt = (rows + TN - 1) / TN;
-  const int local = u - s_ts[lo];
+  const int local = u - at;
   const int ni = local / tt;
   const int ti = local - ni * tt;
   FTile t;
   t.e = lo;
-  t.row0 = s_off[lo] + ti * TN;
+  t.row0 = first + ti * TN;
   t.rows = min(TN, rows - ti * TN);
   t.n0 = ni * FM;
   return t;
 }
 
-// one output value: thread's column c of row `row`, z = the full sum
-template <bool GATED>
-__device__ __forceinline__ void few_out(const FewArgs& g, long long row, int c, float z,
-                                        float bias) {
-  z += bias;
-  const bool ok = c < g.N;
-  if (g.z != nullptr && ok)
-    g.z[row * g.N + c] = static_cast<uint16_t>(pack_bf16x2(z, 0.f) & 0xffffu);
-  int oc = c;
-  bool mine = ok;
-  float v;
-  if constexpr (GATED) {
-    const float up = __shfl_down_sync(0xffffffffu, z, 1);   // column c + 1
-    v = (g.act == MOE_ACT_SWIGLU ? gate_phi<MOE_ACT_SWIGLU>(z) : gate_phi<MOE_ACT_GEGLU>(z)) * up;
-    mine = ok && !(c & 1);
-    oc = c >> 1;
-  } else {
-    v = linear_act1(g.act, z);
+// 8 float32 values from the same place in each of the cluster's CTAs, added
+// in the order of the ranks (split 1: this CTA's own)
+__device__ __forceinline__ void sum8(const float* p, int split, float (&z)[8]) {
+  if (split == 1) {
+    const float4 a = *reinterpret_cast<const float4*>(p);
+    const float4 b = *reinterpret_cast<const float4*>(p + 4);
+    z[0] = a.x; z[1] = a.y; z[2] = a.z; z[3] = a.w;
+    z[4] = b.x; z[5] = b.y; z[6] = b.z; z[7] = b.w;
+    return;
   }
-  if (!mine) return;
-  const long long at = row * g.ldo + oc;
-  if (g.residual != nullptr) v += __uint_as_float(static_cast<uint32_t>(g.residual[at]) << 16);
-  if (g.out_f32 != nullptr) g.out_f32[at] = v;
-  else g.out[at] = static_cast<uint16_t>(pack_bf16x2(v, 0.f) & 0xffffu);
+  const uint32_t at = smem_u32(p);
+  float w[MAX_SPLIT][8];
+#pragma unroll
+  for (int r = 0; r < MAX_SPLIT; ++r)
+    if (r < split) {
+      const uint32_t pa = mapa_shared(at, r);
+      ld_cluster_v4(pa, w[r][0], w[r][1], w[r][2], w[r][3]);
+      ld_cluster_v4(pa + 16, w[r][4], w[r][5], w[r][6], w[r][7]);
+    }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) z[i] = w[0][i];
+#pragma unroll
+  for (int r = 1; r < MAX_SPLIT; ++r)
+    if (r < split) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z[i] += w[r][i];
+    }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                    pack_bf16x2(v[6], v[7]));
+}
+
+// 8 neighbouring columns from c (a multiple of 8 below N) of row `row`: bias,
+// pre-activation, activation, residual, output
+template <bool GATED>
+__device__ __forceinline__ void few_out(const FewArgs& g, long long row, int c, const uint4& bias,
+                                        float (&z)[8]) {
+  const uint32_t b[4] = {bias.x, bias.y, bias.z, bias.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    z[2 * i] += bf16_lo(b[i]);
+    z[2 * i + 1] += bf16_hi(b[i]);
+  }
+  if (g.z != nullptr) *reinterpret_cast<uint4*>(g.z + row * g.N + c) = pack8(z);
+  if constexpr (!GATED) {
+    linear_act(g.act, z);
+    const long long at = row * g.ldo + c;
+    if (g.residual != nullptr) add_bf16<8>(g.residual + at, z);
+    if (g.out_f32 != nullptr) {
+      float4* o = reinterpret_cast<float4*>(g.out_f32 + at);
+      o[0] = make_float4(z[0], z[1], z[2], z[3]);
+      o[1] = make_float4(z[4], z[5], z[6], z[7]);
+    } else {
+      *reinterpret_cast<uint4*>(g.out + at) = pack8(z);
+    }
+  } else {
+    float v[4];
+    linear_glu(g.act, z, v);
+    const long long at = row * g.ldo + c / 2;
+    if (g.residual != nullptr) {
+      const uint2 r = *reinterpret_cast<const uint2*>(g.residual + at);
+      v[0] += bf16_lo(r.x); v[1] += bf16_hi(r.x); v[2] += bf16_lo(r.y); v[3] += bf16_hi(r.y);
+    }
+    if (g.out_f32 != nullptr)
+      *reinterpret_cast<float4*>(g.out_f32 + at) = make_float4(v[0], v[1], v[2], v[3]);
+    else
+      *reinterpret_cast<uint2*>(g.out + at) =
+          make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+  }
+}
+
+// the accumulator columns of the tile's tokens of this thread's lane into its
+// column of the tile's sums (put, or added to what earlier chains left)
+__device__ __forceinline__ void take_chain(uint32_t tb, int tokens, bool first, float* col) {
+#pragma unroll 1
+  for (int t = 0; t < tokens; t += 16) {
+    uint32_t r[16];
+    tmem_ld16(tb + t, r);
+    tmem_wait_ld();
+    if (first) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) col[(t + i) * FM] = __uint_as_float(r[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) col[(t + i) * FM] += __uint_as_float(r[i]);
+    }
+  }
 }
 
 template <bool KN, int TN, bool GATED>
-__global__ void __launch_bounds__(FT, FC<TN>::ctas)
+__global__ void __launch_bounds__(FT, 1)
     few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                const FewArgs g) {
   using C = FC<TN>;
@@ -132,6 +210,25 @@ __global__ void __launch_bounds__(FT, FC<TN>::ctas)
   const int rank = static_cast<int>(cluster_ctarank());
   const int unit0 = blockIdx.x / split;
   const int unit_step = gridDim.x / split;
+  const int nt = (g.N + FM - 1) / FM;
+  const int kblocks = g.K / FK;
+  const int kb0 = static_cast<int>(static_cast<long long>(kblocks) * rank / split);
+  const int kb1 = static_cast<int>(static_cast<long long>(kblocks) * (rank + 1) / split);
+  const int chain = g.out_f32 != nullptr ? CHAIN : kblocks;
+
+  auto load = [&](const FTile& t, int kb, int stage) {
+    uint8_t* sw = smem + stage * C::stage_bytes;
+    uint64_t* fb = &full_bar[stage];
+    mbar_arrive_expect_tx(fb, C::stage_bytes);
+    if constexpr (KN) {
+      tma_load_3d(sw, &tmW, fb, t.n0, kb * FK, t.e);
+      tma_load_3d(sw + W_BOX, &tmW, fb, t.n0 + 64, kb * FK, t.e);
+    } else {
+      tma_load_3d(sw, &tmW, fb, kb * FK, t.n0, t.e);
+    }
+    tma_load_2d(sw + W_BYTES, &tmX, fb, kb * FK, t.row0);
+  };
+  int ahead = 0;      // stages of the first unit that are already loading
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < NST; ++i) {
@@ -140,129 +237,128 @@ __global__ void __launch_bounds__(FT, FC<TN>::ctas)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull_bar[i], 1);
-      mbar_init(&tempty_bar[i], 4);
+      mbar_init(&tempty_bar[i], FE);
     }
-    mbar_init(rfull_bar, 4 * split);
-    mbar_init(rempty_bar, 4 * split);
+    mbar_init(rfull_bar, FE * split);
+    mbar_init(rempty_bar, FE * split);
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     fence_mbar_init();
-    prefetch_tmap(&tmW);
-    prefetch_tmap(&tmX);
+    // dense: the first unit is known, so its loads start before anything else
+    if (g.offsets == nullptr && unit0 < nt * ((g.M_cap + TN - 1) / TN)) {
+      const FTile t = few_tile<TN>(g, nullptr, nullptr, unit0);
+      for (; ahead < NST && kb0 + ahead < kb1; ++ahead) load(t, kb0 + ahead, ahead);
+    }
   }
   if (warp == 1) tmem_alloc(tmem_slot, C::tmem_cols);
-  if (warp == 2) {
-    // offsets made safe and the units' prefix, as in the grouped GEMM
+  if (warp == 2 && g.offsets != nullptr) {
+    // offsets made safe (within [0, M_cap], non-decreasing, from 0) and the
+    // experts' first units, 32 experts at a time
     bool bad = false;
-    for (int i = lane; i <= g.E; i += 32) {
-      const int v = g.offsets != nullptr ? g.offsets[i] : (i == 0 ? 0 : g.M_cap);
-      if (v < 0 || v > g.M_cap) bad = true;
-      s_off[i] = min(max(v, 0), g.M_cap);
-    }
-    __syncwarp();
-    if (lane == 0) {
-      int prev = 0;
-      for (int i = 0; i <= g.E; ++i) {
-        if (s_off[i] < prev) { bad = true; s_off[i] = prev; }
-        prev = s_off[i];
-      }
-      if (s_off[0] != 0) bad = true;
-    }
-    if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0) set_err(g.err, MOE_DEV_BAD_OFFSETS);
-    __syncwarp();
-    const int nt = (g.N + FM - 1) / FM;
-    int carry = 0;
-    for (int base = 0; base < g.E; base += 32) {
-      const int e = base + lane;
-      const int t = (e < g.E) ? (s_off[e + 1] - s_off[e] + TN - 1) / TN * nt : 0;
-      int v = t;
+    int top = 0, carry = 0;
+    for (int base = 0; base <= g.E; base += 32) {
+      const int i = base + lane;
+      const int raw = i <= g.E ? g.offsets[i] : 0;
+      int v = min(max(raw, 0), g.M_cap);
+      if (i == 0) v = 0;
+      int m = max(v, top);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += y;
+        const int y = __shfl_up_sync(0xffffffffu, m, o);
+        if (lane >= o) m = max(m, y);
       }
-      if (e < g.E) s_ts[e] = carry + v - t;
-      carry += __shfl_sync(0xffffffffu, v, 31);
+      if (i <= g.E) {
+        if (m != raw) bad = true;
+        s_off[i] = m;
+      }
+      // expert i - 1 ends at m
+      int prev = __shfl_up_sync(0xffffffffu, m, 1);
+      if (lane == 0) prev = top;
+      int c = (i >= 1 && i <= g.E) ? (m - prev + TN - 1) / TN * nt : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, c, o);
+        if (lane >= o) c += y;
+      }
+      if (i <= g.E) s_ts[i] = carry + c;
+      top = __shfl_sync(0xffffffffu, m, 31);
+      carry += __shfl_sync(0xffffffffu, c, 31);
     }
-    if (lane == 0) s_ts[g.E] = carry;
+    if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0) set_err(g.err, MOE_DEV_BAD_OFFSETS);
   }
   tc_fence_before();
-  // the peers' barriers are initialised before any CTA arrives on them
-  cluster_sync();
+  __syncthreads();
   tc_fence_after();
+  // the peers' barriers are initialised before the epilogue arrives on them
+  // (it waits then; everything before runs ahead)
+  cluster_arrive();
 
   const uint32_t tmem_base = *tmem_slot;
-  const int units = s_ts[g.E];
-  const int kblocks = g.K / FK;
-  const int kb0 = static_cast<int>(static_cast<long long>(kblocks) * rank / split);
-  const int kb1 = static_cast<int>(static_cast<long long>(kblocks) * (rank + 1) / split);
+  const int units = g.offsets != nullptr ? s_ts[g.E] : nt * ((g.M_cap + TN - 1) / TN);
 
   if (warp == 0) {
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0;
-      bool issued[NST];
-      uint32_t issued_parity[NST];
-      for (int i = 0; i < NST; ++i) { issued[i] = false; issued_parity[i] = 0; }
       bool ok = true;
+      uint32_t used = 0, parity = 0;    // stages loaded so far, and their phases
+      for (int i = 0; i < ahead; ++i) used |= 1u << i;
       for (int u = unit0; u < units && ok; u += unit_step) {
         const FTile t = few_tile<TN>(g, s_off, s_ts, u);
         for (int kb = kb0; kb < kb1; ++kb) {
-          if (!mbar_wait(&empty_bar[stage], phase ^ 1, abort_flag)) { ok = false; break; }
-          uint8_t* sw = smem + stage * C::stage_bytes;
-          uint64_t* fb = &full_bar[stage];
-          mbar_arrive_expect_tx(fb, C::stage_bytes);
-          if constexpr (KN) {
-            tma_load_3d(sw, &tmW, fb, t.n0, kb * FK, t.e);
-            tma_load_3d(sw + W_BOX, &tmW, fb, t.n0 + 64, kb * FK, t.e);
+          if (ahead > 0) {
+            --ahead;
           } else {
-            tma_load_3d(sw, &tmW, fb, kb * FK, t.n0, t.e);
+            if (!mbar_wait(&empty_bar[stage], phase ^ 1, abort_flag)) { ok = false; break; }
+            load(t, kb, stage);
+            used |= 1u << stage;
+            parity = (parity & ~(1u << stage)) | (phase << stage);
           }
-          tma_load_2d(sw + W_BYTES, &tmX, fb, kb * FK, t.row0);
-          issued[stage] = true;
-          issued_parity[stage] = phase;
           if (++stage == NST) { stage = 0; phase ^= 1; }
         }
       }
       if (!ok) {
         // give up: wait (bounded) for the copies in flight
         for (int i = 0; i < NST; ++i)
-          if (issued[i]) {
+          if ((used >> i) & 1u) {
             const uint32_t a = smem_u32(&full_bar[i]);
             const uint64_t t0 = globaltimer_ns();
-            while (!mbar_try_wait(a, issued_parity[i]) && globaltimer_ns() - t0 < kWaitLimitNs) {}
+            while (!mbar_try_wait(a, (parity >> i) & 1u) && globaltimer_ns() - t0 < kWaitLimitNs) {}
           }
       }
     }
     __syncwarp();
+    cluster_wait();
   } else if (warp == 1) {
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0;
-      int local = 0;
+      int local = 0;                    // chains so far
       bool ok = true;
-      for (int u = unit0; u < units && ok; u += unit_step, ++local) {
-        const int buf = local & 1;
-        const uint32_t aph = (local >> 1) & 1;
-        if (!mbar_wait(&tempty_bar[buf], aph ^ 1, abort_flag)) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t d = tmem_base + buf * TN;
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if (!mbar_wait(&full_bar[stage], phase, abort_flag)) { ok = false; break; }
+      for (int u = unit0; u < units && ok; u += unit_step) {
+        for (int c0 = kb0; c0 < kb1 && ok; c0 += chain, ++local) {
+          const int buf = local & 1;
+          if (!mbar_wait(&tempty_bar[buf], ((local >> 1) & 1) ^ 1, abort_flag)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t w0 = smem_u32(smem + stage * C::stage_bytes);
-          const uint32_t x0 = w0 + W_BYTES;
+          const uint32_t d = tmem_base + buf * TN;
+          const int c1 = min(c0 + chain, kb1);
+          for (int kb = c0; kb < c1; ++kb) {
+            if (!mbar_wait(&full_bar[stage], phase, abort_flag)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t w0 = smem_u32(smem + stage * C::stage_bytes);
+            const uint32_t x0 = w0 + W_BYTES;
 #pragma unroll
-          for (int kk = 0; kk < FK / 16; ++kk) {
-            const uint64_t wd = KN ? sdesc_sw128(w0 + kk * 2048, W_BOX, 1024)
-                                   : sdesc_sw128(w0 + kk * 32, 16, 1024);
-            const uint64_t xd = sdesc_sw128(x0 + kk * 32, 16, 1024);
-            umma_bf16(d, wd, xd, IDESC, (kb > kb0 || kk > 0) ? 1u : 0u);
+            for (int kk = 0; kk < FK / 16; ++kk) {
+              const uint64_t wd = KN ? sdesc_sw128(w0 + kk * 2048, W_BOX, 1024)
+                                     : sdesc_sw128(w0 + kk * 32, 16, 1024);
+              const uint64_t xd = sdesc_sw128(x0 + kk * 32, 16, 1024);
+              umma_bf16(d, wd, xd, IDESC, (kb > c0 || kk > 0) ? 1u : 0u);
+            }
+            umma_commit(&empty_bar[stage]);
+            if (++stage == NST) { stage = 0; phase ^= 1; }
           }
-          umma_commit(&empty_bar[stage]);
-          if (++stage == NST) { stage = 0; phase ^= 1; }
+          if (ok) umma_commit(&tfull_bar[buf]);
         }
-        if (ok) umma_commit(&tfull_bar[buf]);
       }
       if (!ok) {
         // give up: the MMAs already issued finish before TMEM is freed
@@ -273,70 +369,84 @@ __global__ void __launch_bounds__(FT, FC<TN>::ctas)
       }
     }
     __syncwarp();
+    cluster_wait();
   } else {
     const int q = warp & 3;                 // TMEM lane quadrant
-    const int n = q * 32 + lane;            // output column within the tile
-    int local = 0;
-    for (int u = unit0; u < units; u += unit_step, ++local) {
+    const int tid = q * 32 + lane;          // its column of the tile, then its place in the output pass
+    int local = 0, mine = 0;                // chains and units so far
+    bool ok = true, joined = false;
+    for (int u = unit0; u < units && ok; u += unit_step, ++mine) {
       const FTile t = few_tile<TN>(g, s_off, s_ts, u);
-      const int buf = local & 1;
-      const uint32_t aph = (local >> 1) & 1;
-      const int c = t.n0 + n;
-      const float bias = (g.bias != nullptr && c < g.N)
-          ? __uint_as_float(static_cast<uint32_t>(g.bias[static_cast<long long>(t.e) * g.N + c]) << 16)
-          : 0.f;
-      bool ok = true;
-      if (lane == 0) {
-        ok = mbar_wait(&tfull_bar[buf], aph, abort_flag);
-        // the peers have read the previous unit's partials
-        if (ok && split > 1 && local > 0)
-          ok = mbar_wait_cluster(rempty_bar, (local - 1) & 1, abort_flag);
+      // the output's part of the tile: a thread takes 8 neighbouring columns
+      // of a token, 16 threads a token, tokens rank, rank + split, ...  What
+      // it reads there is on its way while the tile is computed.
+      const int c = t.n0 + (tid & 15) * 8;
+      uint4 bias = make_uint4(0, 0, 0, 0);
+      if (c < g.N) {
+        if (g.bias != nullptr)
+          bias = __ldg(reinterpret_cast<const uint4*>(g.bias + static_cast<long long>(t.e) * g.N + c));
+        const int k = rank + (tid >> 4) * split;
+        if (g.residual != nullptr && k < t.rows)
+          prefetch_l2(g.residual + (static_cast<long long>(t.row0) + k) * g.ldo + (GATED ? c / 2 : c));
       }
-      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-      tc_fence_after();
-      const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * TN;
-      // the accumulators, 16 tokens at a time
-      for (int t0 = 0; t0 < TN; t0 += 16) {
-        if (t0 >= t.rows) break;            // uniform: the rest are other rows
-        uint32_t r[16];
-        tmem_ld16(tb + t0, r);
-        tmem_wait_ld();
-        if (split > 1) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) red[(t0 + i) * FM + n] = __uint_as_float(r[i]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (t0 + i < t.rows)
-              few_out<GATED>(g, static_cast<long long>(t.row0) + t0 + i, c, __uint_as_float(r[i]), bias);
+      for (int c0 = kb0; c0 < kb1 && ok; c0 += chain, ++local) {
+        const int buf = local & 1;
+        if (lane == 0) {
+          ok = mbar_wait(&tfull_bar[buf], (local >> 1) & 1, abort_flag);
+          // the previous unit's sums have been read
+          if (ok && c0 == kb0)
+            ok = mbar_wait_cluster(rempty_bar, (mine & 1) ^ 1, abort_flag);
         }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&tempty_bar[buf]);
-      if (split > 1) {
-        // this warp's partials are written: tell every CTA of the cluster
-        if (lane < split) mbar_arrive_cluster(mapa_shared(smem_u32(rfull_bar), lane));
-        if (lane == 0) ok = mbar_wait_cluster(rfull_bar, local & 1, abort_flag);
-        if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-        // every lane reads the peers' buffers, so every lane acquires (the
-        // phase is complete and the next one needs this warp: no waiting)
-        while (!mbar_try_wait_cluster(smem_u32(rfull_bar), local & 1) && !*abort_flag) {}
-        for (int k = rank; k < t.rows; k += split) {
-          const uint32_t at = smem_u32(&red[k * FM + n]);
-          float z = 0.f;
-          for (int p = 0; p < split; ++p) z += ld_cluster_f32(mapa_shared(at, p));
-          few_out<GATED>(g, static_cast<long long>(t.row0) + k, c, z, bias);
-        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        tc_fence_after();
+        take_chain(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * TN, t.rows, c0 == kb0, red + tid);
+        tc_fence_before();
         __syncwarp();
-        if (lane < split) mbar_arrive_cluster(mapa_shared(smem_u32(rempty_bar), lane));
+        if (lane == 0) mbar_arrive(&tempty_bar[buf]);
       }
+      if (!joined) {      // every CTA of the cluster has its barriers
+        cluster_wait();
+        joined = true;
+      }
+      // The tile's sums are in shared memory, a CTA's part in each; tell
+      // every CTA of the cluster (split 1: this CTA's other warps), and wait
+      // for all.
+      __syncwarp();
+      if (ok) {
+        if (lane < split) mbar_arrive_cluster(mapa_shared(smem_u32(rfull_bar), lane));
+        if (lane == 0) ok = mbar_wait_cluster(rfull_bar, mine & 1, abort_flag);
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      // every lane reads what other warps wrote, so every lane acquires (the
+      // phase is complete and the next one needs this warp: no waiting)
+      while (!mbar_try_wait_cluster(smem_u32(rfull_bar), mine & 1) && !*abort_flag) {}
+      if (c < g.N) {
+        const float* src = red + (tid & 15) * 8;
+        const int step = 2 * FE * split;
+        // two tokens in flight
+        for (int k = rank + (tid >> 4) * split; k < t.rows; k += 2 * step) {
+          float z0[8], z1[8];
+          const bool two = k + step < t.rows;
+          sum8(src + k * FM, split, z0);
+          if (two) sum8(src + (k + step) * FM, split, z1);
+          few_out<GATED>(g, static_cast<long long>(t.row0) + k, c, bias, z0);
+          if (two) few_out<GATED>(g, static_cast<long long>(t.row0) + k + step, c, bias, z1);
+        }
+      }
+      __syncwarp();
+      if (lane < split) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(rempty_bar), lane));
     }
+    if (!joined) cluster_wait();
   }
 
   tc_fence_before();
-  // no CTA leaves while a peer may still read its partials or arrive on it
-  cluster_sync();
+  __syncwarp();
+  // no CTA leaves while a peer may still read its sums or arrive on it (what
+  // was read is in registers, and nobody reads the stores: relaxed)
+  cluster_arrive_relaxed();
+  cluster_wait();
   if (*abort_flag && threadIdx.x == 0) set_err(g.err, MOE_DEV_TIMEOUT);
   if (warp == 1) {
     tc_fence_after();
@@ -346,52 +456,76 @@ __global__ void __launch_bounds__(FT, FC<TN>::ctas)
 
 constexpr int kMaxDevices = 64;
 
+int split_index(int split) { return split == 1 ? 0 : split == 2 ? 1 : split == 4 ? 2 : 3; }
+
+void few_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute& at, int split) {
+  cfg.blockDim = dim3(FT);
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = split;
+  at.val.clusterDim.y = 1;
+  at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+}
+
+// Clusters of `split` CTAs, one an SM, that the device holds at once (a GPC's
+// SMs are not a multiple of 8: 152, 76, 36 and 15 for 1, 2, 4 and 8), found
+// once per device.  It sizes grids only; no cluster waits for another.
+int few_clusters(int split, int num_sms) {
+  static int known[kMaxDevices][4] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return num_sms / split;
+  int& k = known[dev][split_index(split)];
+  if (k == 0) {
+    auto kern = few_kernel<true, 16, false>;
+    const int smem = static_cast<int>(FC<16>::smem(1));
+    int n = 0;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at;
+    few_config(cfg, at, split);
+    cfg.gridDim = dim3(num_sms / split * split);
+    cfg.dynamicSmemBytes = smem;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(FC<16>::smem(MOE_MAX_EXPERTS))) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1)
+      n = num_sms / split;
+    k = n < 1 ? 1 : n;
+  }
+  return k;
+}
+
+long long few_units(int E, int M_cap, int N, int tn, bool ragged) {
+  const long long nt = (N + FM - 1) / FM;
+  // ragged: an upper bound over all ways the rows can lie
+  const long long tiles = ragged ? static_cast<long long>(M_cap) / tn + (E < M_cap ? E : M_cap)
+                                 : (static_cast<long long>(M_cap) + tn - 1) / tn;
+  return nt * tiles;
+}
+
 template <bool KN, int TN, bool GATED>
 cudaError_t few_t(const CUtensorMap& tw, const CUtensorMap& tx, const FewArgs& g, int split,
                   int num_sms, cudaStream_t s) {
   auto kern = few_kernel<KN, TN, GATED>;
   static_assert(FC<TN>::smem(MOE_MAX_EXPERTS) <= 227 * 1024, "shared memory of a CTA");
-  const size_t smem = FC<TN>::smem(g.E);
-  // clusters that fit at once with this shared memory, kept per device and
-  // split (it only sizes the grid: no cluster waits for another)
-  struct Fit {
-    size_t smem;
-    int clusters;
-  };
-  static Fit fit_of[kMaxDevices][4] = {};
+  static bool set[kMaxDevices] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(FT);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = split;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  Fit& known = fit_of[dev][split == 1 ? 0 : split == 2 ? 1 : split == 4 ? 2 : 3];
-  int fit = known.clusters;
-  if (known.smem != smem) {
+  if (!set[dev]) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(FC<TN>::smem(MOE_MAX_EXPERTS)));
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(num_sms / split * split);
-    cfg.dynamicSmemBytes = smem;
-    e = cudaOccupancyMaxActiveClusters(&fit, kern, &cfg);
-    if (e != cudaSuccess) return e;
-    if (fit < 1) fit = 1;
-    known = Fit{smem, fit};
+    set[dev] = true;
   }
-  const long long nt = (g.N + FM - 1) / FM;
-  const long long tiles = static_cast<long long>(g.M_cap) / TN + (g.E < g.M_cap ? g.E : g.M_cap);
-  const long long units = nt * (g.E == 1 ? (static_cast<long long>(g.M_cap) + TN - 1) / TN : tiles);
-  const long long clusters = units < fit ? units : fit;
-  cfg.gridDim = dim3(static_cast<unsigned>(clusters * split));
-  cfg.dynamicSmemBytes = smem;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at;
+  few_config(cfg, at, split);
+  cfg.stream = s;
+  const long long units = few_units(g.E, g.M_cap, g.N, TN, g.offsets != nullptr);
+  const long long fit = few_clusters(split, num_sms);
+  cfg.gridDim = dim3(static_cast<unsigned>((units < fit ? units : fit) * split));
+  cfg.dynamicSmemBytes = FC<TN>::smem(g.E);
   return cudaLaunchKernelEx(&cfg, kern, tw, tx, g);
 }
 
@@ -465,7 +599,7 @@ __device__ __forceinline__ void dz8(const uint4& z, const uint32_t* d, float (&o
     for (int i = 0; i < 4; ++i) {
       const float gr = (i & 1) ? bf16_hi(d[i >> 1]) : bf16_lo(d[i >> 1]);
       float p, dp;
-      gate_phi_dphi<ACT>(bf16_lo(zw[i]), p, dp);
+      linear_phi<ACT == MOE_ACT_GEGLU>(bf16_lo(zw[i]), p, dp);
       o[2 * i] = gr * bf16_hi(zw[i]) * dp;
       o[2 * i + 1] = gr * p;
     }
@@ -569,20 +703,30 @@ int dz_blocks_cap(int E, int M_cap) {
 
 }  // namespace
 
-FewPlan few_plan(int E, int M_cap, int K, int N, bool ragged, int num_sms) {
+FewPlan few_plan(int E, int M_cap, int K, int N, bool ragged, bool f32, int num_sms) {
   const long long active = ragged ? (E < M_cap ? E : M_cap) : 1;
   const long long avg = (M_cap + active - 1) / active;
   // 128 x 256 tiles of the grouped GEMM, when the rows are spread evenly
   const long long big = (avg + 127) / 128 * active * ((N + 255) / 256);
-  if (avg > 64 && big >= num_sms) return FewPlan{0, 0};
+  if (!f32 && avg > 64 && big >= num_sms) return FewPlan{0, 0};
   FewPlan p;
   const long long r = ragged ? 2 * avg : avg;
   p.tn = r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128;
-  const long long slots = static_cast<long long>(num_sms) * (p.tn <= 64 ? 2 : 1);
   const long long units = (avg + p.tn - 1) / p.tn * active * ((N + FM - 1) / FM);
-  p.split = 1;
-  while (p.split < MAX_SPLIT && units * p.split * 2 <= slots && K / FK >= 4 * p.split * 2)
-    p.split *= 2;
+  // The split: the fewest stages of any CTA, each split's rounds over the
+  // clusters that fit times its share of K and the join (about 6 stages'
+  // time); where K is short the join is not worth it
+  const long long kb = K / FK;
+  long long best = -1;
+  for (int split = 1; split <= MAX_SPLIT; split *= 2) {
+    if (split > 1 && kb < 4 * split) break;
+    const long long fit = few_clusters(split, num_sms);
+    const long long cost = (units + fit - 1) / fit * ((kb + split - 1) / split + (split > 1 ? 6 : 2));
+    if (best < 0 || cost < best) {
+      best = cost;
+      p.split = split;
+    }
+  }
   return p;
 }
 

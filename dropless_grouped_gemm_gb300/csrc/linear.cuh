@@ -26,12 +26,12 @@ struct FewArgs {
 
 // Tokens per tile of the few-row kernel (its maps' box rows) and how many
 // CTAs of a cluster share a tile's reduction, for a product of this size;
-// 0 tokens: the 128 x 256-tile kernel serves it.
+// 0 tokens: the 128 x 256-tile kernel serves it (bf16 outputs only).
 struct FewPlan {
   int tn;
   int split;
 };
-FewPlan few_plan(int E, int M_cap, int K, int N, bool ragged, int num_sms);
+FewPlan few_plan(int E, int M_cap, int K, int N, bool ragged, bool f32, int num_sms);
 
 // tw: the weights [E, K, N] with boxes of 64 columns x 64 rows (kn), or
 // [E, N, K] with 64 x 128 (nk); tx: a [M_cap, K] with 64 x plan.tn
