@@ -1203,11 +1203,12 @@ int moe_grouped_linear(const moe_bf16* a, const int32_t* offsets, int E, int M_c
   const bool kn = b_layout == MOE_B_KN;
   const int n_out = linear_gated(act) ? N / 2 : N;
   const bool f32 = out_type == MOE_TYPE_F32;
-  CUtensorMap tb;
-  if (kn ? !map_w(&tb, B, E, K, N, 64) : !map_w(&tb, B, E, N, K, 128)) return MOE_E_CUDA;
   const moe::FewPlan plan = moe::few_plan(E, M_cap, K, N, offsets != nullptr, f32, sms);
+  CUtensorMap tb;
+  if (kn ? !map_w(&tb, B, E, K, N, 64) : !map_w(&tb, B, E, N, K, plan.tn ? 64 : 128))
+    return MOE_E_CUDA;
   CUtensorMap ta;
-  if (!map_act(&ta, a, M_cap, K, plan.tn ? plan.tn : moe::kBM)) return MOE_E_CUDA;
+  if (!map_act(&ta, a, M_cap, K, plan.tn ? plan.x_rows : moe::kBM)) return MOE_E_CUDA;
   if (plan.tn) {
     moe::FewArgs g{};
     g.offsets = offsets; g.E = E; g.M_cap = M_cap; g.K = K; g.N = N; g.bias = bias; g.act = act;

@@ -15,11 +15,17 @@
 // in the order of the ranks, so reruns are bitwise identical and no
 // workspace, atomic or second launch is needed.
 //
+// A dense product with more tokens than 64 (a gate over a batch, a large
+// decode batch) is bound by what its stages keep in flight from L2 (about
+// 130 KB an SM, 1.3 us each way).  There two CTAs form a pair (2-SM MMAs,
+// tcgen05.mma.cta_group::2): 256 columns x 128 tokens, each CTA with its 128
+// columns of the weights and 64 of the tokens, 24 KB a stage instead of 32.
+//
 // The tensor cores add into their float32 accumulator with less than a
 // float32 addition's rounding, an error that grows with the number of
 // additions (K = 7168 in one chain: 3.7e-6 of the result, against 8e-7 for a
-// float32 product).  A float32 output therefore ends its chains after 1024
-// of K and adds them in shared memory.
+// float32 product).  A float32 output therefore ends its chains after 64
+// additions an accumulator and adds them in shared memory.
 //
 // Roles (192 threads, one CTA an SM, so that the stages can hold 130 to 200
 // KB of loads in flight): warp 0 TMA producer, warp 1 TMEM owner and MMA
@@ -41,15 +47,21 @@ constexpr int FK = 64;                // reduction elements per stage
 constexpr int W_BYTES = FM * FK * 2;  // 16 KB
 constexpr int W_BOX = 64 * FK * 2;    // a 64 (columns) x 64 (K) box
 constexpr int MAX_SPLIT = 8;
-constexpr int CHAIN = 1024 / FK;      // stages per accumulation chain, float32 output
+constexpr int PAIR_TN = 128;          // tokens of a pair's tile
+constexpr int CHAIN = 64;             // MMAs per accumulation chain, float32 output
 
-template <int TN>
+template <int TN, bool PAIR>
 struct FC {
-  static constexpr int x_bytes = TN * FK * 2;
+  static constexpr int x_rows = PAIR ? TN / 2 : TN;
+  static constexpr int x_bytes = x_rows * FK * 2;
   static constexpr int stage_bytes = W_BYTES + x_bytes;
-  static constexpr int stages = TN == 16 ? 11 : TN == 32 ? 9 : TN == 64 ? 7 : 4;
+  static constexpr int stages = PAIR ? 6 : TN == 16 ? 11 : TN == 32 ? 9 : TN == 64 ? 7 : 4;
   static constexpr int red_bytes = TN * FM * 4;   // the tile's float32 sums
-  static constexpr int tmem_cols = 2 * TN;   // two accumulators; a power of two >= 32
+  // accumulators that the MMAs of a stage take in turn, in two buffers: two
+  // double the float32 chains' length at the same error, so that they are
+  // drained half as often (8192 x 4096 x 4096: 300 -> 287 us)
+  static constexpr int nacc = TN == 128 ? 2 : 1;
+  static constexpr int tmem_cols = 2 * nacc * TN;   // 32 to 512, a power of two
   static constexpr size_t smem(int E) {
     return 1024 + static_cast<size_t>(stages) * stage_bytes + red_bytes + (2 * stages + 7) * 8 +
            16 + 2 * (E + 1) * 4;
@@ -62,10 +74,10 @@ struct FTile {
 
 // unit u -> tile: an expert's units run over its token tiles first, so that
 // consecutive units share their weights through L2.  Dense (no offsets): by
-// arithmetic alone.
-template <int TN>
+// arithmetic alone.  Pair: 256 columns, of which CTA sh has 128.
+template <int TN, bool PAIR>
 __device__ __forceinline__ FTile few_tile(const FewArgs& g, const int* s_off, const int* s_ts,
-                                          int u) {
+                                          int u, int sh) {
   int lo = 0, first = 0, rows = g.M_cap, at = 0;
   if (g.offsets != nullptr) {
     int hi = g.E - 1;
@@ -86,37 +98,37 @@ __device__ __forceinline__ FTile few_tile(const FewArgs& g, const int* s_off, co
   t.e = lo;
   t.row0 = first + ti * TN;
   t.rows = min(TN, rows - ti * TN);
-  t.n0 = ni * FM;
+  t.n0 = PAIR ? (2 * ni + sh) * FM : ni * FM;
   return t;
 }
 
-// 8 float32 values from the same place in each of the cluster's CTAs, added
-// in the order of the ranks (split 1: this CTA's own)
-__device__ __forceinline__ void sum8(const float* p, int split, float (&z)[8]) {
-  if (split == 1) {
-    const float4 a = *reinterpret_cast<const float4*>(p);
-    const float4 b = *reinterpret_cast<const float4*>(p + 4);
-    z[0] = a.x; z[1] = a.y; z[2] = a.z; z[3] = a.w;
-    z[4] = b.x; z[5] = b.y; z[6] = b.z; z[7] = b.w;
-    return;
-  }
+// 8 float32 values from the same place in each CTA of a split (ranks first,
+// first + stride, ...), loaded, then added in the order of the ranks
+template <int S>
+__device__ __forceinline__ void load8(const float* p, int first, int stride, float (&w)[S][8]) {
   const uint32_t at = smem_u32(p);
-  float w[MAX_SPLIT][8];
 #pragma unroll
-  for (int r = 0; r < MAX_SPLIT; ++r)
-    if (r < split) {
-      const uint32_t pa = mapa_shared(at, r);
+  for (int r = 0; r < S; ++r) {
+    if constexpr (S == 1) {
+      const float4 a = *reinterpret_cast<const float4*>(p);
+      const float4 b = *reinterpret_cast<const float4*>(p + 4);
+      w[0][0] = a.x; w[0][1] = a.y; w[0][2] = a.z; w[0][3] = a.w;
+      w[0][4] = b.x; w[0][5] = b.y; w[0][6] = b.z; w[0][7] = b.w;
+    } else {
+      const uint32_t pa = mapa_shared(at, first + r * stride);
       ld_cluster_v4(pa, w[r][0], w[r][1], w[r][2], w[r][3]);
       ld_cluster_v4(pa + 16, w[r][4], w[r][5], w[r][6], w[r][7]);
     }
+  }
+}
+template <int S>
+__device__ __forceinline__ void add8(const float (&w)[S][8], float (&z)[8]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) z[i] = w[0][i];
+  for (int i = 0; i < 8; ++i) {
+    z[i] = w[0][i];
 #pragma unroll
-  for (int r = 1; r < MAX_SPLIT; ++r)
-    if (r < split) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) z[i] += w[r][i];
-    }
+    for (int r = 1; r < S; ++r) z[i] += w[r][i];
+  }
 }
 
 __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
@@ -163,31 +175,58 @@ __device__ __forceinline__ void few_out(const FewArgs& g, long long row, int c, 
   }
 }
 
-// the accumulator columns of the tile's tokens of this thread's lane into its
+// the accumulators' columns of the tile's tokens of this thread's lane into its
 // column of the tile's sums (put, or added to what earlier chains left)
+template <int TN, int NACC>
 __device__ __forceinline__ void take_chain(uint32_t tb, int tokens, bool first, float* col) {
 #pragma unroll 1
   for (int t = 0; t < tokens; t += 16) {
-    uint32_t r[16];
-    tmem_ld16(tb + t, r);
+    uint32_t r[NACC][16];
+#pragma unroll
+    for (int a = 0; a < NACC; ++a) tmem_ld16(tb + a * TN + t, r[a]);
     tmem_wait_ld();
-    if (first) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) col[(t + i) * FM] = __uint_as_float(r[i]);
-    } else {
+    for (int i = 0; i < 16; ++i) {
+      float v = first ? 0.f : col[(t + i) * FM];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) col[(t + i) * FM] += __uint_as_float(r[i]);
+      for (int a = 0; a < NACC; ++a) v += __uint_as_float(r[a][i]);
+      col[(t + i) * FM] = v;
     }
   }
 }
 
-template <bool KN, int TN, bool GATED>
+// the output pass of one tile for a split over S CTAs: a thread takes 8
+// neighbouring columns from c of a token, 16 threads a token, tokens rank,
+// rank + S, ...; as many tokens' loads in flight as 64 registers hold
+template <bool GATED, int S>
+__device__ __forceinline__ void few_store(const FewArgs& g, const FTile& t, const float* src,
+                                          int k0, int c, const uint4& bias, int first, int stride) {
+  constexpr int U = S <= 2 ? 4 : S == 4 ? 2 : 1;
+  constexpr int STEP = 2 * FE * S;
+#pragma unroll 1
+  for (int k = k0; k < t.rows; k += U * STEP) {
+    float w[U][S][8];
+#pragma unroll
+    for (int b = 0; b < U; ++b)
+      if (k + b * STEP < t.rows) load8<S>(src + (k + b * STEP) * FM, first, stride, w[b]);
+#pragma unroll
+    for (int b = 0; b < U; ++b)
+      if (k + b * STEP < t.rows) {
+        float z[8];
+        add8<S>(w[b], z);
+        few_out<GATED>(g, static_cast<long long>(t.row0) + k + b * STEP, c, bias, z);
+      }
+  }
+}
+
+template <bool KN, int TN, bool GATED, bool PAIR>
 __global__ void __launch_bounds__(FT, 1)
     few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                const FewArgs g) {
-  using C = FC<TN>;
+  using C = FC<TN, PAIR>;
   constexpr int NST = C::stages;
-  constexpr uint32_t IDESC = idesc_bf16(FM, TN, KN, false);
+  constexpr int SH = PAIR ? 2 : 1;
+  constexpr uint32_t IDESC = idesc_bf16(SH * FM, TN, KN, false);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -206,27 +245,36 @@ __global__ void __launch_bounds__(FT, 1)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int split = static_cast<int>(cluster_nctarank());
-  const int rank = static_cast<int>(cluster_ctarank());
-  const int unit0 = blockIdx.x / split;
-  const int unit_step = gridDim.x / split;
-  const int nt = (g.N + FM - 1) / FM;
+  // the cluster: split parts of K, each a CTA or a pair
+  const int csize = static_cast<int>(cluster_nctarank());
+  const int crank = static_cast<int>(cluster_ctarank());
+  const int split = csize / SH;
+  const int sh = crank % SH;
+  const int rank = crank / SH;
+  const uint16_t pair = static_cast<uint16_t>(3u << (crank - sh));   // both CTAs of the pair
+  const int unit0 = blockIdx.x / csize;
+  const int unit_step = gridDim.x / csize;
+  const int nt = (g.N + SH * FM - 1) / (SH * FM);
   const int kblocks = g.K / FK;
   const int kb0 = static_cast<int>(static_cast<long long>(kblocks) * rank / split);
   const int kb1 = static_cast<int>(static_cast<long long>(kblocks) * (rank + 1) / split);
-  const int chain = g.out_f32 != nullptr ? CHAIN : kblocks;
+  const int chain = g.out_f32 != nullptr ? CHAIN * C::nacc / (FK / 16) : kblocks;   // in stages
 
+  // a pair's bytes all count on its first CTA's barrier
+  const uint32_t full0 = PAIR ? mapa_shared(smem_u32(full_bar), crank - sh) : 0u;
   auto load = [&](const FTile& t, int kb, int stage) {
     uint8_t* sw = smem + stage * C::stage_bytes;
     uint64_t* fb = &full_bar[stage];
-    mbar_arrive_expect_tx(fb, C::stage_bytes);
-    if constexpr (KN) {
-      tma_load_3d(sw, &tmW, fb, t.n0, kb * FK, t.e);
-      tma_load_3d(sw + W_BOX, &tmW, fb, t.n0 + 64, kb * FK, t.e);
-    } else {
-      tma_load_3d(sw, &tmW, fb, kb * FK, t.n0, t.e);
+    const uint32_t fbc = full0 + stage * 8;
+    if (!PAIR || sh == 0) mbar_arrive_expect_tx(fb, SH * C::stage_bytes);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {     // 64 of the CTA's columns each
+      const int x = KN ? t.n0 + 64 * h : kb * FK, y = KN ? kb * FK : t.n0 + 64 * h;
+      if constexpr (PAIR) tma_load_3d_pair(sw + h * W_BOX, &tmW, fbc, x, y, t.e);
+      else tma_load_3d(sw + h * W_BOX, &tmW, fb, x, y, t.e);
     }
-    tma_load_2d(sw + W_BYTES, &tmX, fb, kb * FK, t.row0);
+    if constexpr (PAIR) tma_load_2d_pair(sw + W_BYTES, &tmX, fbc, kb * FK, t.row0 + C::x_rows * sh);
+    else tma_load_2d(sw + W_BYTES, &tmX, fb, kb * FK, t.row0);
   };
   int ahead = 0;      // stages of the first unit that are already loading
 
@@ -237,7 +285,7 @@ __global__ void __launch_bounds__(FT, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull_bar[i], 1);
-      mbar_init(&tempty_bar[i], FE);
+      mbar_init(&tempty_bar[i], SH * FE);   // a pair's first CTA issues for both
     }
     mbar_init(rfull_bar, FE * split);
     mbar_init(rempty_bar, FE * split);
@@ -245,12 +293,15 @@ __global__ void __launch_bounds__(FT, 1)
     *abort_flag = 0;
     fence_mbar_init();
     // dense: the first unit is known, so its loads start before anything else
-    if (g.offsets == nullptr && unit0 < nt * ((g.M_cap + TN - 1) / TN)) {
-      const FTile t = few_tile<TN>(g, nullptr, nullptr, unit0);
+    if (!PAIR && g.offsets == nullptr && unit0 < nt * ((g.M_cap + TN - 1) / TN)) {
+      const FTile t = few_tile<TN, PAIR>(g, nullptr, nullptr, unit0, sh);
       for (; ahead < NST && kb0 + ahead < kb1; ++ahead) load(t, kb0 + ahead, ahead);
     }
   }
-  if (warp == 1) tmem_alloc(tmem_slot, C::tmem_cols);
+  if (warp == 1) {
+    if constexpr (PAIR) tmem_alloc_pair(tmem_slot, C::tmem_cols);
+    else tmem_alloc(tmem_slot, C::tmem_cols);
+  }
   if (warp == 2 && g.offsets != nullptr) {
     // offsets made safe (within [0, M_cap], non-decreasing, from 0) and the
     // experts' first units, 32 experts at a time
@@ -290,11 +341,14 @@ __global__ void __launch_bounds__(FT, 1)
   __syncthreads();
   tc_fence_after();
   // the peers' barriers are initialised before the epilogue arrives on them
-  // (it waits then; everything before runs ahead)
+  // (it waits then; everything before runs ahead), and before a pair's loads
+  // and commits
   cluster_arrive();
+  if constexpr (PAIR) cluster_wait();
 
   const uint32_t tmem_base = *tmem_slot;
-  const int units = g.offsets != nullptr ? s_ts[g.E] : nt * ((g.M_cap + TN - 1) / TN);
+  const int units =
+      g.offsets != nullptr ? s_ts[g.E] : nt * ((g.M_cap + TN - 1) / TN);
 
   if (warp == 0) {
     if (lane == 0) {
@@ -304,7 +358,7 @@ __global__ void __launch_bounds__(FT, 1)
       uint32_t used = 0, parity = 0;    // stages loaded so far, and their phases
       for (int i = 0; i < ahead; ++i) used |= 1u << i;
       for (int u = unit0; u < units && ok; u += unit_step) {
-        const FTile t = few_tile<TN>(g, s_off, s_ts, u);
+        const FTile t = few_tile<TN, PAIR>(g, s_off, s_ts, u, sh);
         for (int kb = kb0; kb < kb1; ++kb) {
           if (ahead > 0) {
             --ahead;
@@ -318,9 +372,15 @@ __global__ void __launch_bounds__(FT, 1)
         }
       }
       if (!ok) {
-        // give up: wait (bounded) for the copies in flight
+        // give up: wait (bounded) for the copies in flight (a pair's second
+        // CTA, whose bytes count on the first one's barriers, waits 1 ms, far
+        // longer than a copy takes)
+        if (PAIR && sh != 0) {
+          const uint64_t t0 = globaltimer_ns();
+          while (globaltimer_ns() - t0 < 1000000ull) {}
+        }
         for (int i = 0; i < NST; ++i)
-          if ((used >> i) & 1u) {
+          if (((used >> i) & 1u) && (!PAIR || sh == 0)) {
             const uint32_t a = smem_u32(&full_bar[i]);
             const uint64_t t0 = globaltimer_ns();
             while (!mbar_try_wait(a, (parity >> i) & 1u) && globaltimer_ns() - t0 < kWaitLimitNs) {}
@@ -328,9 +388,9 @@ __global__ void __launch_bounds__(FT, 1)
       }
     }
     __syncwarp();
-    cluster_wait();
+    if constexpr (!PAIR) cluster_wait();
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (lane == 0 && sh == 0) {      // a pair's first CTA issues for both
       int stage = 0;
       uint32_t phase = 0;
       int local = 0;                    // chains so far
@@ -338,9 +398,14 @@ __global__ void __launch_bounds__(FT, 1)
       for (int u = unit0; u < units && ok; u += unit_step) {
         for (int c0 = kb0; c0 < kb1 && ok; c0 += chain, ++local) {
           const int buf = local & 1;
-          if (!mbar_wait(&tempty_bar[buf], ((local >> 1) & 1) ^ 1, abort_flag)) { ok = false; break; }
+          const uint32_t tph = ((local >> 1) & 1) ^ 1;
+          if (!(PAIR ? mbar_wait_cluster(&tempty_bar[buf], tph, abort_flag)
+                     : mbar_wait(&tempty_bar[buf], tph, abort_flag))) {
+            ok = false;
+            break;
+          }
           tc_fence_after();
-          const uint32_t d = tmem_base + buf * TN;
+          const uint32_t d0 = tmem_base + buf * (C::nacc * TN);
           const int c1 = min(c0 + chain, kb1);
           for (int kb = c0; kb < c1; ++kb) {
             if (!mbar_wait(&full_bar[stage], phase, abort_flag)) { ok = false; break; }
@@ -352,31 +417,40 @@ __global__ void __launch_bounds__(FT, 1)
               const uint64_t wd = KN ? sdesc_sw128(w0 + kk * 2048, W_BOX, 1024)
                                      : sdesc_sw128(w0 + kk * 32, 16, 1024);
               const uint64_t xd = sdesc_sw128(x0 + kk * 32, 16, 1024);
-              umma_bf16(d, wd, xd, IDESC, (kb > c0 || kk > 0) ? 1u : 0u);
+              const uint32_t d = d0 + (kk % C::nacc) * TN;
+              const uint32_t add = (kb > c0 || kk >= C::nacc) ? 1u : 0u;
+              if constexpr (PAIR) umma_bf16_pair(d, wd, xd, IDESC, add);
+              else umma_bf16(d, wd, xd, IDESC, add);
             }
-            umma_commit(&empty_bar[stage]);
+            if constexpr (PAIR) umma_commit_pair_mask(&empty_bar[stage], pair);
+            else umma_commit(&empty_bar[stage]);
             if (++stage == NST) { stage = 0; phase ^= 1; }
           }
-          if (ok) umma_commit(&tfull_bar[buf]);
+          if (ok) {
+            if constexpr (PAIR) umma_commit_pair_mask(&tfull_bar[buf], pair);
+            else umma_commit(&tfull_bar[buf]);
+          }
         }
       }
       if (!ok) {
         // give up: the MMAs already issued finish before TMEM is freed
-        umma_commit(drain_bar);
+        if constexpr (PAIR) umma_commit_pair(drain_bar);
+        else umma_commit(drain_bar);
         const uint32_t a = smem_u32(drain_bar);
         const uint64_t t0 = globaltimer_ns();
         while (!mbar_try_wait(a, 0) && globaltimer_ns() - t0 < kWaitLimitNs) {}
       }
     }
     __syncwarp();
-    cluster_wait();
+    if constexpr (!PAIR) cluster_wait();
   } else {
     const int q = warp & 3;                 // TMEM lane quadrant
     const int tid = q * 32 + lane;          // its column of the tile, then its place in the output pass
     int local = 0, mine = 0;                // chains and units so far
-    bool ok = true, joined = false;
+    bool ok = true, joined = PAIR;
+    const uint32_t tempty0 = PAIR ? mapa_shared(smem_u32(tempty_bar), crank - sh) : 0u;
     for (int u = unit0; u < units && ok; u += unit_step, ++mine) {
-      const FTile t = few_tile<TN>(g, s_off, s_ts, u);
+      const FTile t = few_tile<TN, PAIR>(g, s_off, s_ts, u, sh);
       // the output's part of the tile: a thread takes 8 neighbouring columns
       // of a token, 16 threads a token, tokens rank, rank + split, ...  What
       // it reads there is on its way while the tile is computed.
@@ -400,10 +474,15 @@ __global__ void __launch_bounds__(FT, 1)
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
         tc_fence_after();
-        take_chain(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * TN, t.rows, c0 == kb0, red + tid);
+        take_chain<TN, C::nacc>(
+            tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * (C::nacc * TN), t.rows,
+            c0 == kb0, red + tid);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&tempty_bar[buf]);
+        if (lane == 0) {
+          if (PAIR && sh != 0) mbar_arrive_cluster(tempty0 + buf * 8);
+          else mbar_arrive(&tempty_bar[buf]);
+        }
       }
       if (!joined) {      // every CTA of the cluster has its barriers
         cluster_wait();
@@ -414,7 +493,7 @@ __global__ void __launch_bounds__(FT, 1)
       // for all.
       __syncwarp();
       if (ok) {
-        if (lane < split) mbar_arrive_cluster(mapa_shared(smem_u32(rfull_bar), lane));
+        if (lane < split) mbar_arrive_cluster(mapa_shared(smem_u32(rfull_bar), lane * SH + sh));
         if (lane == 0) ok = mbar_wait_cluster(rfull_bar, mine & 1, abort_flag);
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -424,19 +503,17 @@ __global__ void __launch_bounds__(FT, 1)
       while (!mbar_try_wait_cluster(smem_u32(rfull_bar), mine & 1) && !*abort_flag) {}
       if (c < g.N) {
         const float* src = red + (tid & 15) * 8;
-        const int step = 2 * FE * split;
-        // two tokens in flight
-        for (int k = rank + (tid >> 4) * split; k < t.rows; k += 2 * step) {
-          float z0[8], z1[8];
-          const bool two = k + step < t.rows;
-          sum8(src + k * FM, split, z0);
-          if (two) sum8(src + (k + step) * FM, split, z1);
-          few_out<GATED>(g, static_cast<long long>(t.row0) + k, c, bias, z0);
-          if (two) few_out<GATED>(g, static_cast<long long>(t.row0) + k + step, c, bias, z1);
+        const int k0 = rank + (tid >> 4) * split;
+        switch (split) {
+          case 1: few_store<GATED, 1>(g, t, src, k0, c, bias, sh, SH); break;
+          case 2: few_store<GATED, 2>(g, t, src, k0, c, bias, sh, SH); break;
+          case 4: few_store<GATED, 4>(g, t, src, k0, c, bias, sh, SH); break;
+          default:
+            if constexpr (!PAIR) few_store<GATED, 8>(g, t, src, k0, c, bias, sh, SH);
         }
       }
       __syncwarp();
-      if (lane < split) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(rempty_bar), lane));
+      if (lane < split) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(rempty_bar), lane * SH + sh));
     }
     if (!joined) cluster_wait();
   }
@@ -450,7 +527,8 @@ __global__ void __launch_bounds__(FT, 1)
   if (*abort_flag && threadIdx.x == 0) set_err(g.err, MOE_DEV_TIMEOUT);
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, C::tmem_cols);
+    if constexpr (PAIR) tmem_dealloc_pair(tmem_base, C::tmem_cols);
+    else tmem_dealloc(tmem_base, C::tmem_cols);
   }
 }
 
@@ -468,7 +546,7 @@ void few_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute& at, int split) {
   cfg.numAttrs = 1;
 }
 
-// Clusters of `split` CTAs, one an SM, that the device holds at once (a GPC's
+// Clusters of `split` CTAs (any kernel's), one an SM, that the device holds at once (a GPC's
 // SMs are not a multiple of 8: 152, 76, 36 and 15 for 1, 2, 4 and 8), found
 // once per device.  It sizes grids only; no cluster waits for another.
 int few_clusters(int split, int num_sms) {
@@ -477,8 +555,8 @@ int few_clusters(int split, int num_sms) {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return num_sms / split;
   int& k = known[dev][split_index(split)];
   if (k == 0) {
-    auto kern = few_kernel<true, 16, false>;
-    const int smem = static_cast<int>(FC<16>::smem(1));
+    auto kern = few_kernel<true, 16, false, false>;
+    const int smem = static_cast<int>(FC<16, false>::smem(1));
     int n = 0;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at;
@@ -486,7 +564,7 @@ int few_clusters(int split, int num_sms) {
     cfg.gridDim = dim3(num_sms / split * split);
     cfg.dynamicSmemBytes = smem;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(FC<16>::smem(MOE_MAX_EXPERTS))) != cudaSuccess ||
+                             static_cast<int>(FC<16, false>::smem(MOE_MAX_EXPERTS))) != cudaSuccess ||
         cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1)
       n = num_sms / split;
     k = n < 1 ? 1 : n;
@@ -494,19 +572,20 @@ int few_clusters(int split, int num_sms) {
   return k;
 }
 
-long long few_units(int E, int M_cap, int N, int tn, bool ragged) {
-  const long long nt = (N + FM - 1) / FM;
+long long few_units(int E, int M_cap, int N, int tn, bool pair, bool ragged) {
+  const long long nt = (N + (pair ? 2 : 1) * FM - 1) / ((pair ? 2 : 1) * FM);
   // ragged: an upper bound over all ways the rows can lie
   const long long tiles = ragged ? static_cast<long long>(M_cap) / tn + (E < M_cap ? E : M_cap)
                                  : (static_cast<long long>(M_cap) + tn - 1) / tn;
   return nt * tiles;
 }
 
-template <bool KN, int TN, bool GATED>
+template <bool KN, int TN, bool GATED, bool PAIR>
 cudaError_t few_t(const CUtensorMap& tw, const CUtensorMap& tx, const FewArgs& g, int split,
                   int num_sms, cudaStream_t s) {
-  auto kern = few_kernel<KN, TN, GATED>;
-  static_assert(FC<TN>::smem(MOE_MAX_EXPERTS) <= 227 * 1024, "shared memory of a CTA");
+  using C = FC<TN, PAIR>;
+  auto kern = few_kernel<KN, TN, GATED, PAIR>;
+  static_assert(C::smem(MOE_MAX_EXPERTS) <= 227 * 1024, "shared memory of a CTA");
   static bool set[kMaxDevices] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -514,18 +593,19 @@ cudaError_t few_t(const CUtensorMap& tw, const CUtensorMap& tx, const FewArgs& g
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
   if (!set[dev]) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(FC<TN>::smem(MOE_MAX_EXPERTS)));
+                             static_cast<int>(C::smem(MOE_MAX_EXPERTS)));
     if (e != cudaSuccess) return e;
     set[dev] = true;
   }
+  constexpr int SH = PAIR ? 2 : 1;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute at;
-  few_config(cfg, at, split);
+  few_config(cfg, at, SH * split);
   cfg.stream = s;
-  const long long units = few_units(g.E, g.M_cap, g.N, TN, g.offsets != nullptr);
-  const long long fit = few_clusters(split, num_sms);
-  cfg.gridDim = dim3(static_cast<unsigned>((units < fit ? units : fit) * split));
-  cfg.dynamicSmemBytes = FC<TN>::smem(g.E);
+  const long long units = few_units(g.E, g.M_cap, g.N, TN, PAIR, g.offsets != nullptr);
+  const long long fit = few_clusters(SH * split, num_sms);
+  cfg.gridDim = dim3(static_cast<unsigned>((units < fit ? units : fit) * SH * split));
+  cfg.dynamicSmemBytes = C::smem(g.E);
   return cudaLaunchKernelEx(&cfg, kern, tw, tx, g);
 }
 
@@ -533,10 +613,12 @@ template <bool KN, bool GATED>
 cudaError_t few_tn(const CUtensorMap& tw, const CUtensorMap& tx, const FewArgs& g,
                    const FewPlan& p, int num_sms, cudaStream_t s) {
   switch (p.tn) {
-    case 16: return few_t<KN, 16, GATED>(tw, tx, g, p.split, num_sms, s);
-    case 32: return few_t<KN, 32, GATED>(tw, tx, g, p.split, num_sms, s);
-    case 64: return few_t<KN, 64, GATED>(tw, tx, g, p.split, num_sms, s);
-    case 128: return few_t<KN, 128, GATED>(tw, tx, g, p.split, num_sms, s);
+    case 16: return few_t<KN, 16, GATED, false>(tw, tx, g, p.split, num_sms, s);
+    case 32: return few_t<KN, 32, GATED, false>(tw, tx, g, p.split, num_sms, s);
+    case 64: return few_t<KN, 64, GATED, false>(tw, tx, g, p.split, num_sms, s);
+    case 128:
+      return p.pair ? few_t<KN, PAIR_TN, GATED, true>(tw, tx, g, p.split, num_sms, s)
+                    : few_t<KN, 128, GATED, false>(tw, tx, g, p.split, num_sms, s);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -703,31 +785,51 @@ int dz_blocks_cap(int E, int M_cap) {
 
 }  // namespace
 
+// The choice, by an estimate of the time in nanoseconds, with these measured
+// rates: a stage (64 of K) of a streaming tile takes its 16 KB of weights'
+// share of 6.6 TB/s and no less than 280 ns (an SM draws 60 KB/us from HBM),
+// a TN = 128 tile 330 ns, a pair's 310 ns; joining a split 2.5 us (TN = 128:
+// 5 us), ending a tile 1 us; a 128 x 256 tile of the grouped GEMM (256 rows
+// or more: a 256 x 256 one on two SMs) 290 ns a stage, or its 32 KB of
+// weights' share where no other tile reads them, and 4 us of start and end.
+// Dense, us, this kernel / the grouped GEMM: 64 x 4096 x 4096 17.7 / 37.4,
+// 512 x 4096 x 4096 28.7 / 30.0, 1024 x 4096 x 4096 47.5 / 30.7, 1024 x 7168 x
+// 2048 41.9 / 45.7; 8 experts, 4096 x 4096: 64 rows 51.6 / 54.6, 2048 rows
+// 93.2 / 59.4.  float32 outputs stay here for their accuracy.
 FewPlan few_plan(int E, int M_cap, int K, int N, bool ragged, bool f32, int num_sms) {
   const long long active = ragged ? (E < M_cap ? E : M_cap) : 1;
   const long long avg = (M_cap + active - 1) / active;
-  // 128 x 256 tiles of the grouped GEMM, when the rows are spread evenly
-  const long long big = (avg + 127) / 128 * active * ((N + 255) / 256);
-  if (!f32 && avg > 64 && big >= num_sms) return FewPlan{0, 0};
+  const long long kb = K / FK;
   FewPlan p;
   const long long r = ragged ? 2 * avg : avg;
   p.tn = r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128;
-  const long long units = (avg + p.tn - 1) / p.tn * active * ((N + FM - 1) / FM);
-  // The split: the fewest stages of any CTA, each split's rounds over the
-  // clusters that fit times its share of K and the join (about 6 stages'
-  // time); where K is short the join is not worth it
-  const long long kb = K / FK;
+  p.pair = !ragged && p.tn == PAIR_TN && N > FM;
+  const int sh = p.pair ? 2 : 1;
+  p.x_rows = p.tn / sh;
+  const long long units = (avg + p.tn - 1) / p.tn * active * ((N + sh * FM - 1) / (sh * FM));
   long long best = -1;
-  for (int split = 1; split <= MAX_SPLIT; split *= 2) {
+  for (int split = 1; split * sh <= MAX_SPLIT; split *= 2) {
     if (split > 1 && kb < 4 * split) break;
-    const long long fit = few_clusters(split, num_sms);
-    const long long cost = (units + fit - 1) / fit * ((kb + split - 1) / split + (split > 1 ? 6 : 2));
+    const long long fit = few_clusters(split * sh, num_sms);
+    const long long ctas = (units < fit ? units : fit) * split * sh;
+    long long stage = p.pair ? 310 : 330;
+    if (p.tn <= 64) stage = ctas * 16384 / 6600 < 280 ? 280 : ctas * 16384 / 6600;
+    const long long join = split == 1 ? 1000 : p.tn == 128 ? 5000 : 2500;
+    const long long cost = (units + fit - 1) / fit * ((kb + split - 1) / split * stage + join);
     if (best < 0 || cost < best) {
       best = cost;
       p.split = split;
     }
   }
-  return p;
+  if (f32) return p;
+  const bool two = avg >= 256;
+  const long long tiles = (avg + (two ? 255 : 127)) / (two ? 256 : 128) * active * ((N + 255) / 256);
+  const long long places = two ? num_sms / 2 : num_sms;
+  long long stage = 290;
+  if (avg <= 128 && (tiles < places ? tiles : places) * 32768 / 6600 > stage)
+    stage = (tiles < places ? tiles : places) * 32768 / 6600;
+  const long long big = (tiles + places - 1) / places * kb * stage + 4000;
+  return big < best ? FewPlan{} : p;
 }
 
 cudaError_t launch_few(const CUtensorMap& tw, const CUtensorMap& tx, bool kn, const FewArgs& g,

@@ -24,17 +24,20 @@ struct FewArgs {
   int32_t* err;
 };
 
-// Tokens per tile of the few-row kernel (its maps' box rows) and how many
-// CTAs of a cluster share a tile's reduction, for a product of this size;
-// 0 tokens: the 128 x 256-tile kernel serves it (bf16 outputs only).
+// How the few-row kernel serves a product of this size: tokens per tile (0:
+// it does not, the 128 x 256-tile kernel does; bf16 outputs only), how many
+// parts of K the CTAs of a cluster take, whether two CTAs form a pair over
+// 256 columns, and the rows of a's box that a CTA loads.
 struct FewPlan {
-  int tn;
-  int split;
+  int tn = 0;
+  int split = 1;
+  bool pair = false;
+  int x_rows = 0;
 };
 FewPlan few_plan(int E, int M_cap, int K, int N, bool ragged, bool f32, int num_sms);
 
-// tw: the weights [E, K, N] with boxes of 64 columns x 64 rows (kn), or
-// [E, N, K] with 64 x 128 (nk); tx: a [M_cap, K] with 64 x plan.tn
+// tw: the weights [E, K, N] (kn) or [E, N, K] (nk) with boxes of 64 columns x
+// 64 rows; tx: a [M_cap, K] with 64 x plan.x_rows
 cudaError_t launch_few(const CUtensorMap& tw, const CUtensorMap& tx, bool kn, const FewArgs& g,
                        const FewPlan& plan, int num_sms, cudaStream_t s);
 

@@ -372,6 +372,14 @@ __device__ __forceinline__ void umma_commit_pair_mc(uint64_t* bar) {
       "h"(static_cast<uint16_t>(0x3))
       : "memory");
 }
+// the same for the pair whose CTAs are in cta_mask (clusters of several pairs)
+__device__ __forceinline__ void umma_commit_pair_mask(uint64_t* bar, uint16_t cta_mask) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %1;" ::"r"(smem_u32(bar)),
+      "h"(cta_mask)
+      : "memory");
+}
 __device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(

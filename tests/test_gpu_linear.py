@@ -89,6 +89,7 @@ FEW = [
     (1, 17, 512, 320, "dense"),
     (1, 40, 640, 128, "dense"),
     (1, 129, 448, 256, "dense"),       # two token tiles of 128
+    (1, 300, 256, 192, "dense"),       # three token tiles: the last pair has one
     (1, 1000, 512, 256, "dense"),
     (6, 6, 512, 192, "ragged"),
     (9, 70, 256, 256, "ragged"),
