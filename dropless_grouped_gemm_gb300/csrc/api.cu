@@ -202,7 +202,7 @@ int check_mlp_sizes(int E, int M_cap, int d, int n) {
 int check_loss(int T, int E, int k, const int32_t* seg, int S, int type) {
   if (T < 0 || E < 1 || E > MOE_MAX_EXPERTS || k < 1 || k > E || S < 1 || S > moe::kMaxSegments)
     return MOE_E_SIZE;
-  if (static_cast<long long>(T) * k >= (1LL << 31)) return MOE_E_SIZE;
+  if (T > (1 << 30) || static_cast<long long>(T) * k >= (1LL << 31)) return MOE_E_SIZE;
   if (!seg && S != 1) return MOE_E_SIZE;
   if (type != MOE_TYPE_F32 && type != MOE_TYPE_BF16) return MOE_E_ARG;
   return MOE_OK;
@@ -214,6 +214,7 @@ int check_linear(const int32_t* offsets, int E, int M_cap, int K, int N, int b_l
   const int rc = check_mlp_sizes(E, M_cap, K, N);
   if (rc) return rc;
   if (static_cast<long long>(M_cap) * K >= (1LL << 40)) return MOE_E_SIZE;
+  if (K > (1 << 23) || N > (1 << 23) || M_cap > (1 << 30)) return MOE_E_SIZE;
   if (!offsets && E != 1) return MOE_E_SIZE;
   if (b_layout != MOE_B_KN && b_layout != MOE_B_NK) return MOE_E_ARG;
   if (act < MOE_ACT_SWIGLU || act > MOE_ACT_GELU) return MOE_E_ARG;

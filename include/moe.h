@@ -723,7 +723,7 @@ int moe_mx_quantize_tiled(const moe_bf16* src, int rows, int cols,
  * seg_offsets alone fix: reruns are bitwise identical.  NaN logits of a
  * valid token reach the losses.
  *   workspace: moe_router_loss_workspace_size(T, E, S) bytes, 16-byte
- *   aligned, not initialised.  1 <= S <= 4096.  Two launches.
+ *   aligned, not initialised.  1 <= S <= 4096, T <= 2^30.  Two launches.
  */
 size_t moe_router_loss_workspace_size(int T, int E, int S);
 int moe_router_loss(const void* logits, int logits_type, const int32_t* topk_idx, int T, int E,
@@ -767,7 +767,7 @@ int moe_router_loss_bwd(const void* logits, int logits_type, const int32_t* topk
  *   bf16 or NULL, may be `out` itself; z [M_cap, N] bf16 or NULL: the
  *   pre-activation, for the backward; out [M_cap, n_out], bf16 or float32
  *   (out_type).  Rows outside every expert are not written.  K, N multiples
- *   of 64; pointers 16-byte aligned.
+ *   of 64, at most 2^23; pointers 16-byte aligned.
  * Few rows (decoding: a token, or a few per expert; a gate's few columns)
  * run a kernel of their own that splits the reduction over a cluster of
  * CTAs; reruns are bitwise identical.  One launch (two where automatic pair

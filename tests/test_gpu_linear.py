@@ -277,3 +277,26 @@ def test_captures_into_a_graph_on_another_stream():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+def test_backward_captures_into_a_graph_on_another_stream():
+    import dropless_grouped_gemm_gb300 as M_
+    E, M, K, N = 3, 400, 128, 256
+    off = cuda_i32(_offsets("ragged", E, M, 4))
+    a, B, _, _ = _data(22, E, M, K, N, "swiglu", "kn", False, False)
+    z = W.normal((M, N), (22, W.X, 5), 1.5, "cuda")
+    dout = W.normal((M, N // 2), (22, W.DO, 0), 1.0, "cuda")
+    want = M_.grouped_linear_bwd(dout, a, off, B, "swiglu", z, True)
+    bufs = dict(zip(("dz", "da", "dB", "dbias", "err"), (torch.zeros_like(t) for t in want)))
+    ws = torch.full((M_.grouped_linear_bwd_workspace_size(E, M, N),), 0xFF, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=st):
+        M_.grouped_linear_bwd(dout, a, off, B, "swiglu", z, True, workspace=ws, **bufs)
+    for _ in range(2):
+        g.replay()
+    torch.cuda.synchronize()
+    for name, t in zip(bufs, want):
+        assert torch.equal(bufs[name], t), name
