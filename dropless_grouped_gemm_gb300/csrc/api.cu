@@ -164,6 +164,22 @@ bool map_w(CUtensorMap* m, const void* p, int E, int rows, int cols, int box_row
   return make_map(m, p, 3, dims, box, u8);
 }
 
+// [E, rows, cols] weights, cols a multiple of 64, seen as [E][cols / 64][rows]
+// [64]: one box of 2 x 64 columns x 64 rows, the two column groups one after
+// the other (128-byte swizzle: a group's rows are 128 bytes)
+bool map_w_groups(CUtensorMap* m, const void* p, int E, int rows, int cols) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(cols / 64),
+                              static_cast<cuuint64_t>(E)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(cols) * 2, 128,
+                                 static_cast<cuuint64_t>(rows) * cols * 2};
+  const cuuint32_t box[4] = {64, 64, 2, 1}, estr[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(p), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // [E, rows, cols] bf16 output written by staged TMA stores: box (64 cols,
 // 128-byte swizzle) or (32 cols, 64-byte swizzle) x 32 rows x 1
 bool map_out3(CUtensorMap* m, const void* p, int E, int rows, int cols, bool wide) {
@@ -1206,7 +1222,8 @@ int moe_grouped_linear(const moe_bf16* a, const int32_t* offsets, int E, int M_c
   const bool f32 = out_type == MOE_TYPE_F32;
   const moe::FewPlan plan = moe::few_plan(E, M_cap, K, N, offsets != nullptr, f32, sms);
   CUtensorMap tb;
-  if (kn ? !map_w(&tb, B, E, K, N, 64) : !map_w(&tb, B, E, N, K, plan.tn ? 64 : 128))
+  if (kn ? !(plan.tn ? map_w_groups(&tb, B, E, K, N) : map_w(&tb, B, E, K, N, 64))
+         : !map_w(&tb, B, E, N, K, 128))
     return MOE_E_CUDA;
   CUtensorMap ta;
   if (!map_act(&ta, a, M_cap, K, plan.tn ? plan.x_rows : moe::kBM)) return MOE_E_CUDA;

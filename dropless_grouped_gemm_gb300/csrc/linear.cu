@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(FT, 1)
   int* s_off = reinterpret_cast<int*>(tmem_slot + 4);
   int* s_ts = s_off + (g.E + 1);
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);   // (uniform to the compiler too)
   const int lane = threadIdx.x & 31;
   // the cluster: split parts of K, each a CTA or a pair
   const int csize = static_cast<int>(cluster_nctarank());
@@ -267,11 +267,13 @@ __global__ void __launch_bounds__(FT, 1)
     uint64_t* fb = &full_bar[stage];
     const uint32_t fbc = full0 + stage * 8;
     if (!PAIR || sh == 0) mbar_arrive_expect_tx(fb, SH * C::stage_bytes);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {     // 64 of the CTA's columns each
-      const int x = KN ? t.n0 + 64 * h : kb * FK, y = KN ? kb * FK : t.n0 + 64 * h;
-      if constexpr (PAIR) tma_load_3d_pair(sw + h * W_BOX, &tmW, fbc, x, y, t.e);
-      else tma_load_3d(sw + h * W_BOX, &tmW, fb, x, y, t.e);
+    // the weights' 16 KB in one load (KN: two groups of 64 columns)
+    if constexpr (KN) {
+      if constexpr (PAIR) tma_load_4d_pair(sw, &tmW, fbc, 0, kb * FK, t.n0 / 64, t.e);
+      else tma_load_4d(sw, &tmW, fb, 0, kb * FK, t.n0 / 64, t.e);
+    } else {
+      if constexpr (PAIR) tma_load_3d_pair(sw, &tmW, fbc, kb * FK, t.n0, t.e);
+      else tma_load_3d(sw, &tmW, fb, kb * FK, t.n0, t.e);
     }
     if constexpr (PAIR) tma_load_2d_pair(sw + W_BYTES, &tmX, fbc, kb * FK, t.row0 + C::x_rows * sh);
     else tma_load_2d(sw + W_BYTES, &tmX, fb, kb * FK, t.row0);
@@ -390,49 +392,65 @@ __global__ void __launch_bounds__(FT, 1)
     __syncwarp();
     if constexpr (!PAIR) cluster_wait();
   } else if (warp == 1) {
-    if (lane == 0 && sh == 0) {      // a pair's first CTA issues for both
+    // The whole warp walks the stages, one elected lane issues: with stage,
+    // addresses and descriptors warp-uniform the four MMAs of a stage cost
+    // few cycles to issue.  (Issued from a branch on the lane they took 330
+    // cycles, more than the MMAs themselves and, with the wait, than the
+    // stage's loads: 0.27 us a stage whatever the tile.)
+    if (sh == 0) {      // a pair's first CTA issues for both
       int stage = 0;
       uint32_t phase = 0;
       int local = 0;                    // chains so far
       bool ok = true;
+      bool ready = false;               // the stage was seen full ahead of its turn
+      const uint32_t w_lo0 = sdesc_lo(smem_u32(smem), KN ? W_BOX : 16);
+      const uint32_t x_lo0 = sdesc_lo(smem_u32(smem) + W_BYTES, 16);
       for (int u = unit0; u < units && ok; u += unit_step) {
         for (int c0 = kb0; c0 < kb1 && ok; c0 += chain, ++local) {
           const int buf = local & 1;
           const uint32_t tph = ((local >> 1) & 1) ^ 1;
-          if (!(PAIR ? mbar_wait_cluster(&tempty_bar[buf], tph, abort_flag)
-                     : mbar_wait(&tempty_bar[buf], tph, abort_flag))) {
-            ok = false;
-            break;
-          }
+          ok = __all_sync(0xffffffffu, PAIR ? mbar_wait_cluster(&tempty_bar[buf], tph, abort_flag)
+                                            : mbar_wait(&tempty_bar[buf], tph, abort_flag));
+          if (!ok) break;
           tc_fence_after();
           const uint32_t d0 = tmem_base + buf * (C::nacc * TN);
           const int c1 = min(c0 + chain, kb1);
           for (int kb = c0; kb < c1; ++kb) {
-            if (!mbar_wait(&full_bar[stage], phase, abort_flag)) { ok = false; break; }
-            tc_fence_after();
-            const uint32_t w0 = smem_u32(smem + stage * C::stage_bytes);
-            const uint32_t x0 = w0 + W_BYTES;
-#pragma unroll
-            for (int kk = 0; kk < FK / 16; ++kk) {
-              const uint64_t wd = KN ? sdesc_sw128(w0 + kk * 2048, W_BOX, 1024)
-                                     : sdesc_sw128(w0 + kk * 32, 16, 1024);
-              const uint64_t xd = sdesc_sw128(x0 + kk * 32, 16, 1024);
-              const uint32_t d = d0 + (kk % C::nacc) * TN;
-              const uint32_t add = (kb > c0 || kk >= C::nacc) ? 1u : 0u;
-              if constexpr (PAIR) umma_bf16_pair(d, wd, xd, IDESC, add);
-              else umma_bf16(d, wd, xd, IDESC, add);
+            if (!ready) {
+              ok = __all_sync(0xffffffffu, mbar_wait(&full_bar[stage], phase, abort_flag));
+              if (!ok) break;
             }
-            if constexpr (PAIR) umma_commit_pair_mask(&empty_bar[stage], pair);
-            else umma_commit(&empty_bar[stage]);
-            if (++stage == NST) { stage = 0; phase ^= 1; }
+            tc_fence_after();
+            // look at the next stage while this one's MMAs are issued
+            const int ns = stage + 1 == NST ? 0 : stage + 1;
+            const bool next = mbar_test(&full_bar[ns], ns == 0 ? phase ^ 1 : phase);
+            const uint32_t w_lo = w_lo0 + stage * (C::stage_bytes >> 4);
+            const uint32_t x_lo = x_lo0 + stage * (C::stage_bytes >> 4);
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < FK / 16; ++kk) {
+                const uint64_t wd = sdesc_of(w_lo + kk * (KN ? 2048 >> 4 : 32 >> 4));
+                const uint64_t xd = sdesc_of(x_lo + kk * (32 >> 4));
+                const uint32_t d = d0 + (kk % C::nacc) * TN;
+                const uint32_t add = (kb > c0 || kk >= C::nacc) ? 1u : 0u;
+                if constexpr (PAIR) umma_bf16_pair(d, wd, xd, IDESC, add);
+                else umma_bf16(d, wd, xd, IDESC, add);
+              }
+              if constexpr (PAIR) umma_commit_pair_mask(&empty_bar[stage], pair);
+              else umma_commit(&empty_bar[stage]);
+            }
+            ready = __all_sync(0xffffffffu, next);
+            stage = ns;
+            if (ns == 0) phase ^= 1;
           }
-          if (ok) {
+          if (ok && elect_one()) {
             if constexpr (PAIR) umma_commit_pair_mask(&tfull_bar[buf], pair);
             else umma_commit(&tfull_bar[buf]);
           }
+          __syncwarp();
         }
       }
-      if (!ok) {
+      if (!ok && elect_one()) {
         // give up: the MMAs already issued finish before TMEM is freed
         if constexpr (PAIR) umma_commit_pair(drain_bar);
         else umma_commit(drain_bar);
@@ -806,16 +824,15 @@ int dz_blocks_cap(int E, int M_cap) {
 }  // namespace
 
 // The choice, by an estimate of the time in nanoseconds, with these measured
-// rates: a stage (64 of K) of a streaming tile takes its 16 KB of weights'
-// share of 6.6 TB/s and no less than 280 ns (an SM draws 60 KB/us from HBM),
-// a TN = 128 tile 330 ns, a pair's 310 ns; joining a split 2.5 us (TN = 128:
-// 5 us), ending a tile 1 us; a 128 x 256 tile of the grouped GEMM (256 rows
-// or more: a 256 x 256 one on two SMs) 290 ns a stage, or its 32 KB of
-// weights' share where no other tile reads them, and 4 us of start and end.
-// Dense, us, this kernel / the grouped GEMM: 64 x 4096 x 4096 17.7 / 37.4,
-// 512 x 4096 x 4096 28.7 / 30.0, 1024 x 4096 x 4096 47.5 / 30.7, 1024 x 7168 x
-// 2048 41.9 / 45.7; 8 experts, 4096 x 4096: 64 rows 51.6 / 54.6, 2048 rows
-// 93.2 / 59.4.  float32 outputs stay here for their accuracy.
+// rates: a stage (64 of K) takes 220 ns, a TN = 128 tile's 260, a pair's 240,
+// and its 16 KB of weights' share of 6.6 TB/s where no other tile reads them;
+// joining a split 2.5 us (TN = 128: 5 us), ending a tile 1 us; a 128 x 256 tile
+// of the grouped GEMM (256 rows or more: a 256 x 256 one on two SMs) 290 ns a
+// stage, its 32 KB of weights' share of 5.6 TB/s, and 4 us of start and end.
+// Measured, us, this kernel / the grouped GEMM: dense 64 x 4096 x 4096
+// 14.4 / 37.4, 512 x 4096 x 4096 24.1 / 30.0, 1024 x 4096 x 4096 38.1 / 30.7,
+// 1024 x 7168 x 2048 33.9 / 45.7; 8 experts, 4096 x 4096: 64 rows 47.3 / 54.5,
+// 2048 rows 90.6 / 59.4.  float32 outputs stay here for their accuracy.
 FewPlan few_plan(int E, int M_cap, int K, int N, bool ragged, bool f32, int num_sms) {
   const long long active = ragged ? (E < M_cap ? E : M_cap) : 1;
   const long long avg = (M_cap + active - 1) / active;
@@ -832,8 +849,9 @@ FewPlan few_plan(int E, int M_cap, int K, int N, bool ragged, bool f32, int num_
     if (split > 1 && kb < 4 * split) break;
     const long long fit = few_clusters(split * sh, num_sms);
     const long long ctas = (units < fit ? units : fit) * split * sh;
-    long long stage = p.pair ? 310 : 330;
-    if (p.tn <= 64) stage = ctas * 16384 / 6600 < 280 ? 280 : ctas * 16384 / 6600;
+    long long stage = p.pair ? 240 : 260;
+    if (p.tn <= 64) stage = 220;
+    if (avg <= p.tn && ctas * 16384 / 6600 > stage) stage = ctas * 16384 / 6600;
     const long long join = split == 1 ? 1000 : p.tn == 128 ? 5000 : 2500;
     const long long cost = (units + fit - 1) / fit * ((kb + split - 1) / split * stage + join);
     if (best < 0 || cost < best) {
@@ -846,8 +864,8 @@ FewPlan few_plan(int E, int M_cap, int K, int N, bool ragged, bool f32, int num_
   const long long tiles = (avg + (two ? 255 : 127)) / (two ? 256 : 128) * active * ((N + 255) / 256);
   const long long places = two ? num_sms / 2 : num_sms;
   long long stage = 290;
-  if (avg <= 128 && (tiles < places ? tiles : places) * 32768 / 6600 > stage)
-    stage = (tiles < places ? tiles : places) * 32768 / 6600;
+  if (avg <= 128 && (tiles < places ? tiles : places) * 32768 / 5600 > stage)
+    stage = (tiles < places ? tiles : places) * 32768 / 5600;
   const long long big = (tiles + places - 1) / places * kb * stage + 4000;
   return big < best ? FewPlan{} : p;
 }
