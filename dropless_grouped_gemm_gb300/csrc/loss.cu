@@ -14,13 +14,12 @@
 //
 // Forward, two kernels.  loss_rows: a block takes one unit, up to `chunk`
 // consecutive tokens of one segment.  A group of L lanes (4 to 32, so that
-// each holds about 8 logits) takes a token, the next token's row loading
-// meanwhile, and keeps the sums of P of its experts in registers over its
-// tokens; the block adds its groups' sums in a fixed order and writes one
-// partial row per unit, so that no order depends on timing.  loss_finish,
-// launched programmatically behind it: adds the units of each segment in
-// order (a block per segment and slice of experts); the block that finishes last
-// adds the blocks' terms in order.  Backward: one kernel, a group of lanes
+// each holds 8 to 32 logits) takes a token and keeps the sums of P of its
+// experts in registers over its tokens; the block adds its groups' sums in a
+// fixed order and writes one partial row per unit, so that no order depends
+// on timing.  loss_finish, launched programmatically behind it: adds the
+// units of each segment in order (a block per segment and slice of experts);
+// the block that finishes last adds the blocks' terms in order.  Backward: one kernel, a group of lanes
 // per token, which reads each logit once and writes its gradient.
 // All are bound by HBM on long batches and by launch latency on short ones.
 #include <cuda_bf16.h>
@@ -43,13 +42,13 @@ struct Ws {
   int32_t* ticket;
 };
 
-// Tokens per unit: about one unit (a block of 16 warps) for each of the 456
-// places that 152 SMs have at three blocks each, a few left for segments that
+// Tokens per unit: about one unit (a block of 16 warps) for each of the 304
+// places that 152 SMs have at two blocks each, a few left for segments that
 // end inside a unit (a constant, so that the workspace size and the order of
 // the sums do not depend on the device queried).  65,536 tokens x 256 experts
-// in 16 sequences, forward as a whole: 26.2 us, against 28.9 with 608 units,
-// 31.5 with 1780 of 8 warps.
-constexpr int kUnits = 440;
+// in 16 sequences, forward as a whole: 22.0 us, against 25.9 with 440 units,
+// whose second wave is short.
+constexpr int kUnits = 300;
 int chunk_of(int T) {
   const int per = (T + kUnits - 1) / kUnits;
   const int c = (per + 15) / 16 * 16;
@@ -226,7 +225,7 @@ __device__ __forceinline__ float exp2_(float x) {
 constexpr float kLowest = -3.3895313892515355e38f;
 
 template <class T, int VEC, int NV, int L, int W>
-__global__ void __launch_bounds__(32 * W, NV <= 8 ? 3 : 1) loss_rows(const RouterLossArgs a, const Ws w, int chunk) {
+__global__ void __launch_bounds__(32 * W, NV <= 16 ? 2 : 1) loss_rows(const RouterLossArgs a, const Ws w, int chunk) {
   constexpr int G = 32 / L;                 // tokens of a warp at a time
   extern __shared__ float sm[];             // [W][E] sums, then [E] counts
   int32_t* hist = reinterpret_cast<int32_t*>(sm + W * a.E);
@@ -265,7 +264,7 @@ __global__ void __launch_bounds__(32 * W, NV <= 8 ? 3 : 1) loss_rows(const Route
   int nval = 0;
   bool bad_id = false;
   const T* logits = static_cast<const T*>(a.logits);
-  // a round is G tokens of each warp.  Loads are not staged ahead: with 48
+  // a round is G tokens of each warp.  Loads are not staged ahead: with 32
   // warps an SM, one warp's wait is covered by the others' arithmetic
   for (int tw = t0 + warp * G; tw < t1; tw += W * G) {
     const int t = tw + grp;
@@ -579,6 +578,7 @@ __global__ void __launch_bounds__(kBwdThreads) loss_bwd(const RouterLossArgs a, 
       // the group's row in shared memory: each pair leaves its number at its
       // expert and reads it back, so that an expert chosen twice shows; such
       // tokens (no router makes them) take their pairs one after another.
+      // (__match_any_sync in place of the numbers: 34.2 us against 31.7.)
       float* add = s_add + (warp * G + grp) * a.E;
       int* tag = reinterpret_cast<int*>(add);
       for (int j0 = 0; j0 < a.k; j0 += L) {
@@ -657,38 +657,53 @@ __global__ void __launch_bounds__(kBwdThreads) loss_bwd(const RouterLossArgs a, 
 }
 
 template <class T, int VEC, int NV, int L>
-cudaError_t go(const RouterLossArgs& a, int num_sms, cudaStream_t s, bool bwd, int chunk,
-               const Ws& w) {
-  if (bwd) {
-    // rounds of a warp: one while the SMs' 2048 threads are not full, then
-    // up to eight, whose tokens mostly share their segment's weights
-    constexpr int G = 32 / L, W = kBwdThreads / 32;
-    const long long waves = static_cast<long long>(num_sms) * 64 * G;
-    long long per = (a.T + waves - 1) / waves;
-    per = per < 1 ? 1 : (per > 8 ? 8 : per);
-    const long long blocks = (a.T + per * G * W - 1) / (per * G * W);
-    if (a.probs != nullptr)
-      loss_bwd<T, VEC, NV, L, true>
-          <<<static_cast<int>(blocks), kBwdThreads, static_cast<size_t>(W) * G * a.E * 4, s>>>(
-              a, static_cast<int>(per));   // at most 32 KB
-    else
-      loss_bwd<T, VEC, NV, L, false><<<static_cast<int>(blocks), kBwdThreads, 0, s>>>(a, static_cast<int>(per));
-  } else {
-    constexpr int W = NV <= 16 ? 16 : 8;    // [W][E] sums: at most 37 KB
-    const size_t smem = static_cast<size_t>(W + 1) * a.E * 4;
-    loss_rows<T, VEC, NV, L, W><<<units_cap(a.T, a.S), 32 * W, smem, s>>>(a, w, chunk);
-  }
+cudaError_t go_bwd(const RouterLossArgs& a, int num_sms, cudaStream_t s) {
+  // rounds of a warp: one while the SMs' 2048 threads are not full, then
+  // up to eight, whose tokens mostly share their segment's weights
+  constexpr int G = 32 / L, W = kBwdThreads / 32;
+  const long long waves = static_cast<long long>(num_sms) * 64 * G;
+  long long per = (a.T + waves - 1) / waves;
+  per = per < 1 ? 1 : (per > 8 ? 8 : per);
+  const long long blocks = (a.T + per * G * W - 1) / (per * G * W);
+  const int grid = static_cast<int>(blocks), rounds = static_cast<int>(per);
+  if (a.probs != nullptr)   // with a row of E terms for each group: at most 32 KB
+    loss_bwd<T, VEC, NV, L, true>
+        <<<grid, kBwdThreads, static_cast<size_t>(W) * G * a.E * 4, s>>>(a, rounds);
+  else
+    loss_bwd<T, VEC, NV, L, false><<<grid, kBwdThreads, 0, s>>>(a, rounds);
   return cudaGetLastError();
 }
+template <class T, int VEC, int NV, int L>
+cudaError_t go_fwd(const RouterLossArgs& a, cudaStream_t s, int chunk, const Ws& w) {
+  constexpr int W = NV <= 16 ? 16 : 8;    // [W][E] sums: at most 37 KB
+  const size_t smem = static_cast<size_t>(W + 1) * a.E * 4;
+  loss_rows<T, VEC, NV, L, W><<<units_cap(a.T, a.S), 32 * W, smem, s>>>(a, w, chunk);
+  return cudaGetLastError();
+}
+template <class T, int VEC, int NV, int L>
+cudaError_t go(const RouterLossArgs& a, int num_sms, cudaStream_t s, bool bwd, int chunk,
+               const Ws& w) {
+  return bwd ? go_bwd<T, VEC, NV, L>(a, num_sms, s) : go_fwd<T, VEC, NV, L>(a, s, chunk, w);
+}
 
-// lanes and values per lane: the smallest instance that covers E
+// Lanes and values per lane: the smallest instance that covers E.  The
+// forward, bound by its instructions, takes 16 values a lane and half the
+// lanes, which halves the shuffles and the per-token work (65,536 x 256: 26.4
+// -> 22.0 us); the backward, which also holds the counts, 8 (31.7 us, 33.9
+// with 16).
 template <class T, int VEC>
 cudaError_t pick(const RouterLossArgs& a, int num_sms, cudaStream_t s, bool bwd, int chunk,
                  const Ws& w) {
   if (a.E <= 32) return go<T, VEC, 8, 4>(a, num_sms, s, bwd, chunk, w);
-  if (a.E <= 64) return go<T, VEC, 8, 8>(a, num_sms, s, bwd, chunk, w);
-  if (a.E <= 128) return go<T, VEC, 8, 16>(a, num_sms, s, bwd, chunk, w);
-  if (a.E <= 256) return go<T, VEC, 8, 32>(a, num_sms, s, bwd, chunk, w);
+  if (bwd) {
+    if (a.E <= 64) return go_bwd<T, VEC, 8, 8>(a, num_sms, s);
+    if (a.E <= 128) return go_bwd<T, VEC, 8, 16>(a, num_sms, s);
+    if (a.E <= 256) return go_bwd<T, VEC, 8, 32>(a, num_sms, s);
+  } else {
+    if (a.E <= 64) return go_fwd<T, VEC, 16, 4>(a, s, chunk, w);
+    if (a.E <= 128) return go_fwd<T, VEC, 16, 8>(a, s, chunk, w);
+    if (a.E <= 256) return go_fwd<T, VEC, 16, 16>(a, s, chunk, w);
+  }
   if (a.E <= 512) return go<T, VEC, 16, 32>(a, num_sms, s, bwd, chunk, w);
   return go<T, VEC, 32, 32>(a, num_sms, s, bwd, chunk, w);
 }

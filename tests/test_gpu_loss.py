@@ -178,6 +178,26 @@ def test_unrouted_and_bad_ids_and_offsets():
         assert int(r["err"].item()) == M.DEV_BAD_OFFSETS, off
 
 
+@pytest.mark.parametrize("E,k", [(6, 4), (100, 12), (300, 40)])
+def test_an_expert_chosen_twice_gets_both_terms(E, k):
+    import dropless_grouped_gemm_gb300 as M
+    T = 37
+    _, zf, idx, _, _, p, dp = _inputs(13, T, E, k, 1, False, torch.float32)
+    idx[::3, 1] = idx[::3, 0]
+    idx[::5, 2:4] = idx[::5, :1]
+    z = zf.astype(np.float32)
+    ref = O.router_loss(z, idx)
+    r = M.router_loss(_cuda(z), cuda_i32(idx))
+    g = M.router_loss_bwd(_cuda(z), cuda_i32(idx), r, _cuda(np.ones(2, np.float32)), _cuda(p), _cuda(dp))
+    again = M.router_loss_bwd(_cuda(z), cuda_i32(idx), r, _cuda(np.ones(2, np.float32)), _cuda(p), _cuda(dp))
+    torch.cuda.synchronize()
+    assert r["counts"].cpu().tolist() == ref["counts"].tolist()
+    assert torch.equal(g, again)
+    want = O.router_loss_bwd(z, idx, [1.0, 1.0], p, dp)
+    # every term is below 4 in magnitude here, up to five add up
+    assert np.abs(g.cpu().numpy() - want).max() <= 96 * U * 20
+
+
 def test_no_tokens():
     import dropless_grouped_gemm_gb300 as M
     z = torch.empty((0, 16), device="cuda")
