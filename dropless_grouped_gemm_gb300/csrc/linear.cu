@@ -280,24 +280,30 @@ __global__ void __launch_bounds__(FT, 1)
   };
   int ahead = 0;      // stages of the first unit that are already loading
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < NST; ++i) {
-      mbar_init(&full_bar[i], 1);
-      mbar_init(&empty_bar[i], 1);
+  if (warp == 0) {
+    if (lane == 0) {
+      for (int i = 0; i < NST; ++i) {
+        mbar_init(&full_bar[i], 1);
+        mbar_init(&empty_bar[i], 1);
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&tfull_bar[i], 1);
+        mbar_init(&tempty_bar[i], SH * FE);   // a pair's first CTA issues for both
+      }
+      mbar_init(rfull_bar, FE * split);
+      mbar_init(rempty_bar, FE * split);
+      mbar_init(drain_bar, 1);
+      *abort_flag = 0;
+      fence_mbar_init();
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&tfull_bar[i], 1);
-      mbar_init(&tempty_bar[i], SH * FE);   // a pair's first CTA issues for both
-    }
-    mbar_init(rfull_bar, FE * split);
-    mbar_init(rempty_bar, FE * split);
-    mbar_init(drain_bar, 1);
-    *abort_flag = 0;
-    fence_mbar_init();
+    __syncwarp();
     // dense: the first unit is known, so its loads start before anything else
     if (!PAIR && g.offsets == nullptr && unit0 < nt * ((g.M_cap + TN - 1) / TN)) {
       const FTile t = few_tile<TN, PAIR>(g, nullptr, nullptr, unit0, sh);
-      for (; ahead < NST && kb0 + ahead < kb1; ++ahead) load(t, kb0 + ahead, ahead);
+      ahead = min(NST, kb1 - kb0);
+      if (elect_one())
+        for (int i = 0; i < ahead; ++i) load(t, kb0 + i, i);
+      __syncwarp();
     }
   }
   if (warp == 1) {
@@ -353,40 +359,46 @@ __global__ void __launch_bounds__(FT, 1)
       g.offsets != nullptr ? s_ts[g.E] : nt * ((g.M_cap + TN - 1) / TN);
 
   if (warp == 0) {
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      uint32_t used = 0, parity = 0;    // stages loaded so far, and their phases
-      for (int i = 0; i < ahead; ++i) used |= 1u << i;
-      for (int u = unit0; u < units && ok; u += unit_step) {
-        const FTile t = few_tile<TN, PAIR>(g, s_off, s_ts, u, sh);
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if (ahead > 0) {
-            --ahead;
-          } else {
-            if (!mbar_wait(&empty_bar[stage], phase ^ 1, abort_flag)) { ok = false; break; }
-            load(t, kb, stage);
-            used |= 1u << stage;
-            parity = (parity & ~(1u << stage)) | (phase << stage);
+    // the whole warp walks the stages, one elected lane issues (as the MMA
+    // warp does, and for the same reason)
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true, ready = false;
+    uint32_t issued = ahead;          // stages loaded so far
+    for (int u = unit0; u < units && ok; u += unit_step) {
+      const FTile t = few_tile<TN, PAIR>(g, s_off, s_ts, u, sh);
+      for (int kb = kb0; kb < kb1; ++kb) {
+        const int ns = stage + 1 == NST ? 0 : stage + 1;
+        if (ahead > 0) {
+          --ahead;
+        } else {
+          if (!ready) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&empty_bar[stage], phase ^ 1, abort_flag));
+            if (!ok) break;
           }
-          if (++stage == NST) { stage = 0; phase ^= 1; }
+          const bool next = mbar_test(&empty_bar[ns], ns == 0 ? phase : phase ^ 1);
+          if (elect_one()) load(t, kb, stage);
+          ready = __all_sync(0xffffffffu, next);
+          ++issued;
         }
+        stage = ns;
+        if (ns == 0) phase ^= 1;
       }
-      if (!ok) {
-        // give up: wait (bounded) for the copies in flight (a pair's second
-        // CTA, whose bytes count on the first one's barriers, waits 1 ms, far
-        // longer than a copy takes)
-        if (PAIR && sh != 0) {
+    }
+    if (!ok && elect_one()) {
+      // give up: wait (bounded) for the copies in flight, the last load of
+      // each stage (a pair's second CTA, whose bytes count on the first one's
+      // barriers, waits 1 ms, far longer than a copy takes)
+      if (PAIR && sh != 0) {
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 1000000ull) {}
+      } else {
+        for (uint32_t i = 0; i < NST && i < issued; ++i) {
+          const uint32_t last = issued - 1 - (issued - 1 - i) % NST;
+          const uint32_t a = smem_u32(&full_bar[i]);
           const uint64_t t0 = globaltimer_ns();
-          while (globaltimer_ns() - t0 < 1000000ull) {}
+          while (!mbar_try_wait(a, (last / NST) & 1u) && globaltimer_ns() - t0 < kWaitLimitNs) {}
         }
-        for (int i = 0; i < NST; ++i)
-          if (((used >> i) & 1u) && (!PAIR || sh == 0)) {
-            const uint32_t a = smem_u32(&full_bar[i]);
-            const uint64_t t0 = globaltimer_ns();
-            while (!mbar_try_wait(a, (parity >> i) & 1u) && globaltimer_ns() - t0 < kWaitLimitNs) {}
-          }
       }
     }
     __syncwarp();
