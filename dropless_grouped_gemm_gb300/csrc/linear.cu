@@ -16,16 +16,19 @@
 // workspace, atomic or second launch is needed.
 //
 // A dense product with more tokens than 64 (a gate over a batch, a large
-// decode batch) is bound by what its stages keep in flight from L2 (about
-// 130 KB an SM, 1.3 us each way).  There two CTAs form a pair (2-SM MMAs,
+// decode batch) has arithmetic to do.  There two CTAs form a pair (2-SM MMAs,
 // tcgen05.mma.cta_group::2): 256 columns x 128 tokens, each CTA with its 128
-// columns of the weights and 64 of the tokens, 24 KB a stage instead of 32.
+// columns of the weights and 64 of the tokens, 24 KB a stage instead of 32
+// (8192 x 4096 x 4096 float32: 221 us against 293 without pairs).
 //
 // The tensor cores add into their float32 accumulator with less than a
 // float32 addition's rounding, an error that grows with the number of
-// additions (K = 7168 in one chain: 3.7e-6 of the result, against 8e-7 for a
-// float32 product).  A float32 output therefore ends its chains after 64
-// additions an accumulator and adds them in shared memory.
+// additions (K = 7168 in one chain: 3.7e-6 of the result, against 8.4e-7 for
+// a float32 product).  A float32 output therefore ends its chains after 64
+// additions an accumulator and adds them in shared memory: 8.5e-7.  A stage's
+// MMAs take two accumulators in turn, which the epilogue adds: half as many
+// drains of these chains (221 us against 287 with one accumulator; bf16, 512
+// x 4096 x 4096, 23.4 against 24.4).
 //
 // Roles (192 threads, one CTA an SM, so that the stages can hold 130 to 200
 // KB of loads in flight): warp 0 TMA producer, warp 1 TMEM owner and MMA
@@ -48,6 +51,7 @@ constexpr int W_BYTES = FM * FK * 2;  // 16 KB
 constexpr int W_BOX = 64 * FK * 2;    // a 64 (columns) x 64 (K) box
 constexpr int MAX_SPLIT = 8;
 constexpr int PAIR_TN = 128;          // tokens of a pair's tile
+constexpr int NACC = 2;               // accumulators that a stage's MMAs take in turn
 constexpr int CHAIN = 64;             // MMAs per accumulation chain, float32 output
 
 template <int TN, bool PAIR>
@@ -57,11 +61,7 @@ struct FC {
   static constexpr int stage_bytes = W_BYTES + x_bytes;
   static constexpr int stages = PAIR ? 6 : TN == 16 ? 11 : TN == 32 ? 9 : TN == 64 ? 7 : 4;
   static constexpr int red_bytes = TN * FM * 4;   // the tile's float32 sums
-  // accumulators that the MMAs of a stage take in turn, in two buffers: two
-  // double the float32 chains' length at the same error, so that they are
-  // drained half as often (8192 x 4096 x 4096: 300 -> 287 us)
-  static constexpr int nacc = TN == 128 ? 2 : 1;
-  static constexpr int tmem_cols = 2 * nacc * TN;   // 32 to 512, a power of two
+  static constexpr int tmem_cols = 2 * NACC * TN;   // two buffers: 64 to 512, a power of two
   static constexpr size_t smem(int E) {
     return 1024 + static_cast<size_t>(stages) * stage_bytes + red_bytes + (2 * stages + 7) * 8 +
            16 + 2 * (E + 1) * 4;
@@ -177,7 +177,7 @@ __device__ __forceinline__ void few_out(const FewArgs& g, long long row, int c, 
 
 // the accumulators' columns of the tile's tokens of this thread's lane into its
 // column of the tile's sums (put, or added to what earlier chains left)
-template <int TN, int NACC>
+template <int TN>
 __device__ __forceinline__ void take_chain(uint32_t tb, int tokens, bool first, float* col) {
 #pragma unroll 1
   for (int t = 0; t < tokens; t += 16) {
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(FT, 1)
   const int kblocks = g.K / FK;
   const int kb0 = static_cast<int>(static_cast<long long>(kblocks) * rank / split);
   const int kb1 = static_cast<int>(static_cast<long long>(kblocks) * (rank + 1) / split);
-  const int chain = g.out_f32 != nullptr ? CHAIN * C::nacc / (FK / 16) : kblocks;   // in stages
+  const int chain = g.out_f32 != nullptr ? CHAIN * NACC / (FK / 16) : kblocks;   // in stages
 
   // a pair's bytes all count on its first CTA's barrier
   const uint32_t full0 = PAIR ? mapa_shared(smem_u32(full_bar), crank - sh) : 0u;
@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(FT, 1)
                                             : mbar_wait(&tempty_bar[buf], tph, abort_flag));
           if (!ok) break;
           tc_fence_after();
-          const uint32_t d0 = tmem_base + buf * (C::nacc * TN);
+          const uint32_t d0 = tmem_base + buf * (NACC * TN);
           const int c1 = min(c0 + chain, kb1);
           for (int kb = c0; kb < c1; ++kb) {
             if (!ready) {
@@ -443,8 +443,8 @@ __global__ void __launch_bounds__(FT, 1)
               for (int kk = 0; kk < FK / 16; ++kk) {
                 const uint64_t wd = sdesc_of(w_lo + kk * (KN ? 2048 >> 4 : 32 >> 4));
                 const uint64_t xd = sdesc_of(x_lo + kk * (32 >> 4));
-                const uint32_t d = d0 + (kk % C::nacc) * TN;
-                const uint32_t add = (kb > c0 || kk >= C::nacc) ? 1u : 0u;
+                const uint32_t d = d0 + (kk % NACC) * TN;
+                const uint32_t add = (kb > c0 || kk >= NACC) ? 1u : 0u;
                 if constexpr (PAIR) umma_bf16_pair(d, wd, xd, IDESC, add);
                 else umma_bf16(d, wd, xd, IDESC, add);
               }
@@ -504,8 +504,8 @@ __global__ void __launch_bounds__(FT, 1)
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
         tc_fence_after();
-        take_chain<TN, C::nacc>(
-            tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * (C::nacc * TN), t.rows,
+        take_chain<TN>(
+            tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * (NACC * TN), t.rows,
             c0 == kb0, red + tid);
         tc_fence_before();
         __syncwarp();
