@@ -242,8 +242,11 @@ def _need(t, dtype, name, ndim=None):
 _ERR_WORDS: dict = {}
 
 
-def _err_word(err, device):
+def _err_word(err, device, stream=None):
     if err is None:
+        if stream is not None and stream.cuda_stream != _current_stream():
+            with torch.cuda.stream(stream):     # zeroed in the call's own order
+                return _err_word(None, device)
         if torch.cuda.is_current_stream_capturing():
             return torch.zeros(1, dtype=torch.int32, device=device)
         words = _ERR_WORDS.setdefault((device, _current_stream()), [])
@@ -895,6 +898,14 @@ def activation_bwd(h, da, offsets, act: str = "swiglu", dh=None, stream=None):
 _TYPE = {torch.float32: 0, torch.bfloat16: 1}
 
 
+def _scratch(nbytes: int, device, stream):
+    """Workspace for one call, kept from reuse until the call's stream is past it."""
+    ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+    if stream is not None:
+        ws.record_stream(stream)
+    return ws
+
+
 def _float_type(t, name):
     if t not in _TYPE:
         raise MoeError(f"{name} must be torch.float32 or torch.bfloat16, got {t}")
@@ -938,10 +949,9 @@ def router_loss(logits: torch.Tensor, topk_idx: torch.Tensor, seg_offsets=None, 
         "lse": torch.empty(T, dtype=torch.float32, device=dev),
         "n_valid": torch.empty(S, dtype=torch.int32, device=dev),
     }
-    o["err"] = _err_word(err if err is not None else o.get("err"), dev)
+    o["err"] = _err_word(err if err is not None else o.get("err"), dev, stream)
     if workspace is None:
-        workspace = torch.empty(max(router_loss_workspace_size(T, E, S), 16), dtype=torch.uint8,
-                                device=dev)
+        workspace = _scratch(router_loss_workspace_size(T, E, S), dev, stream)
     rc = lib().moe_router_loss(_ptr(logits), lt, _ptr(topk_idx), T, E, k, _ptr(seg_offsets), S,
                                _ptr(token_mask), _ptr(o["loss"]), _ptr(o["counts"]),
                                _ptr(o["lse"]), _ptr(o["n_valid"]), _ptr(workspace),
@@ -1027,7 +1037,7 @@ def grouped_linear(a: torch.Tensor, offsets, B: torch.Tensor, act: str = "none",
         z = torch.empty((M_cap, N), dtype=torch.bfloat16, device=a.device)
     _need(z, torch.bfloat16, "z")
     _same_shape(z, (M_cap, N), "z")
-    err = _err_word(err, a.device)
+    err = _err_word(err, a.device, stream)
     rc = lib().moe_grouped_linear(_ptr(a), _ptr(offsets), E, M_cap, K, N, _ptr(B), layout,
                                   _ptr(bias), LINEAR_ACT[act], _ptr(residual), _ptr(z), _ptr(out),
                                   ot, _ptr(err), _stream(stream))
@@ -1074,9 +1084,8 @@ def grouped_linear_bwd(dout: torch.Tensor, a: torch.Tensor, offsets, B: torch.Te
         _need(t, ty, nm)
         _same_shape(t, shape, nm)
     if bias and workspace is None:
-        workspace = torch.empty(max(grouped_linear_bwd_workspace_size(E, M_cap, N), 16),
-                                dtype=torch.uint8, device=dev)
-    err = _err_word(err, dev)
+        workspace = _scratch(grouped_linear_bwd_workspace_size(E, M_cap, N), dev, stream)
+    err = _err_word(err, dev, stream)
     rc = lib().moe_grouped_linear_bwd(
         _ptr(dout), _ptr(z), _ptr(a), _ptr(offsets), E, M_cap, K, N, _ptr(B), layout,
         LINEAR_ACT[act], FLAG_ACCUMULATE_DW if accumulate_dw else 0, _ptr(dz), _ptr(da), _ptr(dB),
@@ -1172,7 +1181,7 @@ def grouped_mlp_fwd_ckpt(x_perm: torch.Tensor, offsets: torch.Tensor, W1: torch.
         y_perm = torch.empty((M_cap, d), dtype=torch.bfloat16, device=dev)
     _ckpt_args(h_q, h_s, "h")
     _same_shape(h_q, (M_cap, n1), "h_q")
-    err = _err_word(err, dev)
+    err = _err_word(err, dev, stream)
     rc = lib().moe_grouped_mlp_fwd_ckpt(_ptr(x_perm), _ptr(offsets), E, M_cap, d, n, _ptr(W1),
                                         _ptr(W2), ACT[act], _ptr(h_q), _ptr(h_s), _ptr(a),
                                         _ptr(y_perm), _ptr(err), _stream(stream))
@@ -1212,7 +1221,7 @@ def grouped_mlp_bwd_routed_ckpt(x_perm, h_q, h_s, do_perm, pair_of_row, probs, o
         dW1 = torch.empty((E, d, n1), dtype=bf, device=dev)
     if dW2 is None:
         dW2 = torch.empty((E, n, d), dtype=bf, device=dev)
-    err = _err_word(err, dev)
+    err = _err_word(err, dev, stream)
     rc = lib().moe_grouped_mlp_bwd_routed_ckpt(
         _ptr(x_perm), _ptr(h_q), _ptr(h_s), _ptr(do_perm), _ptr(pair_of_row), _ptr(probs),
         _ptr(offsets), E, M_cap, d, n, _ptr(W1), _ptr(W2), ACT[act], flags, _ptr(dh),

@@ -701,8 +701,8 @@ int moe_mx_quantize_tiled(const moe_bf16* src, int rows, int cols,
  * capacity nothing but training keeps the experts' loads even; the losses
  * themselves are the common ones, the pages do not fix them).
  *   logits      [T, E] float32 or bf16 (logits_type MOE_TYPE_*)
- *   topk_idx    [T, k] int32, as moe_router_topk writes it (-1: no route;
- *               other ids outside [0, E) are skipped and set
+ *   topk_idx    [T, k] int32, as moe_router_topk writes it (-1: no route; a
+ *               valid token's other ids outside [0, E) are skipped and set
  *               MOE_DEV_BAD_EXPERT)
  *   seg_offsets [S+1] int32 (device): sequence s is tokens
  *               [seg_offsets[s], seg_offsets[s+1]); starts at 0,

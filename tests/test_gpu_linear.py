@@ -279,6 +279,33 @@ def test_captures_into_a_graph_on_another_stream():
     assert torch.equal(out, want)
 
 
+def test_a_stream_of_its_own_without_waiting():
+    """Calls given a side stream while the current one is busy, with scratch
+    and error words of their own: the results of the current stream's calls."""
+    import dropless_grouped_gemm_gb300 as M_
+    E, M, K, N = 3, 400, 128, 256
+    off = cuda_i32(_offsets("ragged", E, M, 4))
+    a, B, b, _ = _data(23, E, M, K, N, "silu", "kn", True, False)
+    dout = W.normal((M, N), (23, W.DO, 0), 1.0, "cuda")
+    want, z, _ = M_.grouped_linear(a, off, B, "silu", b, save_z=True)
+    wb = M_.grouped_linear_bwd(dout, a, off, B, "silu", z, True)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    busy = torch.empty(1 << 26, device="cuda")
+    for _ in range(4):
+        busy.fill_(1.0)                                   # the current stream has work queued
+        got, _, err = M_.grouped_linear(a, off, B, "silu", b, z=z.clone(), stream=None)
+        st.wait_stream(torch.cuda.current_stream())
+        gb = M_.grouped_linear_bwd(dout, a, off, B, "silu", z, True, stream=st)
+        junk = torch.full((1 << 20,), float("nan"), device="cuda")   # would land in freed scratch
+        st.synchronize()
+        assert int(gb[-1].item()) == 0 and int(err.item()) == 0
+        assert torch.equal(got, want)
+        for x, y in zip(gb[:4], wb[:4]):
+            assert torch.equal(x, y)
+        del junk
+
+
 def test_backward_captures_into_a_graph_on_another_stream():
     import dropless_grouped_gemm_gb300 as M_
     E, M, K, N = 3, 400, 128, 256
