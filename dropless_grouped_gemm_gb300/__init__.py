@@ -249,10 +249,11 @@ def _err_word(err, device, stream=None):
                 return _err_word(None, device)
         if torch.cuda.is_current_stream_capturing():
             return torch.zeros(1, dtype=torch.int32, device=device)
-        words = _ERR_WORDS.setdefault((device, _current_stream()), [])
+        key = (device.index, _current_stream())
         try:
-            return words.pop()
-        except IndexError:
+            return _ERR_WORDS[key].pop()
+        except (KeyError, IndexError):
+            words = _ERR_WORDS.setdefault(key, [])
             words.extend(torch.zeros(64, dtype=torch.int32, device=device).split(1))
             return words.pop()
     _need(err, torch.int32, "err")
@@ -971,11 +972,13 @@ def router_loss_bwd(logits: torch.Tensor, topk_idx: torch.Tensor, fwd: dict, dlo
     gate's weight gradient)."""
     lt, T, E, k, S = _router_args(logits, topk_idx, seg_offsets, token_mask)
     if dlogits is None:
+        ot = _float_type(dtype or torch.float32, "dlogits")
         dlogits = torch.empty((T, E), dtype=dtype or torch.float32, device=logits.device)
-    ot = _float_type(dlogits.dtype, "dlogits")
-    _need(dlogits, dlogits.dtype, "dlogits", 2)
-    for t, ty, nm, shape in ((dlogits, dlogits.dtype, "dlogits", (T, E)),
-                             (dloss, torch.float32, "dloss", (2,)),
+    else:
+        ot = _float_type(dlogits.dtype, "dlogits")
+        _need(dlogits, dlogits.dtype, "dlogits", 2)
+        _same_shape(dlogits, (T, E), "dlogits")
+    for t, ty, nm, shape in ((dloss, torch.float32, "dloss", (2,)),
                              (probs, torch.float32, "probs", (T, k)),
                              (dprobs, torch.float32, "dprobs", (T, k)),
                              (fwd["lse"], torch.float32, "lse", (T,)),
@@ -1029,14 +1032,17 @@ def grouped_linear(a: torch.Tensor, offsets, B: torch.Tensor, act: str = "none",
         raise MoeError("bias must hold E*N values")
     _same_shape(residual, (M_cap, n_out), "residual")
     if out is None:
+        ot = _float_type(out_dtype, "out")
         out = torch.empty((M_cap, n_out), dtype=out_dtype, device=a.device)
-    ot = _float_type(out.dtype, "out")
-    _need(out, out.dtype, "out")
-    _same_shape(out, (M_cap, n_out), "out")
-    if save_z and z is None:
+    else:
+        ot = _float_type(out.dtype, "out")
+        _need(out, out.dtype, "out")
+        _same_shape(out, (M_cap, n_out), "out")
+    if z is not None:
+        _need(z, torch.bfloat16, "z")
+        _same_shape(z, (M_cap, N), "z")
+    elif save_z:
         z = torch.empty((M_cap, N), dtype=torch.bfloat16, device=a.device)
-    _need(z, torch.bfloat16, "z")
-    _same_shape(z, (M_cap, N), "z")
     err = _err_word(err, a.device, stream)
     rc = lib().moe_grouped_linear(_ptr(a), _ptr(offsets), E, M_cap, K, N, _ptr(B), layout,
                                   _ptr(bias), LINEAR_ACT[act], _ptr(residual), _ptr(z), _ptr(out),
@@ -1069,20 +1075,20 @@ def grouped_linear_bwd(dout: torch.Tensor, a: torch.Tensor, offsets, B: torch.Te
     if accumulate_dw and (dB is None or (bias and dbias is None)):
         raise ValueError("accumulate_dw needs the dB (and dbias) to accumulate into")
     dev = a.device
-    if act != "none" and dz is None:
-        dz = torch.empty((M_cap, N), dtype=torch.bfloat16, device=dev)
-    if da is None:
-        da = torch.empty((M_cap, K), dtype=torch.bfloat16, device=dev)
-    if dB is None:
-        dB = torch.empty_like(B)
-    if bias and dbias is None:
-        dbias = torch.empty((E, N), dtype=torch.float32, device=dev)
     for t, ty, nm, shape in ((dz, torch.bfloat16, "dz", (M_cap, N)),
                              (da, torch.bfloat16, "da", (M_cap, K)),
                              (dB, torch.bfloat16, "dB", tuple(B.shape)),
                              (dbias, torch.float32, "dbias", (E, N))):
         _need(t, ty, nm)
         _same_shape(t, shape, nm)
+    if act != "none" and dz is None:
+        dz = torch.empty((M_cap, N), dtype=torch.bfloat16, device=dev)
+    if da is None:
+        da = torch.empty((M_cap, K), dtype=torch.bfloat16, device=dev)
+    if dB is None:
+        dB = torch.empty(B.shape, dtype=torch.bfloat16, device=dev)
+    if bias and dbias is None:
+        dbias = torch.empty((E, N), dtype=torch.float32, device=dev)
     if bias and workspace is None:
         workspace = _scratch(grouped_linear_bwd_workspace_size(E, M_cap, N), dev, stream)
     err = _err_word(err, dev, stream)
@@ -1104,13 +1110,13 @@ def checkpoint_pack(src: torch.Tensor, q=None, s=None, stream=None):
     (both uint8).  Returns (q, s)."""
     _need(src, torch.bfloat16, "src", 2)
     rows, cols = src.shape
+    for t, nm, shape in ((q, "q", (rows, cols)), (s, "s", (rows, cols // 32))):
+        _need(t, torch.uint8, nm)
+        _same_shape(t, shape, nm)
     if q is None:
         q = torch.empty((rows, cols), dtype=torch.uint8, device=src.device)
     if s is None:
         s = torch.empty((rows, cols // 32), dtype=torch.uint8, device=src.device)
-    for t, nm, shape in ((q, "q", (rows, cols)), (s, "s", (rows, cols // 32))):
-        _need(t, torch.uint8, nm)
-        _same_shape(t, shape, nm)
     rc = lib().moe_checkpoint_pack(_ptr(src), rows, cols, _ptr(q), _ptr(s), _stream(stream))
     _check(rc, "moe_checkpoint_pack")
     return q, s

@@ -96,6 +96,7 @@ FEW = [
     (4, 200, 384, 128, "ragged"),
     (40, 700, 128, 64, "one"),         # 44 tiles of 16 in one expert
     (300, 64, 192, 128, "ragged"),     # most experts empty
+    (1024, 40, 64, 64, "ragged"),      # as many experts as there may be
 ]
 # the 128 x 256-tile kernel: ragged ends, pairs of CTAs and single ones
 BIG = [
