@@ -576,9 +576,9 @@ void few_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute& at, int split) {
   cfg.numAttrs = 1;
 }
 
-// Clusters of `split` CTAs (any kernel's), one an SM, that the device holds at once (a GPC's
-// SMs are not a multiple of 8: 152, 76, 36 and 15 for 1, 2, 4 and 8), found
-// once per device.  It sizes grids only; no cluster waits for another.
+// Clusters of `split` CTAs (any kernel's), one an SM, that the device holds at
+// once (a GPC's SMs are not a multiple of 8: 152, 76, 36 and 15 for 1, 2, 4 and
+// 8), found once per device.  It sizes grids only; no cluster waits for another.
 int few_clusters(int split, int num_sms) {
   static int known[kMaxDevices][4] = {};
   int dev = 0;

@@ -19,8 +19,9 @@
 // fixed order and writes one partial row per unit, so that no order depends
 // on timing.  loss_finish, launched programmatically behind it: adds the
 // units of each segment in order (a block per segment and slice of experts);
-// the block that finishes last adds the blocks' terms in order.  Backward: one kernel, a group of lanes
-// per token, which reads each logit once and writes its gradient.
+// the block that finishes last adds the blocks' terms in order.  Backward:
+// one kernel, a group of lanes per token, which reads each logit once and
+// writes its gradient.
 // All are bound by HBM on long batches and by launch latency on short ones.
 #include <cuda_bf16.h>
 
