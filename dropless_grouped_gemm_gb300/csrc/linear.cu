@@ -503,6 +503,7 @@ __global__ void __launch_bounds__(FT, 1)
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
+        __syncwarp();     // what lane 0 acquired orders every lane's writes
         tc_fence_after();
         take_chain<TN>(
             tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * (NACC * TN), t.rows,
@@ -542,18 +543,19 @@ __global__ void __launch_bounds__(FT, 1)
             if constexpr (!PAIR) few_store<GATED, 8>(g, t, src, k0, c, bias, sh, SH);
         }
       }
+      // this warp has read its peers' sums: the arrival releases the reads of
+      // all its lanes, after which the peers overwrite what was read
       __syncwarp();
-      if (lane < split) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(rempty_bar), lane * SH + sh));
+      if (lane < split) mbar_arrive_cluster(mapa_shared(smem_u32(rempty_bar), lane * SH + sh));
     }
     if (!joined) cluster_wait();
   }
 
   tc_fence_before();
   __syncwarp();
-  // no CTA leaves while a peer may still read its sums or arrive on it (what
-  // was read is in registers, and nobody reads the stores: relaxed)
-  cluster_arrive_relaxed();
-  cluster_wait();
+  // no CTA leaves while a peer may still read its sums or arrive on it: the
+  // arrival releases this thread's reads of and arrivals on its peers
+  cluster_sync();
   if (*abort_flag && threadIdx.x == 0) set_err(g.err, MOE_DEV_TIMEOUT);
   if (warp == 1) {
     tc_fence_after();
