@@ -210,9 +210,10 @@ __device__ __forceinline__ void load_row(const T* __restrict__ row, int E, int l
   }
 }
 
-// The softmax in base 2: e^(z - m) = 2^(z log2 e - m2) with m2 = m log2 e,
-// one fused multiply-add and one exponential per logit, and
-// lse = (m2 + log2 sum) ln 2, in which m2's rounding cancels.
+// The softmax in base 2: e^(z - m) = 2^((z - m) log2 e), the subtraction
+// first: it is exact where z and m are close, so that a row's offset, however
+// large, costs nothing (m log2 e, rounded, is off by 64 at m = 1e9 and past
+// float32 at 3e38).  lse = m + ln sum, rounded once.
 constexpr float kLog2E = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 __device__ __forceinline__ float exp2_(float x) {
@@ -285,15 +286,14 @@ __global__ void __launch_bounds__(32 * W, NV <= 16 ? 2 : 1) loss_rows(const Rout
     // has no weight at all (its lse^2 would overflow): with m = 0 every term
     // is 0 and lse = log 0; NaN goes through
     if (m <= kLowest) m = 0.f;
-    const float m2 = m * kLog2E;
     float tot = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      v[i] = exp2_(fmaf(v[i], kLog2E, -m2));
+      v[i] = exp2_((v[i] - m) * kLog2E);
       tot += v[i];
     }
     tot = group_sum<L>(tot);
-    const float lse = (m2 + log2f(tot)) * kLn2;
+    const float lse = fmaf(log2f(tot), kLn2, m);
     if (have && l == 0) a.lse[t] = lse;
     if (on && !(lse == -INFINITY)) {
       const float inv = __fdividef(1.0f, tot);
