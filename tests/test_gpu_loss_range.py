@@ -1,4 +1,5 @@
-"""Router losses over the whole range of the logits: rows far from zero.
+"""Router losses and their gradient over the whole range of the logits: rows
+far from zero.
 
 Tolerances, with u = 2^-24.  The exponents are 2^((v - m) log2 e): v - m is
 exact for values within a factor of two of each other and otherwise rounded
@@ -16,6 +17,10 @@ pytestmark = pytest.mark.gpu
 
 U = 2.0 ** -24
 LARGE = [-5e9, -1e10, -3e10, -1e11, -1e12, -1e20, -1e30, -3e38, 1e10, 1e11, 1e30, 3e38]
+
+
+def _cuda(a):
+    return None if a is None else torch.from_numpy(np.ascontiguousarray(a)).cuda()
 
 
 def _rows(E, seed=3):
@@ -67,3 +72,43 @@ def test_both_losses_with_rows_padded_by_a_large_value(v):
     assert r["counts"].cpu().tolist() == ref["counts"].tolist()
     got = r["loss"].cpu().numpy().astype(np.float64)
     assert np.all(np.abs(got - ref["loss"]) <= 512 * U * ref["loss"])
+
+
+@pytest.mark.parametrize("E,dtype", [(8, torch.float32), (60, torch.bfloat16), (64, torch.float32),
+                                     (200, torch.float32), (520, torch.float32), (1023, torch.float32)])
+def test_gradient_of_rows_of_large_logits(E, dtype):
+    import dropless_grouped_gemm_gb300 as M
+    k = 2
+    zt = torch.from_numpy(_rows(E)).to(dtype)
+    z = zt.double().numpy()
+    T = z.shape[0]
+    idx = np.argsort(-z, axis=1, kind="stable")[:, :k].astype(np.int32)
+    ref = O.router_loss(z, idx)
+    r = M.router_loss(zt.cuda(), cuda_i32(idx))
+    for dl in ([1.0, 0.0], [0.5, 0.25]):
+        dl = np.array(dl, np.float32)
+        g = M.router_loss_bwd(zt.cuda(), cuda_i32(idx), r, _cuda(dl)).cpu().numpy().astype(np.float64)
+        want = O.router_loss_bwd(z, idx, dl)
+        P, lse = O.ops._softmax(z)
+        w = dl[0] * E * ref["counts"][0] / (k * T * T)
+        mag = P * (w + (P * w).sum(axis=1, keepdims=True) + 2 * dl[1] * np.abs(lse[:, None]) / T)
+        assert np.all(np.abs(g - want) <= 256 * U * mag + 1e-38), dl
+
+
+@pytest.mark.parametrize("off", [0.0, 1e3, -1e4, 3e5])
+@pytest.mark.parametrize("E", [8, 60, 256, 1000])
+def test_gradient_does_not_depend_on_a_common_offset(E, off):
+    """Logits on a grid that the offset leaves exact: the same softmax."""
+    import dropless_grouped_gemm_gb300 as M
+    T, k = 70, 2
+    rng = np.random.default_rng(E)
+    z = (np.round(rng.standard_normal((T, E)) * 64) / 32 + off).astype(np.float32)
+    idx = np.argsort(-z, axis=1, kind="stable")[:, :k].astype(np.int32)
+    ref = O.router_loss(z, idx)
+    r = M.router_loss(_cuda(z), cuda_i32(idx))
+    dl = np.array([1.0, 0.0], np.float32)
+    g = M.router_loss_bwd(_cuda(z), cuda_i32(idx), r, _cuda(dl)).cpu().numpy().astype(np.float64)
+    P, _ = O.ops._softmax(z)
+    w = E * ref["counts"][0] / (k * T * T)
+    mag = P * (w + (P * w).sum(axis=1, keepdims=True))
+    assert np.all(np.abs(g - O.router_loss_bwd(z, idx, dl)) <= 256 * U * mag + 1e-38)
