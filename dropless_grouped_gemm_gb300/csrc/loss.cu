@@ -487,11 +487,18 @@ __global__ void __launch_bounds__(TH) loss_finish(const RouterLossArgs a, const 
   }
 }
 
-// largest s in [0, S] with start(s) <= t; seg may hold any values, so the
-// search is bounded by its index range alone
-__device__ __forceinline__ int segment_of(const int32_t* __restrict__ seg, int S, int t) {
+// The sequence of token t, as walk_segments lays them out: segment 0 begins
+// at 0, the others at the running maximum of the offsets.  Of non-decreasing
+// offsets (ordered) the last one at or below t, by bisection; else the one
+// before the first offset above t, one by one.
+__device__ __forceinline__ int segment_of(const int32_t* __restrict__ seg, int S, int t,
+                                          bool ordered) {
   if (seg == nullptr) return 0;
   int lo = 0, hi = S;
+  if (!ordered) {
+    while (lo < S && seg[lo + 1] <= t) ++lo;
+    return lo;
+  }
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (seg[mid] <= t) lo = mid;
@@ -514,10 +521,14 @@ __global__ void __launch_bounds__(kBwdThreads) loss_bwd(const RouterLossArgs a, 
   const long long first = (static_cast<long long>(blockIdx.x) * W + warp) * per_warp * G;
   const T* logits = static_cast<const T*>(a.logits);
   int n = 0;
-  for (int s = threadIdx.x; s < a.S; s += kBwdThreads) n += a.n_valid[s];
+  bool unordered = false;
+  for (int s = threadIdx.x; s < a.S; s += kBwdThreads) {
+    n += a.n_valid[s];
+    if (a.seg != nullptr && s > 0 && a.seg[s] > a.seg[s + 1]) unordered = true;
+  }
   n = __reduce_add_sync(0xffffffffu, n);
   if (lane == 0) s_part[warp] = n;
-  __syncthreads();
+  const bool ordered = !__syncthreads_or(unordered);
   n = 0;
 #pragma unroll
   for (int q = 0; q < W; ++q) n += s_part[q];
@@ -544,7 +555,7 @@ __global__ void __launch_bounds__(kBwdThreads) loss_bwd(const RouterLossArgs a, 
       dp = a.dprobs[p0 + l];
     }
     bool valid = !(lse == -INFINITY) && (a.mask == nullptr || a.mask[t] != 0);
-    const int s = segment_of(a.seg, a.S, t);
+    const int s = segment_of(a.seg, a.S, t, ordered);
     if (s != cur) {
       cur = s;
       const int ns = s < a.S ? a.n_valid[s] : 0;

@@ -1,5 +1,5 @@
 """Router losses and their gradient over the whole range of the logits: rows
-far from zero.
+far from zero, and sequence offsets that have to be corrected.
 
 Tolerances, with u = 2^-24.  The exponents are 2^((v - m) log2 e): v - m is
 exact for values within a factor of two of each other and otherwise rounded
@@ -112,3 +112,26 @@ def test_gradient_does_not_depend_on_a_common_offset(E, off):
     w = E * ref["counts"][0] / (k * T * T)
     mag = P * (w + (P * w).sum(axis=1, keepdims=True))
     assert np.all(np.abs(g - O.router_loss_bwd(z, idx, dl)) <= 256 * U * mag + 1e-38)
+
+
+@pytest.mark.parametrize("off", [[0, 30, 10, 50], [0, 60, 50, 50], [3, 20, 10, 40], [0, -4, 25, 50],
+                                 [0, 45, 0, 45, 0, 45, 50], [7, 3, 90, 12]])
+def test_gradient_takes_the_corrected_offsets(off):
+    """The forward clamps the offsets to [0, T], begins at 0 and takes their
+    running maximum; the gradient has to be that of the same sequences."""
+    import dropless_grouped_gemm_gb300 as M
+    T, E, k = 50, 24, 3
+    rng = np.random.default_rng(8)
+    z = rng.standard_normal((T, E)).astype(np.float32)
+    idx = np.argsort(-z, axis=1, kind="stable")[:, :k].astype(np.int32)
+    fixed = np.maximum.accumulate(np.clip([0] + off[1:], 0, T)).astype(np.int32)
+    dl = _cuda(np.array([1.0, 0.5], np.float32))
+    a = M.router_loss(_cuda(z), cuda_i32(idx), cuda_i32(fixed))
+    b = M.router_loss(_cuda(z), cuda_i32(idx), cuda_i32(off))
+    ga = M.router_loss_bwd(_cuda(z), cuda_i32(idx), a, dl, seg_offsets=cuda_i32(fixed))
+    gb = M.router_loss_bwd(_cuda(z), cuda_i32(idx), b, dl, seg_offsets=cuda_i32(off))
+    torch.cuda.synchronize()
+    assert int(a["err"].item()) == 0 and int(b["err"].item()) == M.DEV_BAD_OFFSETS
+    for n in ("loss", "counts", "n_valid", "lse"):
+        assert torch.equal(a[n], b[n]), n
+    assert torch.equal(ga, gb)
