@@ -311,23 +311,22 @@ __global__ void __launch_bounds__(FT, 1)
     else tmem_alloc(tmem_slot, C::tmem_cols);
   }
   if (warp == 2 && g.offsets != nullptr) {
-    // offsets made safe (within [0, M_cap], non-decreasing, from 0) and the
-    // experts' first units, 32 experts at a time
+    // offsets made safe (within [0, M_cap], non-decreasing by their running
+    // maximum, as in the grouped GEMM) and the experts' first units, 32
+    // experts at a time
     bool bad = false;
     int top = 0, carry = 0;
     for (int base = 0; base <= g.E; base += 32) {
       const int i = base + lane;
       const int raw = i <= g.E ? g.offsets[i] : 0;
-      int v = min(max(raw, 0), g.M_cap);
-      if (i == 0) v = 0;
-      int m = max(v, top);
+      int m = max(min(max(raw, 0), g.M_cap), top);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, m, o);
         if (lane >= o) m = max(m, y);
       }
       if (i <= g.E) {
-        if (m != raw) bad = true;
+        if (m != raw || (i == 0 && m != 0)) bad = true;
         s_off[i] = m;
       }
       // expert i - 1 ends at m
@@ -674,18 +673,36 @@ __device__ __forceinline__ int safe_off(const LinearDzArgs& g, int e) {
   return min(max(g.offsets[e], 0), g.M_cap);
 }
 
+// The rows [lo, hi) of expert x = 32 i + lane, for a warp that walks the
+// experts in order: the offsets clamped and by their running maximum, which
+// are the rows that the products take.  top: where the 32 before ended (the
+// first offset to begin with).
+__device__ __forceinline__ void expert_rows(const LinearDzArgs& g, int x, int& top, int& lo,
+                                            int& hi) {
+  const int lane = threadIdx.x & 31;
+  hi = max(x < g.E ? safe_off(g, x + 1) : 0, top);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, hi, o);
+    if (lane >= o) hi = max(hi, y);
+  }
+  lo = __shfl_up_sync(0xffffffffu, hi, 1);
+  if (lane == 0) lo = top;
+  top = __shfl_sync(0xffffffffu, hi, 31);
+}
+
 // the row block `b` of the ragged rows: expert e and rows [r0, r1); experts
 // are walked by one warp, 32 at a time
 __device__ __forceinline__ bool dz_block(const LinearDzArgs& g, int b, int& e, int& r0, int& r1) {
   const int lane = threadIdx.x & 31;
-  int carry = 0;
+  int carry = 0, top = safe_off(g, 0);
   for (int base = 0; base < g.E; base += 32) {
     const int x = base + lane;
-    const int lo = x < g.E ? safe_off(g, x) : 0;
-    const int hi = x < g.E ? max(safe_off(g, x + 1), lo) : 0;
+    int lo, hi;
+    expert_rows(g, x, top, lo, hi);
     // the grid's last block is past every row block, so it sees all experts
     if (b == g.blocks - 1 && g.offsets != nullptr && x < g.E &&
-        (g.offsets[x] != lo || g.offsets[x + 1] != hi || (x == 0 && lo != 0)))
+        (g.offsets[x + 1] != hi || (x == 0 && g.offsets[0] != 0)))
       set_err(g.err, MOE_DEV_BAD_OFFSETS);
     const int c = (hi - lo + kDzRows - 1) / kDzRows;
     int incl = c;
@@ -803,16 +820,18 @@ __global__ void __launch_bounds__(kDzThreads) dbias_sum(const LinearDzArgs g) {
   const int lane = threadIdx.x & 31, q = threadIdx.x >> 5;
   const int e = blockIdx.y, c = blockIdx.x * 32 + lane;
   if (q == 0) {
-    int n = 0, mine = 0;
-    for (int x = lane; x <= e; x += 32) {
-      const int lo = safe_off(g, x);
-      const int k = (max(safe_off(g, x + 1), lo) - lo + kDzRows - 1) / kDzRows;
+    int n = 0, mine = 0, top = safe_off(g, 0);
+    for (int base = 0; base <= e; base += 32) {
+      const int x = base + lane;
+      int lo, hi;
+      expert_rows(g, x, top, lo, hi);
+      const int k = (hi - lo + kDzRows - 1) / kDzRows;
       if (x < e) n += k;
-      else mine = k;
+      else if (x == e) mine = k;
     }
     n = __reduce_add_sync(0xffffffffu, n);
     mine = __reduce_add_sync(0xffffffffu, mine);
-    if (lane == 0) { s_b0 = n; s_b1 = min(n + mine, g.blocks); }
+    if (lane == 0) { s_b0 = n; s_b1 = n + mine; }
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");   // dz_kernel has ended
   __syncthreads();

@@ -760,8 +760,10 @@ int moe_router_loss_bwd(const void* logits, int logits_type, const int32_t* topk
  * GEMM's epilogue).  For the rows of each expert:
  *   z = a B_e + bias_e          (float32)
  *   out = act(z) + residual     (float32, rounded once)
- *   a [M_cap, K] bf16; offsets [E+1] as moe_grouped_gemm, or NULL with E = 1:
- *   all M_cap rows; B as moe_grouped_gemm (b_layout MOE_B_*); bias [E, N]
+ *   a [M_cap, K] bf16; offsets [E+1] as moe_grouped_gemm (from 0; else each is
+ *   clamped to [0, M_cap], their running maximum is taken, here and in the
+ *   backward, and MOE_DEV_BAD_OFFSETS is set), or NULL with E = 1: all M_cap
+ *   rows; B as moe_grouped_gemm (b_layout MOE_B_*); bias [E, N]
  *   bf16 or NULL; act any MOE_ACT_* (SWIGLU, GEGLU: columns 2j = gate,
  *   2j+1 = up, n_out = N / 2; the others: n_out = N); residual [M_cap, n_out]
  *   bf16 or NULL, may be `out` itself; z [M_cap, N] bf16 or NULL: the
