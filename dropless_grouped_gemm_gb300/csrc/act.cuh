@@ -65,7 +65,8 @@ __device__ __forceinline__ void linear_phi(float x, float& p, float& d) {
   } else {
     const float s = sigmoid_(2.0f * kGeluC * (x + kGeluA * x * x * x));
     p = x * s;
-    d = s + 2.0f * kGeluC * x * s * (1.0f - s) * (1.0f + 3.0f * kGeluA * x * x);
+    // (x^2 bounded: s (1 - s) is 0 long before, and 0 * inf is not)
+    d = s + 2.0f * kGeluC * x * s * (1.0f - s) * (1.0f + 3.0f * kGeluA * fminf(x * x, 1e30f));
   }
 }
 

@@ -1,10 +1,12 @@
-"""The linear operator where its offsets have to be corrected.  The forward's
-tolerance is that of its other tests: (K / 16 + 16) 2^-22 of the terms'
-magnitudes and half a bf16 step."""
+"""The linear operator where its offsets have to be corrected, and its
+activations' derivatives over bf16's whole range.  The forward's tolerance is
+that of its other tests: (K / 16 + 16) 2^-22 of the terms' magnitudes and half
+a bf16 step."""
 import numpy as np
 import pytest
 import torch
 
+import oracle as O
 import workloads as W
 from _helpers import cuda_i32, f64
 
@@ -75,3 +77,28 @@ def test_forward_corrects_bad_offsets_alike_in_both_kernels(M, K, N, dtype):
         mag = np.stack([np.abs(f64(a[r])) @ np.abs(f64(B[e])) + np.abs(f64(b[e])) for r, e in zip(rows, own)])
         got = out[rows].double().cpu().numpy()
         assert np.all(np.abs(got - want) <= (K / 16 + 16) * 2.0 ** -22 * mag + 2.0 ** -8 * np.abs(want))
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "swiglu", "geglu"])
+def test_derivatives_at_large_pre_activations(act):
+    """Where the sigmoid is 0 or 1 to the last bit, phi' is too (past 1.8e19,
+    z^2 is past float32).  Half a bf16 step, and the derivative's 2^-18 at the
+    last three values, doubled by dout."""
+    import dropless_grouped_gemm_gb300 as M_
+    vals = [1e2, 1e9, 1e13, 1e18, 1.7e19, 2e19, 1e20, 1e30, 3e38]
+    g = torch.tensor(vals + [-v for v in vals] + [0.0, 1.0, -1.0], device="cuda").bfloat16()
+    M = g.numel()
+    z = torch.full((M, 64), 0.5, dtype=torch.bfloat16, device="cuda")
+    gated = act in ("swiglu", "geglu")
+    z[:, ::2] = g[:, None]
+    if not gated:
+        z[:, 1::2] = g[:, None]
+    dout = torch.full((M, 32 if gated else 64), 2.0, dtype=torch.bfloat16, device="cuda")
+    a = torch.ones((M, 64), dtype=torch.bfloat16, device="cuda")
+    B = torch.zeros((64, 64), dtype=torch.bfloat16, device="cuda")
+    dz, _, _, _, _ = M_.grouped_linear_bwd(dout, a, None, B, act, z)
+    torch.cuda.synchronize()
+    near = O.dphi(np.array([0.0, 1.0, -1.0]), "swiglu" if act in ("silu", "swiglu") else "geglu")
+    d = 2.0 * (0.5 if gated else 1.0) * np.concatenate([np.ones(len(vals)), np.zeros(len(vals)), near])
+    got = f64(dz)[:, 0]
+    assert np.all(np.abs(got - d) <= 2.0 ** -8 * np.abs(d) + 2.0 ** -17), got
