@@ -65,8 +65,9 @@ __device__ __forceinline__ void linear_phi(float x, float& p, float& d) {
   } else {
     const float s = sigmoid_(2.0f * kGeluC * (x + kGeluA * x * x * x));
     p = x * s;
-    // (x^2 bounded: s (1 - s) is 0 long before, and 0 * inf is not)
-    d = s + 2.0f * kGeluC * x * s * (1.0f - s) * (1.0f + 3.0f * kGeluA * fminf(x * x, 1e30f));
+    // (x bounded: s (1 - s) is 0 long before, and 0 times an overflow is not)
+    const float y = fminf(fmaxf(x, -1e15f), 1e15f);
+    d = s + 2.0f * kGeluC * y * s * (1.0f - s) * (1.0f + 3.0f * kGeluA * y * y);
   }
 }
 
