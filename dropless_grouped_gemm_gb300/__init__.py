@@ -254,7 +254,8 @@ def _err_word(err, device, stream=None):
             return _ERR_WORDS[key].pop()
         except (KeyError, IndexError):
             words = _ERR_WORDS.setdefault(key, [])
-            words.extend(torch.zeros(64, dtype=torch.int32, device=device).split(1))
+            with torch.inference_mode(False):   # ordinary tensors: later calls get them too
+                words.extend(torch.zeros(64, dtype=torch.int32, device=device).split(1))
             return words.pop()
     _need(err, torch.int32, "err")
     return err
