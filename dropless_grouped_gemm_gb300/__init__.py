@@ -303,7 +303,7 @@ def route_offsets(topk_idx: torch.Tensor, E: int, align: int = 1, M_cap: int | N
         "pair_of_row": torch.empty(M_cap, dtype=torch.int32, device=dev),
         "true_total": torch.empty(1, dtype=torch.int32, device=dev),
     }
-    o["err"] = _err_word(err if err is not None else o.get("err"), dev)
+    o["err"] = _err_word(err if err is not None else o.get("err"), dev, stream)
     ws_bytes = route_workspace_size(T, k, E)
     if workspace is None:
         workspace = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=dev)
@@ -335,7 +335,7 @@ def route_logits(logits: torch.Tensor, k: int, align: int = 1, M_cap: int | None
         "pair_of_row": torch.empty(M_cap, dtype=torch.int32, device=dev),
         "true_total": torch.empty(1, dtype=torch.int32, device=dev),
     }
-    o["err"] = _err_word(err if err is not None else o.get("err"), dev)
+    o["err"] = _err_word(err if err is not None else o.get("err"), dev, stream)
     ws_bytes = route_workspace_size(T, k, E)
     if workspace is None:
         workspace = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=dev)
@@ -430,7 +430,7 @@ def grouped_mlp_fwd(x_perm: torch.Tensor, offsets: torch.Tensor, W1: torch.Tenso
         a = torch.empty((M_cap, n), dtype=torch.bfloat16, device=dev)
     if y_perm is None:
         y_perm = torch.empty((M_cap, d), dtype=torch.bfloat16, device=dev)
-    err = _err_word(err, dev)
+    err = _err_word(err, dev, stream)
     flags = FLAG_SAVE_H if save_h else 0
     mxs = None
     if mx is not None:
@@ -474,7 +474,7 @@ def grouped_mlp_fwd_gather(x: torch.Tensor, pair_of_row: torch.Tensor, k: int,
         a = torch.empty((M_cap, n), dtype=torch.bfloat16, device=dev)
     if y_perm is None:
         y_perm = torch.empty((M_cap, d), dtype=torch.bfloat16, device=dev)
-    err = _err_word(err, dev)
+    err = _err_word(err, dev, stream)
     if T == 0:      # the library reads nothing of x then, but needs an address
         x = torch.zeros((1, d), dtype=torch.bfloat16, device=dev)
     rc = lib().moe_grouped_mlp_fwd_gather(
@@ -516,7 +516,7 @@ def grouped_mlp_bwd(x_perm, h_saved, a, dy_perm, offsets, W1, W2, act: str = "sw
         dW1 = torch.empty((E, d, n1), dtype=torch.bfloat16, device=dev)
     if dW2 is None:
         dW2 = torch.empty((E, n, d), dtype=torch.bfloat16, device=dev)
-    err = _err_word(err, dev)
+    err = _err_word(err, dev, stream)
     rc = lib().moe_grouped_mlp_bwd(_ptr(x_perm), _ptr(h_saved), _ptr(a), _ptr(dy_perm),
                                    _ptr(offsets), E, M_cap, d, n, _ptr(W1), _ptr(W2), ACT[act], flags,
                                    _ptr(dh), _ptr(dx_perm), _ptr(dW1), _ptr(dW2), _ptr(amax),
@@ -583,7 +583,7 @@ def mx_quantize(src: torch.Tensor, offsets: torch.Tensor, transposed: bool = Tru
     s = torch.empty((rows, cols // 32), dtype=torch.uint8, device=dev)
     qT = torch.empty((cols, rows), dtype=torch.uint8, device=dev) if transposed else None
     sT = torch.empty((cols, rows // 32), dtype=torch.uint8, device=dev) if transposed else None
-    err = _err_word(err, dev)
+    err = _err_word(err, dev, stream)
     rc = lib().moe_mx_quantize(_ptr(src), rows, cols, _ptr(offsets), offsets.numel() - 1, _ptr(q),
                                _ptr(s), _ptr(qT), _ptr(sT), _ptr(err), _stream(stream))
     _check(rc, "moe_mx_quantize")
@@ -607,7 +607,7 @@ def mx_quantize_tiled(src: torch.Tensor, offsets: torch.Tensor, rowwise: bool = 
     s = torch.empty(rows * cols // 8, dtype=u8, device=dev) if rowwise else None
     qT = torch.empty((cols, rows), dtype=u8, device=dev) if transposed else None
     sT = torch.empty(rows * cols // 8, dtype=u8, device=dev) if transposed else None
-    err = _err_word(err, dev)
+    err = _err_word(err, dev, stream)
     rc = lib().moe_mx_quantize_tiled(_ptr(src), rows, cols, _ptr(offsets), offsets.numel() - 1,
                                      _ptr(q), _ptr(s), _ptr(qT), _ptr(sT), _ptr(err),
                                      _stream(stream))
@@ -701,7 +701,7 @@ def grouped_mlp_bwd_mx(x_perm, h_saved, dy_perm, offsets, mx: dict, act: str = "
         dW1 = torch.empty((E, d, n1), dtype=torch.bfloat16, device=dev)
     if dW2 is None:
         dW2 = torch.empty((E, n, d), dtype=torch.bfloat16, device=dev)
-    err = _err_word(err, dev)
+    err = _err_word(err, dev, stream)
     need = mx_bwd_workspace_size(M_cap, d, n, act)
     if workspace is None:
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
@@ -753,7 +753,7 @@ def grouped_mlp_bwd_routed(x_perm, h_saved, do_perm, pair_of_row, probs, offsets
         dW1 = torch.empty((E, d, n1), dtype=bf, device=dev)
     if dW2 is None:
         dW2 = torch.empty((E, n, d), dtype=bf, device=dev)
-    err = _err_word(err, dev)
+    err = _err_word(err, dev, stream)
     rc = lib().moe_grouped_mlp_bwd_routed(
         _ptr(x_perm), _ptr(h_saved), _ptr(do_perm), _ptr(pair_of_row), _ptr(probs), _ptr(offsets),
         E, M_cap, d, n, _ptr(W1), _ptr(W2), ACT[act], flags, _ptr(dh), _ptr(a_scaled), _ptr(ds_part),
@@ -794,7 +794,7 @@ def grouped_mlp_bwd_routed_gather(x, dO, pair_of_row, k: int, h_saved, probs, of
         dW1 = torch.empty((E, d, n1), dtype=bf, device=dev)
     if dW2 is None:
         dW2 = torch.empty((E, n, d), dtype=bf, device=dev)
-    err = _err_word(err, dev)
+    err = _err_word(err, dev, stream)
     if T == 0:      # nothing of x or dO is read then, but the maps need addresses
         x = dO = torch.zeros((1, d), dtype=bf, device=dev)
     rc = lib().moe_grouped_mlp_bwd_routed_gather(
@@ -860,7 +860,7 @@ def grouped_gemm(a, offsets, B, b_layout: str = "kn", out=None, err=None, stream
     N = B.shape[2] if layout == 0 else B.shape[1]
     if out is None:
         out = torch.empty((M_cap, N), dtype=torch.bfloat16, device=a.device)
-    err = _err_word(err, a.device)
+    err = _err_word(err, a.device, stream)
     rc = lib().moe_grouped_gemm(_ptr(a), _ptr(offsets), E, M_cap, K, N, _ptr(B), layout, _ptr(out),
                                 _ptr(err), _stream(stream))
     _check(rc, "moe_grouped_gemm")

@@ -1,0 +1,31 @@
+"""What a call of the binding makes for itself - its error word, workspace and
+outputs - is made on the stream that the call was given (read from the source;
+no GPU needed)."""
+import ast
+import os
+
+import dropless_grouped_gemm_gb300 as M
+
+MAKERS = {"_err_word": 2}      # name: position of the stream
+
+
+def _calls():
+    """(function, call) of every call of a maker inside a function with a
+    `stream` parameter."""
+    tree = ast.parse(open(os.path.join(os.path.dirname(M.__file__), "__init__.py"), encoding="utf-8").read())
+    for f in tree.body:
+        if isinstance(f, ast.FunctionDef) and not f.name.startswith("_"):
+            names = {a.arg for a in f.args.args + f.args.kwonlyargs}
+            if "stream" in names:
+                yield from ((f.name, c) for c in ast.walk(f) if isinstance(c, ast.Call))
+
+
+def test_error_words_take_the_stream_of_the_call():
+    missing = []
+    for name, c in _calls():
+        maker = getattr(c.func, "id", None)
+        if maker in MAKERS:
+            given = list(c.args[MAKERS[maker]:]) + [k.value for k in c.keywords if k.arg == "stream"]
+            if not any(isinstance(a, ast.Name) and a.id == "stream" for a in given):
+                missing.append((name, c.lineno))
+    assert not missing, missing
