@@ -261,13 +261,36 @@ def _err_word(err, device, stream=None):
     return err
 
 
+# What a call makes for itself comes from the memory of the stream that it runs
+# on: a block that the current stream has freed, with work on it still queued
+# there, is no block that another stream may write.
+
+def _empty(shape, dtype, device, stream=None) -> torch.Tensor:
+    """An output of a call on ``stream``.  The caller reads it on the current
+    stream, so it is kept from reuse until that stream too is past its end."""
+    if stream is None or stream.cuda_stream == _current_stream():
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream())
+    return t
+
+
+def _scratch(nbytes: int, device, stream=None) -> torch.Tensor:
+    """Workspace of a call on ``stream`` alone."""
+    if stream is None or stream.cuda_stream == _current_stream():
+        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+
+
 def router_topk(logits: torch.Tensor, k: int, stream=None):
     """Top-k experts per token and their softmax weights (moe_router_topk).
     Returns (topk_idx int32 [T, k], probs float32 [T, k])."""
     _need(logits, torch.float32, "logits", 2)
     T, E = logits.shape
-    idx = torch.empty((T, k), dtype=torch.int32, device=logits.device)
-    probs = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+    idx = _empty((T, k), torch.int32, logits.device, stream)
+    probs = _empty((T, k), torch.float32, logits.device, stream)
     rc = lib().moe_router_topk(_ptr(logits), T, E, k, _ptr(idx), _ptr(probs), _stream(stream))
     _check(rc, "moe_router_topk")
     return idx, probs
@@ -297,16 +320,16 @@ def route_offsets(topk_idx: torch.Tensor, E: int, align: int = 1, M_cap: int | N
         M_cap = T * k + E * (align - 1)
     dev = topk_idx.device
     o = out if out is not None else {
-        "counts": torch.empty(E, dtype=torch.int32, device=dev),
-        "offsets": torch.empty(E + 1, dtype=torch.int32, device=dev),
-        "row_of_pair": torch.empty(T * k, dtype=torch.int32, device=dev),
-        "pair_of_row": torch.empty(M_cap, dtype=torch.int32, device=dev),
-        "true_total": torch.empty(1, dtype=torch.int32, device=dev),
+        "counts": _empty(E, torch.int32, dev, stream),
+        "offsets": _empty(E + 1, torch.int32, dev, stream),
+        "row_of_pair": _empty(T * k, torch.int32, dev, stream),
+        "pair_of_row": _empty(M_cap, torch.int32, dev, stream),
+        "true_total": _empty(1, torch.int32, dev, stream),
     }
     o["err"] = _err_word(err if err is not None else o.get("err"), dev, stream)
     ws_bytes = route_workspace_size(T, k, E)
     if workspace is None:
-        workspace = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=dev)
+        workspace = _scratch(ws_bytes, dev, stream)
     rc = lib().moe_route_offsets(_ptr(topk_idx), T, k, E, align, M_cap, _ptr(o["counts"]),
                                  _ptr(o["offsets"]), _ptr(o["row_of_pair"]), _ptr(o["pair_of_row"]),
                                  _ptr(o["true_total"]), _ptr(workspace), workspace.numel(),
@@ -327,18 +350,18 @@ def route_logits(logits: torch.Tensor, k: int, align: int = 1, M_cap: int | None
         M_cap = T * k + E * (align - 1)
     dev = logits.device
     o = out if out is not None else {
-        "topk_idx": torch.empty((T, k), dtype=torch.int32, device=dev),
-        "probs": torch.empty((T, k), dtype=torch.float32, device=dev),
-        "counts": torch.empty(E, dtype=torch.int32, device=dev),
-        "offsets": torch.empty(E + 1, dtype=torch.int32, device=dev),
-        "row_of_pair": torch.empty(T * k, dtype=torch.int32, device=dev),
-        "pair_of_row": torch.empty(M_cap, dtype=torch.int32, device=dev),
-        "true_total": torch.empty(1, dtype=torch.int32, device=dev),
+        "topk_idx": _empty((T, k), torch.int32, dev, stream),
+        "probs": _empty((T, k), torch.float32, dev, stream),
+        "counts": _empty(E, torch.int32, dev, stream),
+        "offsets": _empty(E + 1, torch.int32, dev, stream),
+        "row_of_pair": _empty(T * k, torch.int32, dev, stream),
+        "pair_of_row": _empty(M_cap, torch.int32, dev, stream),
+        "true_total": _empty(1, torch.int32, dev, stream),
     }
     o["err"] = _err_word(err if err is not None else o.get("err"), dev, stream)
     ws_bytes = route_workspace_size(T, k, E)
     if workspace is None:
-        workspace = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=dev)
+        workspace = _scratch(ws_bytes, dev, stream)
     rc = lib().moe_route_logits(_ptr(logits), T, E, k, align, M_cap, _ptr(o["topk_idx"]),
                                 _ptr(o["probs"]), _ptr(o["counts"]), _ptr(o["offsets"]),
                                 _ptr(o["row_of_pair"]), _ptr(o["pair_of_row"]),
@@ -361,7 +384,7 @@ def permute(src: torch.Tensor, pair_of_row: torch.Tensor, k: int, scale: torch.T
     T, d = src.shape
     M_cap = pair_of_row.numel()
     if out is None:
-        out = torch.empty((M_cap, d), dtype=torch.bfloat16, device=src.device)
+        out = _empty((M_cap, d), torch.bfloat16, src.device, stream)
     _need(out, torch.bfloat16, "out", 2)
     if row_of_pair is not None:
         if row_of_pair.numel() != T * k:
@@ -388,11 +411,11 @@ def unpermute(src: torch.Tensor, row_of_pair: torch.Tensor, T: int, k: int,
     _need(dO, torch.bfloat16, "dO")
     d = src.shape[1]
     if combine and out is None:
-        out = torch.empty((T, d), dtype=torch.bfloat16, device=src.device)
+        out = _empty((T, d), torch.bfloat16, src.device, stream)
     if not combine:
         out = None
     if dO is not None and dprobs is None:
-        dprobs = torch.empty((T, k), dtype=torch.float32, device=src.device)
+        dprobs = _empty((T, k), torch.float32, src.device, stream)
     _need(out, torch.bfloat16, "out")
     _need(dprobs, torch.float32, "dprobs")
     rc = lib().moe_unpermute(_ptr(src), _ptr(probs), _ptr(row_of_pair), T, k, d, src.shape[0],
@@ -425,11 +448,11 @@ def grouped_mlp_fwd(x_perm: torch.Tensor, offsets: torch.Tensor, W1: torch.Tenso
         raise MoeError("inconsistent shapes")
     dev = x_perm.device
     if save_h and h_saved is None:
-        h_saved = torch.empty((M_cap, n1), dtype=torch.bfloat16, device=dev)
+        h_saved = _empty((M_cap, n1), torch.bfloat16, dev, stream)
     if a is None:
-        a = torch.empty((M_cap, n), dtype=torch.bfloat16, device=dev)
+        a = _empty((M_cap, n), torch.bfloat16, dev, stream)
     if y_perm is None:
-        y_perm = torch.empty((M_cap, d), dtype=torch.bfloat16, device=dev)
+        y_perm = _empty((M_cap, d), torch.bfloat16, dev, stream)
     err = _err_word(err, dev, stream)
     flags = FLAG_SAVE_H if save_h else 0
     mxs = None
@@ -469,14 +492,14 @@ def grouped_mlp_fwd_gather(x: torch.Tensor, pair_of_row: torch.Tensor, k: int,
         raise MoeError("inconsistent shapes")
     dev = x.device
     if save_h and h_saved is None:
-        h_saved = torch.empty((M_cap, n1), dtype=torch.bfloat16, device=dev)
+        h_saved = _empty((M_cap, n1), torch.bfloat16, dev, stream)
     if a is None:
-        a = torch.empty((M_cap, n), dtype=torch.bfloat16, device=dev)
+        a = _empty((M_cap, n), torch.bfloat16, dev, stream)
     if y_perm is None:
-        y_perm = torch.empty((M_cap, d), dtype=torch.bfloat16, device=dev)
+        y_perm = _empty((M_cap, d), torch.bfloat16, dev, stream)
     err = _err_word(err, dev, stream)
     if T == 0:      # the library reads nothing of x then, but needs an address
-        x = torch.zeros((1, d), dtype=torch.bfloat16, device=dev)
+        x = _empty((1, d), torch.bfloat16, dev, stream)
     rc = lib().moe_grouped_mlp_fwd_gather(
         _ptr(x), T, k, _ptr(pair_of_row), _ptr(offsets), E, M_cap, d, n, _ptr(W1), _ptr(W2),
         ACT[act], FLAG_SAVE_H if save_h else 0, _ptr(h_saved) if save_h else None, _ptr(a),
@@ -509,13 +532,13 @@ def grouped_mlp_bwd(x_perm, h_saved, a, dy_perm, offsets, W1, W2, act: str = "sw
     n1 = n if act == "srelu" else 2 * n
     dev = x_perm.device
     if dh is None:
-        dh = torch.empty((M_cap, n1), dtype=torch.bfloat16, device=dev)
+        dh = _empty((M_cap, n1), torch.bfloat16, dev, stream)
     if dx_perm is None:
-        dx_perm = torch.empty((M_cap, d), dtype=torch.bfloat16, device=dev)
+        dx_perm = _empty((M_cap, d), torch.bfloat16, dev, stream)
     if dW1 is None:
-        dW1 = torch.empty((E, d, n1), dtype=torch.bfloat16, device=dev)
+        dW1 = _empty((E, d, n1), torch.bfloat16, dev, stream)
     if dW2 is None:
-        dW2 = torch.empty((E, n, d), dtype=torch.bfloat16, device=dev)
+        dW2 = _empty((E, n, d), torch.bfloat16, dev, stream)
     err = _err_word(err, dev, stream)
     rc = lib().moe_grouped_mlp_bwd(_ptr(x_perm), _ptr(h_saved), _ptr(a), _ptr(dy_perm),
                                    _ptr(offsets), E, M_cap, d, n, _ptr(W1), _ptr(W2), ACT[act], flags,
@@ -560,9 +583,9 @@ def mx_quantize_weights(W2: torch.Tensor, w2_q: torch.Tensor | None = None,
     E, n, d = W2.shape
     offsets = _offsets_arg(offsets, E)
     if w2_q is None:
-        w2_q = torch.empty((E, n, d), dtype=torch.uint8, device=W2.device)
+        w2_q = _empty((E, n, d), torch.uint8, W2.device, stream)
     if w2_s is None:
-        w2_s = torch.empty(E * (n // 32) * d, dtype=torch.uint8, device=W2.device)
+        w2_s = _empty(E * (n // 32) * d, torch.uint8, W2.device, stream)
     _need(w2_q, torch.uint8, "w2_q")
     _need(w2_s, torch.uint8, "w2_s")
     rc = lib().moe_mx_quantize_weights(_ptr(W2), E, n, d, _ptr(offsets), _ptr(w2_q), _ptr(w2_s),
@@ -579,10 +602,10 @@ def mx_quantize(src: torch.Tensor, offsets: torch.Tensor, transposed: bool = Tru
     _need(offsets, torch.int32, "offsets", 1)
     rows, cols = src.shape
     dev = src.device
-    q = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
-    s = torch.empty((rows, cols // 32), dtype=torch.uint8, device=dev)
-    qT = torch.empty((cols, rows), dtype=torch.uint8, device=dev) if transposed else None
-    sT = torch.empty((cols, rows // 32), dtype=torch.uint8, device=dev) if transposed else None
+    q = _empty((rows, cols), torch.uint8, dev, stream)
+    s = _empty((rows, cols // 32), torch.uint8, dev, stream)
+    qT = _empty((cols, rows), torch.uint8, dev, stream) if transposed else None
+    sT = _empty((cols, rows // 32), torch.uint8, dev, stream) if transposed else None
     err = _err_word(err, dev, stream)
     rc = lib().moe_mx_quantize(_ptr(src), rows, cols, _ptr(offsets), offsets.numel() - 1, _ptr(q),
                                _ptr(s), _ptr(qT), _ptr(sT), _ptr(err), _stream(stream))
@@ -603,10 +626,10 @@ def mx_quantize_tiled(src: torch.Tensor, offsets: torch.Tensor, rowwise: bool = 
     rows, cols = src.shape
     dev = src.device
     u8 = torch.uint8
-    q = torch.empty((rows, cols), dtype=u8, device=dev) if rowwise else None
-    s = torch.empty(rows * cols // 8, dtype=u8, device=dev) if rowwise else None
-    qT = torch.empty((cols, rows), dtype=u8, device=dev) if transposed else None
-    sT = torch.empty(rows * cols // 8, dtype=u8, device=dev) if transposed else None
+    q = _empty((rows, cols), u8, dev, stream) if rowwise else None
+    s = _empty(rows * cols // 8, u8, dev, stream) if rowwise else None
+    qT = _empty((cols, rows), u8, dev, stream) if transposed else None
+    sT = _empty(rows * cols // 8, u8, dev, stream) if transposed else None
     err = _err_word(err, dev, stream)
     rc = lib().moe_mx_quantize_tiled(_ptr(src), rows, cols, _ptr(offsets), offsets.numel() - 1,
                                      _ptr(q), _ptr(s), _ptr(qT), _ptr(sT), _ptr(err),
@@ -629,9 +652,9 @@ def mx_quantize_weights_rowwise(W: torch.Tensor, q: torch.Tensor | None = None,
         raise ValueError("offsets needs W as [E, R, K]")
     offsets = _offsets_arg(offsets, E) if offsets is not None else None
     if q is None:
-        q = torch.empty(tuple(W.shape), dtype=torch.uint8, device=W.device)
+        q = _empty(tuple(W.shape), torch.uint8, W.device, stream)
     if s is None:
-        s = torch.empty(rows * K // 32, dtype=torch.uint8, device=W.device)
+        s = _empty(rows * K // 32, torch.uint8, W.device, stream)
     _need(q, torch.uint8, "q")
     _need(s, torch.uint8, "s")
     rc = lib().moe_mx_quantize_weights_rowwise(_ptr(W), rows, K, _ptr(offsets), E, _ptr(q), _ptr(s),
@@ -694,17 +717,17 @@ def grouped_mlp_bwd_mx(x_perm, h_saved, dy_perm, offsets, mx: dict, act: str = "
     n1 = h_saved.shape[1]
     dev = x_perm.device
     if dh is None:
-        dh = torch.empty((M_cap, n1), dtype=torch.bfloat16, device=dev)
+        dh = _empty((M_cap, n1), torch.bfloat16, dev, stream)
     if dx_perm is None:
-        dx_perm = torch.empty((M_cap, d), dtype=torch.bfloat16, device=dev)
+        dx_perm = _empty((M_cap, d), torch.bfloat16, dev, stream)
     if dW1 is None:
-        dW1 = torch.empty((E, d, n1), dtype=torch.bfloat16, device=dev)
+        dW1 = _empty((E, d, n1), torch.bfloat16, dev, stream)
     if dW2 is None:
-        dW2 = torch.empty((E, n, d), dtype=torch.bfloat16, device=dev)
+        dW2 = _empty((E, n, d), torch.bfloat16, dev, stream)
     err = _err_word(err, dev, stream)
     need = mx_bwd_workspace_size(M_cap, d, n, act)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        workspace = _scratch(need, dev, stream)
     _need(workspace, torch.uint8, "workspace")
     for k_ in ("dx_q", "dx_s"):
         _need(mx.get(k_), torch.uint8, k_)
@@ -742,17 +765,17 @@ def grouped_mlp_bwd_routed(x_perm, h_saved, do_perm, pair_of_row, probs, offsets
     dev = x_perm.device
     bf = torch.bfloat16
     if dh is None:
-        dh = torch.empty((M_cap, n1), dtype=bf, device=dev)
+        dh = _empty((M_cap, n1), bf, dev, stream)
     if a_scaled is None:
-        a_scaled = torch.empty((M_cap, n), dtype=bf, device=dev)
+        a_scaled = _empty((M_cap, n), bf, dev, stream)
     if ds_part is None:
-        ds_part = torch.empty((M_cap, (n + 127) // 128), dtype=torch.float32, device=dev)
+        ds_part = _empty((M_cap, (n + 127) // 128), torch.float32, dev, stream)
     if dx_perm is None:
-        dx_perm = torch.empty((M_cap, d), dtype=bf, device=dev)
+        dx_perm = _empty((M_cap, d), bf, dev, stream)
     if dW1 is None:
-        dW1 = torch.empty((E, d, n1), dtype=bf, device=dev)
+        dW1 = _empty((E, d, n1), bf, dev, stream)
     if dW2 is None:
-        dW2 = torch.empty((E, n, d), dtype=bf, device=dev)
+        dW2 = _empty((E, n, d), bf, dev, stream)
     err = _err_word(err, dev, stream)
     rc = lib().moe_grouped_mlp_bwd_routed(
         _ptr(x_perm), _ptr(h_saved), _ptr(do_perm), _ptr(pair_of_row), _ptr(probs), _ptr(offsets),
@@ -783,20 +806,20 @@ def grouped_mlp_bwd_routed_gather(x, dO, pair_of_row, k: int, h_saved, probs, of
     dev = x.device
     bf = torch.bfloat16
     if dh is None:
-        dh = torch.empty((M_cap, n1), dtype=bf, device=dev)
+        dh = _empty((M_cap, n1), bf, dev, stream)
     if a_scaled is None:
-        a_scaled = torch.empty((M_cap, n), dtype=bf, device=dev)
+        a_scaled = _empty((M_cap, n), bf, dev, stream)
     if ds_part is None:
-        ds_part = torch.empty((M_cap, (n + 127) // 128), dtype=torch.float32, device=dev)
+        ds_part = _empty((M_cap, (n + 127) // 128), torch.float32, dev, stream)
     if dx_perm is None:
-        dx_perm = torch.empty((M_cap, d), dtype=bf, device=dev)
+        dx_perm = _empty((M_cap, d), bf, dev, stream)
     if dW1 is None:
-        dW1 = torch.empty((E, d, n1), dtype=bf, device=dev)
+        dW1 = _empty((E, d, n1), bf, dev, stream)
     if dW2 is None:
-        dW2 = torch.empty((E, n, d), dtype=bf, device=dev)
+        dW2 = _empty((E, n, d), bf, dev, stream)
     err = _err_word(err, dev, stream)
     if T == 0:      # nothing of x or dO is read then, but the maps need addresses
-        x = dO = torch.zeros((1, d), dtype=bf, device=dev)
+        x = dO = _empty((1, d), bf, dev, stream)
     rc = lib().moe_grouped_mlp_bwd_routed_gather(
         _ptr(x), _ptr(dO), T, k, _ptr(h_saved), _ptr(pair_of_row), _ptr(probs), _ptr(offsets), E,
         M_cap, d, n, _ptr(W1), _ptr(W2), ACT[act], flags, _ptr(dh), _ptr(a_scaled), _ptr(ds_part),
@@ -811,7 +834,7 @@ def router_grad_rows(ds_part, row_of_pair, T: int, k: int, dprobs=None, stream=N
     _need(row_of_pair, torch.int32, "row_of_pair", 1)
     M_cap, n_parts = ds_part.shape
     if dprobs is None:
-        dprobs = torch.empty((T, k), dtype=torch.float32, device=ds_part.device)
+        dprobs = _empty((T, k), torch.float32, ds_part.device, stream)
     rc = lib().moe_router_grad_rows(_ptr(ds_part), n_parts, _ptr(row_of_pair), T, k, M_cap,
                                     _ptr(dprobs), _stream(stream))
     _check(rc, "moe_router_grad_rows")
@@ -830,13 +853,13 @@ def mx_quantize_weights2(W2: torch.Tensor, w2_q=None, w2_s=None, w2_q_rows=None,
     u8 = torch.uint8
     dev = W2.device
     if w2_q is None:
-        w2_q = torch.empty((E, n, d), dtype=u8, device=dev)
+        w2_q = _empty((E, n, d), u8, dev, stream)
     if w2_s is None:
-        w2_s = torch.empty(E * (n // 32) * d, dtype=u8, device=dev)
+        w2_s = _empty(E * (n // 32) * d, u8, dev, stream)
     if w2_q_rows is None:
-        w2_q_rows = torch.empty((E, n, d), dtype=u8, device=dev)
+        w2_q_rows = _empty((E, n, d), u8, dev, stream)
     if w2_s_rows is None:
-        w2_s_rows = torch.empty(E * n * d // 32, dtype=u8, device=dev)
+        w2_s_rows = _empty(E * n * d // 32, u8, dev, stream)
     for t, nm in ((w2_q, "w2_q"), (w2_s, "w2_s"), (w2_q_rows, "w2_q_rows"), (w2_s_rows, "w2_s_rows")):
         _need(t, u8, nm)
     rc = lib().moe_mx_quantize_weights2(_ptr(W2), E, n, d, _ptr(offsets), _ptr(w2_q), _ptr(w2_s),
@@ -859,7 +882,7 @@ def grouped_gemm(a, offsets, B, b_layout: str = "kn", out=None, err=None, stream
     E = B.shape[0]
     N = B.shape[2] if layout == 0 else B.shape[1]
     if out is None:
-        out = torch.empty((M_cap, N), dtype=torch.bfloat16, device=a.device)
+        out = _empty((M_cap, N), torch.bfloat16, a.device, stream)
     err = _err_word(err, a.device, stream)
     rc = lib().moe_grouped_gemm(_ptr(a), _ptr(offsets), E, M_cap, K, N, _ptr(B), layout, _ptr(out),
                                 _ptr(err), _stream(stream))
@@ -874,7 +897,7 @@ def activation(h, offsets, act: str = "swiglu", a=None, stream=None):
     M_cap, n1 = h.shape
     n = n1 if act == "srelu" else n1 // 2
     if a is None:
-        a = torch.empty((M_cap, n), dtype=torch.bfloat16, device=h.device)
+        a = _empty((M_cap, n), torch.bfloat16, h.device, stream)
     rc = lib().moe_activation(_ptr(h), _ptr(offsets), offsets.numel() - 1, M_cap, n, ACT[act],
                               _ptr(a), _stream(stream))
     _check(rc, "moe_activation")
@@ -888,7 +911,7 @@ def activation_bwd(h, da, offsets, act: str = "swiglu", dh=None, stream=None):
     _need(offsets, torch.int32, "offsets", 1)
     M_cap, n = da.shape
     if dh is None:
-        dh = torch.empty_like(h)
+        dh = _empty(h.shape, h.dtype, h.device, stream)
     rc = lib().moe_activation_bwd(_ptr(h), _ptr(da), _ptr(offsets), offsets.numel() - 1, M_cap, n,
                                   ACT[act], _ptr(dh), _stream(stream))
     _check(rc, "moe_activation_bwd")
@@ -898,14 +921,6 @@ def activation_bwd(h, da, offsets, act: str = "swiglu", dh=None, stream=None):
 # ----------------------------------------------------------------- router losses
 
 _TYPE = {torch.float32: 0, torch.bfloat16: 1}
-
-
-def _scratch(nbytes: int, device, stream):
-    """Workspace for one call, kept from reuse until the call's stream is past it."""
-    ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
-    if stream is not None:
-        ws.record_stream(stream)
-    return ws
 
 
 def _float_type(t, name):
@@ -946,10 +961,10 @@ def router_loss(logits: torch.Tensor, topk_idx: torch.Tensor, seg_offsets=None, 
     lt, T, E, k, S = _router_args(logits, topk_idx, seg_offsets, token_mask)
     dev = logits.device
     o = out if out is not None else {
-        "loss": torch.empty(2, dtype=torch.float32, device=dev),
-        "counts": torch.empty((S, E), dtype=torch.int32, device=dev),
-        "lse": torch.empty(T, dtype=torch.float32, device=dev),
-        "n_valid": torch.empty(S, dtype=torch.int32, device=dev),
+        "loss": _empty(2, torch.float32, dev, stream),
+        "counts": _empty((S, E), torch.int32, dev, stream),
+        "lse": _empty(T, torch.float32, dev, stream),
+        "n_valid": _empty(S, torch.int32, dev, stream),
     }
     o["err"] = _err_word(err if err is not None else o.get("err"), dev, stream)
     if workspace is None:
@@ -974,7 +989,7 @@ def router_loss_bwd(logits: torch.Tensor, topk_idx: torch.Tensor, fwd: dict, dlo
     lt, T, E, k, S = _router_args(logits, topk_idx, seg_offsets, token_mask)
     if dlogits is None:
         ot = _float_type(dtype or torch.float32, "dlogits")
-        dlogits = torch.empty((T, E), dtype=dtype or torch.float32, device=logits.device)
+        dlogits = _empty((T, E), dtype or torch.float32, logits.device, stream)
     else:
         ot = _float_type(dlogits.dtype, "dlogits")
         _need(dlogits, dlogits.dtype, "dlogits", 2)
@@ -1034,7 +1049,7 @@ def grouped_linear(a: torch.Tensor, offsets, B: torch.Tensor, act: str = "none",
     _same_shape(residual, (M_cap, n_out), "residual")
     if out is None:
         ot = _float_type(out_dtype, "out")
-        out = torch.empty((M_cap, n_out), dtype=out_dtype, device=a.device)
+        out = _empty((M_cap, n_out), out_dtype, a.device, stream)
     else:
         ot = _float_type(out.dtype, "out")
         _need(out, out.dtype, "out")
@@ -1043,7 +1058,7 @@ def grouped_linear(a: torch.Tensor, offsets, B: torch.Tensor, act: str = "none",
         _need(z, torch.bfloat16, "z")
         _same_shape(z, (M_cap, N), "z")
     elif save_z:
-        z = torch.empty((M_cap, N), dtype=torch.bfloat16, device=a.device)
+        z = _empty((M_cap, N), torch.bfloat16, a.device, stream)
     err = _err_word(err, a.device, stream)
     rc = lib().moe_grouped_linear(_ptr(a), _ptr(offsets), E, M_cap, K, N, _ptr(B), layout,
                                   _ptr(bias), LINEAR_ACT[act], _ptr(residual), _ptr(z), _ptr(out),
@@ -1083,13 +1098,13 @@ def grouped_linear_bwd(dout: torch.Tensor, a: torch.Tensor, offsets, B: torch.Te
         _need(t, ty, nm)
         _same_shape(t, shape, nm)
     if act != "none" and dz is None:
-        dz = torch.empty((M_cap, N), dtype=torch.bfloat16, device=dev)
+        dz = _empty((M_cap, N), torch.bfloat16, dev, stream)
     if da is None:
-        da = torch.empty((M_cap, K), dtype=torch.bfloat16, device=dev)
+        da = _empty((M_cap, K), torch.bfloat16, dev, stream)
     if dB is None:
-        dB = torch.empty(B.shape, dtype=torch.bfloat16, device=dev)
+        dB = _empty(B.shape, torch.bfloat16, dev, stream)
     if bias and dbias is None:
-        dbias = torch.empty((E, N), dtype=torch.float32, device=dev)
+        dbias = _empty((E, N), torch.float32, dev, stream)
     if bias and workspace is None:
         workspace = _scratch(grouped_linear_bwd_workspace_size(E, M_cap, N), dev, stream)
     err = _err_word(err, dev, stream)
@@ -1115,9 +1130,9 @@ def checkpoint_pack(src: torch.Tensor, q=None, s=None, stream=None):
         _need(t, torch.uint8, nm)
         _same_shape(t, shape, nm)
     if q is None:
-        q = torch.empty((rows, cols), dtype=torch.uint8, device=src.device)
+        q = _empty((rows, cols), torch.uint8, src.device, stream)
     if s is None:
-        s = torch.empty((rows, cols // 32), dtype=torch.uint8, device=src.device)
+        s = _empty((rows, cols // 32), torch.uint8, src.device, stream)
     rc = lib().moe_checkpoint_pack(_ptr(src), rows, cols, _ptr(q), _ptr(s), _stream(stream))
     _check(rc, "moe_checkpoint_pack")
     return q, s
@@ -1134,7 +1149,7 @@ def checkpoint_unpack(q: torch.Tensor, s: torch.Tensor, out=None, stream=None) -
     """The bf16 values of a checkpoint (moe_checkpoint_unpack), exact."""
     rows, cols = _ckpt_args(q, s, "checkpoint")
     if out is None:
-        out = torch.empty((rows, cols), dtype=torch.bfloat16, device=q.device)
+        out = _empty((rows, cols), torch.bfloat16, q.device, stream)
     _need(out, torch.bfloat16, "out", 2)
     _same_shape(out, (rows, cols), "out")
     rc = lib().moe_checkpoint_unpack(_ptr(q), _ptr(s), rows, cols, _ptr(out), _stream(stream))
@@ -1153,7 +1168,7 @@ def permute_checkpoint(q: torch.Tensor, s: torch.Tensor, pair_of_row: torch.Tens
         raise MoeError("row_of_pair must hold T*k entries")
     M_cap = pair_of_row.numel()
     if out is None:
-        out = torch.empty((M_cap, d), dtype=torch.bfloat16, device=q.device)
+        out = _empty((M_cap, d), torch.bfloat16, q.device, stream)
     _need(out, torch.bfloat16, "out", 2)
     _same_shape(out, (M_cap, d), "out")
     rc = lib().moe_permute_checkpoint(_ptr(q), _ptr(s), _ptr(row_of_pair), _ptr(pair_of_row), T, k,
@@ -1179,13 +1194,13 @@ def grouped_mlp_fwd_ckpt(x_perm: torch.Tensor, offsets: torch.Tensor, W1: torch.
         raise MoeError("inconsistent shapes")
     dev = x_perm.device
     if h_q is None:
-        h_q = torch.empty((M_cap, n1), dtype=torch.uint8, device=dev)
+        h_q = _empty((M_cap, n1), torch.uint8, dev, stream)
     if h_s is None:
-        h_s = torch.empty((M_cap, n1 // 32), dtype=torch.uint8, device=dev)
+        h_s = _empty((M_cap, n1 // 32), torch.uint8, dev, stream)
     if a is None:
-        a = torch.empty((M_cap, n), dtype=torch.bfloat16, device=dev)
+        a = _empty((M_cap, n), torch.bfloat16, dev, stream)
     if y_perm is None:
-        y_perm = torch.empty((M_cap, d), dtype=torch.bfloat16, device=dev)
+        y_perm = _empty((M_cap, d), torch.bfloat16, dev, stream)
     _ckpt_args(h_q, h_s, "h")
     _same_shape(h_q, (M_cap, n1), "h_q")
     err = _err_word(err, dev, stream)
@@ -1217,17 +1232,17 @@ def grouped_mlp_bwd_routed_ckpt(x_perm, h_q, h_s, do_perm, pair_of_row, probs, o
     dev = x_perm.device
     bf = torch.bfloat16
     if dh is None:
-        dh = torch.empty((M_cap, n1), dtype=bf, device=dev)
+        dh = _empty((M_cap, n1), bf, dev, stream)
     if a_scaled is None:
-        a_scaled = torch.empty((M_cap, n), dtype=bf, device=dev)
+        a_scaled = _empty((M_cap, n), bf, dev, stream)
     if ds_part is None:
-        ds_part = torch.empty((M_cap, (n + 127) // 128), dtype=torch.float32, device=dev)
+        ds_part = _empty((M_cap, (n + 127) // 128), torch.float32, dev, stream)
     if dx_perm is None:
-        dx_perm = torch.empty((M_cap, d), dtype=bf, device=dev)
+        dx_perm = _empty((M_cap, d), bf, dev, stream)
     if dW1 is None:
-        dW1 = torch.empty((E, d, n1), dtype=bf, device=dev)
+        dW1 = _empty((E, d, n1), bf, dev, stream)
     if dW2 is None:
-        dW2 = torch.empty((E, n, d), dtype=bf, device=dev)
+        dW2 = _empty((E, n, d), bf, dev, stream)
     err = _err_word(err, dev, stream)
     rc = lib().moe_grouped_mlp_bwd_routed_ckpt(
         _ptr(x_perm), _ptr(h_q), _ptr(h_s), _ptr(do_perm), _ptr(pair_of_row), _ptr(probs),

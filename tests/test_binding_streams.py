@@ -6,7 +6,7 @@ import os
 
 import dropless_grouped_gemm_gb300 as M
 
-MAKERS = {"_err_word": 2}      # name: position of the stream
+MAKERS = {"_err_word": 2, "_scratch": 2, "_empty": 3}      # name: position of the stream
 
 
 def _calls():
@@ -20,10 +20,14 @@ def _calls():
                 yield from ((f.name, c) for c in ast.walk(f) if isinstance(c, ast.Call))
 
 
-def test_error_words_take_the_stream_of_the_call():
+def test_what_a_call_makes_takes_its_stream():
     missing = []
     for name, c in _calls():
         maker = getattr(c.func, "id", None)
+        # torch's own allocations are in the current stream's memory
+        if isinstance(c.func, ast.Attribute) and c.func.attr in ("empty", "zeros", "full", "ones", "empty_like",
+                                                                 "zeros_like", "clone"):
+            missing.append((name, c.lineno))
         if maker in MAKERS:
             given = list(c.args[MAKERS[maker]:]) + [k.value for k in c.keywords if k.arg == "stream"]
             if not any(isinstance(a, ast.Name) and a.id == "stream" for a in given):

@@ -1,8 +1,10 @@
-"""Calls given a stream of their own: their error words belong to it."""
+"""Calls given a stream of their own: their error words, workspaces and
+outputs belong to it."""
 import numpy as np
 import pytest
 import torch
 
+import workloads as W
 from _helpers import cuda_i32
 
 pytestmark = pytest.mark.gpu
@@ -75,3 +77,105 @@ def test_error_words_made_in_inference_mode():
     _, _, e1 = M.grouped_linear(a, None, B)
     e1.zero_()
     assert not e1.is_inference() and int(e0.item()) == 0 and int(e1.item()) == 0
+
+
+def _linear_case():
+    E, M, K, N = 3, 400, 128, 256
+    off = cuda_i32([0, 100, 250, 400])
+    a = W.normal((M, K), (40, W.X, 0), 1.0, "cuda")
+    B = W.normal((E, K, N), (40, W.W2, 1), 0.05, "cuda")
+    z = W.normal((M, N), (40, W.X, 5), 1.5, "cuda")
+    dout = W.normal((M, N), (40, W.DO, 0), 1.0, "cuda")
+    return E, M, K, N, off, a, B, z, dout
+
+
+def test_outputs_do_not_come_from_memory_the_current_stream_still_writes():
+    import dropless_grouped_gemm_gb300 as M_
+    E, M, K, N, off, a, B, z, dout = _linear_case()
+    want = M_.grouped_linear_bwd(dout, a, off, B, "silu", z, True)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    keep = _busy()
+    # blocks of the outputs' sizes, freed with a write to each still queued
+    old = [torch.empty_like(t) for t in want[:4]]
+    for t in old:
+        t.fill_(float("nan"))
+    del t, old
+    got = M_.grouped_linear_bwd(dout, a, off, B, "silu", z, True, stream=st)
+    torch.cuda.synchronize()
+    del keep
+    for x, y in zip(got[:4], want[:4]):
+        assert torch.equal(x, y)
+
+
+def test_outputs_are_not_reused_while_the_current_stream_reads_them():
+    import dropless_grouped_gemm_gb300 as M_
+    E, M, K, N, off, a, B, z, dout = _linear_case()
+    want = M_.grouped_linear_bwd(dout, a, off, B, "silu", z, True)
+    other = W.normal((M, N), (41, W.DO, 0), 1.0, "cuda")
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    got = M_.grouped_linear_bwd(dout, a, off, B, "silu", z, True, stream=st)
+    torch.cuda.current_stream().wait_stream(st)
+    keep = _busy()
+    copies = [t.clone() for t in got[:4]]                 # queued behind the busy work
+    del got
+    again = M_.grouped_linear_bwd(other, a, off, B, "silu", z, True, stream=st)
+    torch.cuda.synchronize()
+    del keep, again
+    for x, y in zip(copies, want[:4]):
+        assert torch.equal(x, y)
+
+
+def _pointer(M_, name, index, monkeypatch):
+    """The argument `index` of every call of the C entry `name`."""
+    seen, f = [], getattr(M_.lib(), name)
+
+    def spy(*args):
+        seen.append(args[index])
+        return f(*args)
+    monkeypatch.setattr(M_.lib(), name, spy)
+    return seen
+
+
+def test_workspaces_do_not_come_from_memory_the_current_stream_still_uses(monkeypatch):
+    import dropless_grouped_gemm_gb300 as M_
+    E, M, K, N, off, a, B, z, dout = _linear_case()
+    lin = _pointer(M_, "moe_grouped_linear_bwd", 16, monkeypatch)
+    loss = _pointer(M_, "moe_router_loss", 13, monkeypatch)
+    route = _pointer(M_, "moe_route_offsets", 11, monkeypatch)
+    logits = torch.randn((300, 64), device="cuda")
+    idx = logits.topk(2).indices.int()
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+
+    def calls(s):
+        M_.grouped_linear_bwd(dout, a, off, B, "silu", z, True, stream=s)
+        M_.router_loss(logits, idx, stream=s)
+        M_.route_offsets(idx, 64, stream=s)
+    keep = _busy()
+    calls(None)                                           # their scratch is freed on return
+    calls(st)
+    torch.cuda.synchronize()
+    del keep
+    for p in (lin, loss, route):
+        assert len(p) == 2 and p[0] != p[1], p
+
+
+def test_workspaces_are_not_reused_while_the_call_is_still_queued():
+    """The side stream is busy, so its call runs late; tensors of the
+    workspace's size are made and filled on the current stream meanwhile."""
+    import dropless_grouped_gemm_gb300 as M_
+    E, M, K, N, off, a, B, z, dout = _linear_case()
+    want = M_.grouped_linear_bwd(dout, a, off, B, "silu", z, True)
+    size = M_.grouped_linear_bwd_workspace_size(E, M, N)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        keep = _busy()
+    got = M_.grouped_linear_bwd(dout, a, off, B, "silu", z, True, stream=st)
+    junk = [torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda") for _ in range(16)]
+    torch.cuda.synchronize()
+    del keep, junk
+    for x, y in zip(got[:4], want[:4]):
+        assert torch.equal(x, y)
