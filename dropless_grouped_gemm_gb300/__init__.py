@@ -966,6 +966,13 @@ def router_loss(logits: torch.Tensor, topk_idx: torch.Tensor, seg_offsets=None, 
         "lse": _empty(T, torch.float32, dev, stream),
         "n_valid": _empty(S, torch.int32, dev, stream),
     }
+    if out is not None:
+        for nm, ty, shape in (("loss", torch.float32, (2,)), ("counts", torch.int32, (S, E)),
+                              ("lse", torch.float32, (T,)), ("n_valid", torch.int32, (S,))):
+            if o.get(nm) is None:
+                raise MoeError(f"out needs {nm}")
+            _need(o[nm], ty, nm)
+            _same_shape(o[nm], shape, nm)
     o["err"] = _err_word(err if err is not None else o.get("err"), dev, stream)
     if workspace is None:
         workspace = _scratch(router_loss_workspace_size(T, E, S), dev, stream)
