@@ -1184,6 +1184,26 @@ def permute_checkpoint(q: torch.Tensor, s: torch.Tensor, pair_of_row: torch.Tens
     return out
 
 
+def _mlp_args(x_perm, offsets, W1, W2, act):
+    if act not in ACT:
+        raise MoeError(f"act must be one of {sorted(ACT)}, got {act!r}")
+    if x_perm.dim() != 2 or W2.dim() != 3:
+        raise MoeError("x_perm must have 2 dims and W2 3")
+    M_cap, d = x_perm.shape
+    E, n, d2 = W2.shape
+    n1 = n if act == "srelu" else 2 * n
+    if d2 != d or tuple(W1.shape) != (E, d, n1) or offsets.numel() != E + 1:
+        raise MoeError("inconsistent shapes")
+    return M_cap, d, E, n, n1
+
+
+def _buffers(*given):
+    """Checks (tensor or None, dtype, name, shape) of buffers to write."""
+    for t, ty, nm, shape in given:
+        _need(t, ty, nm)
+        _same_shape(t, shape, nm)
+
+
 def grouped_mlp_fwd_ckpt(x_perm: torch.Tensor, offsets: torch.Tensor, W1: torch.Tensor,
                          W2: torch.Tensor, act: str = "swiglu", h_q=None, h_s=None, a=None,
                          y_perm=None, err=None, stream=None):
@@ -1194,11 +1214,7 @@ def grouped_mlp_fwd_ckpt(x_perm: torch.Tensor, offsets: torch.Tensor, W1: torch.
     _need(offsets, torch.int32, "offsets", 1)
     _need(W1, torch.bfloat16, "W1", 3)
     _need(W2, torch.bfloat16, "W2", 3)
-    M_cap, d = x_perm.shape
-    E, n, d2 = W2.shape
-    n1 = n if act == "srelu" else 2 * n
-    if d2 != d or tuple(W1.shape) != (E, d, n1) or offsets.numel() != E + 1:
-        raise MoeError("inconsistent shapes")
+    M_cap, d, E, n, n1 = _mlp_args(x_perm, offsets, W1, W2, act)
     dev = x_perm.device
     if h_q is None:
         h_q = _empty((M_cap, n1), torch.uint8, dev, stream)
@@ -1210,6 +1226,7 @@ def grouped_mlp_fwd_ckpt(x_perm: torch.Tensor, offsets: torch.Tensor, W1: torch.
         y_perm = _empty((M_cap, d), torch.bfloat16, dev, stream)
     _ckpt_args(h_q, h_s, "h")
     _same_shape(h_q, (M_cap, n1), "h_q")
+    _buffers((a, torch.bfloat16, "a", (M_cap, n)), (y_perm, torch.bfloat16, "y_perm", (M_cap, d)))
     err = _err_word(err, dev, stream)
     rc = lib().moe_grouped_mlp_fwd_ckpt(_ptr(x_perm), _ptr(offsets), E, M_cap, d, n, _ptr(W1),
                                         _ptr(W2), ACT[act], _ptr(h_q), _ptr(h_s), _ptr(a),
@@ -1231,13 +1248,17 @@ def grouped_mlp_bwd_routed_ckpt(x_perm, h_q, h_s, do_perm, pair_of_row, probs, o
     _need(pair_of_row, torch.int32, "pair_of_row", 1)
     _need(probs, torch.float32, "probs")
     _need(offsets, torch.int32, "offsets", 1)
-    M_cap, d = x_perm.shape
-    E, n, _ = W2.shape
-    n1 = n if act == "srelu" else 2 * n
+    M_cap, d, E, n, n1 = _mlp_args(x_perm, offsets, W1, W2, act)
+    _same_shape(do_perm, (M_cap, d), "do_perm")
+    _same_shape(pair_of_row, (M_cap,), "pair_of_row")
     _ckpt_args(h_q, h_s, "h")
     _same_shape(h_q, (M_cap, n1), "h_q")
     dev = x_perm.device
     bf = torch.bfloat16
+    _buffers((dh, bf, "dh", (M_cap, n1)), (a_scaled, bf, "a_scaled", (M_cap, n)),
+             (ds_part, torch.float32, "ds_part", (M_cap, (n + 127) // 128)),
+             (dx_perm, bf, "dx_perm", (M_cap, d)), (dW1, bf, "dW1", (E, d, n1)),
+             (dW2, bf, "dW2", (E, n, d)))
     if dh is None:
         dh = _empty((M_cap, n1), bf, dev, stream)
     if a_scaled is None:

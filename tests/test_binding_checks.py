@@ -90,3 +90,49 @@ def test_router_loss_refuses_buffers_that_do_not_fit(L, bad, monkeypatch):
 def test_router_loss_takes_buffers_that_fit(L):
     o = _loss_out()
     assert _loss(o) is o and L.calls == ["moe_router_loss"]
+
+
+def _ckpt_fwd(**kw):
+    a = dict(x_perm=Fake((96, 128), BF), offsets=Fake(3, I32), W1=Fake((2, 128, 256), BF),
+             W2=Fake((2, 128, 128), BF), h_q=Fake((96, 256), U8), h_s=Fake((96, 8), U8),
+             a=Fake((96, 128), BF), y_perm=Fake((96, 128), BF))
+    a.update(kw)
+    return M.grouped_mlp_fwd_ckpt(**a)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(a=Fake((95, 128), BF)), dict(a=Fake((96, 128), F32)), dict(y_perm=Fake((96, 64), BF)),
+    dict(y_perm=Fake((96, 128), BF, is_cuda=False)), dict(y_perm=Fake((96, 128), BF, contiguous=False)),
+    dict(h_q=Fake((96, 128), U8)), dict(h_s=Fake((96, 4), U8)), dict(act="relu")])
+def test_mlp_fwd_ckpt_refuses_buffers_that_do_not_fit(L, bad):
+    _refused(L, lambda: _ckpt_fwd(**bad))
+
+
+def _ckpt_bwd(**kw):
+    a = dict(x_perm=Fake((96, 128), BF), h_q=Fake((96, 256), U8), h_s=Fake((96, 8), U8),
+             do_perm=Fake((96, 128), BF), pair_of_row=Fake(96, I32), probs=Fake((50, 2), F32),
+             offsets=Fake(3, I32), W1=Fake((2, 128, 256), BF), W2=Fake((2, 128, 128), BF),
+             dh=Fake((96, 256), BF), a_scaled=Fake((96, 128), BF), ds_part=Fake((96, 1), F32),
+             dx_perm=Fake((96, 128), BF), dW1=Fake((2, 128, 256), BF), dW2=Fake((2, 128, 128), BF))
+    a.update(kw)
+    return M.grouped_mlp_bwd_routed_ckpt(**a)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(do_perm=Fake((95, 128), BF)), dict(pair_of_row=Fake(95, I32)), dict(offsets=Fake(4, I32)),
+    dict(W1=Fake((2, 128, 128), BF)), dict(W2=Fake((2, 128, 64), BF)), dict(dh=Fake((96, 128), BF)),
+    dict(dh=Fake((96, 256), F32)), dict(a_scaled=Fake((90, 128), BF)), dict(ds_part=Fake((96, 2), F32)),
+    dict(ds_part=Fake((96, 1), BF)), dict(dx_perm=Fake((96, 64), BF)), dict(dW1=Fake((1, 128, 256), BF)),
+    dict(dW2=Fake((2, 128, 128), BF, is_cuda=False)), dict(dW2=Fake((2, 128, 128), BF, contiguous=False)),
+    dict(h_q=Fake((90, 256), U8)), dict(act="none")])
+def test_mlp_bwd_ckpt_refuses_buffers_that_do_not_fit(L, bad):
+    _refused(L, lambda: _ckpt_bwd(**bad))
+
+
+def test_mlp_ckpt_calls_take_buffers_that_fit(L):
+    _ckpt_fwd()
+    _ckpt_fwd(act="srelu", W1=Fake((2, 128, 128), BF), h_q=Fake((96, 128), U8), h_s=Fake((96, 4), U8))
+    _ckpt_fwd(h_q=None, h_s=None, a=None, y_perm=None)
+    _ckpt_bwd()
+    _ckpt_bwd(dh=None, a_scaled=None, ds_part=None, dx_perm=None, dW1=None, dW2=None)
+    assert L.calls == ["moe_grouped_mlp_fwd_ckpt"] * 3 + ["moe_grouped_mlp_bwd_routed_ckpt"] * 2
