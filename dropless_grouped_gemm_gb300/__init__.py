@@ -276,6 +276,15 @@ def _empty(shape, dtype, device, stream=None) -> torch.Tensor:
     return t
 
 
+def _workspace(given, nbytes: int, device, stream=None) -> torch.Tensor:
+    """The caller's workspace (any type; the library checks its size), or a new one."""
+    if given is None:
+        return _scratch(nbytes, device, stream)
+    if not given.is_cuda or not given.is_contiguous():
+        raise MoeError("workspace must be a contiguous CUDA tensor")
+    return given
+
+
 def _scratch(nbytes: int, device, stream=None) -> torch.Tensor:
     """Workspace of a call on ``stream`` alone."""
     if stream is None or stream.cuda_stream == _current_stream():
@@ -328,8 +337,7 @@ def route_offsets(topk_idx: torch.Tensor, E: int, align: int = 1, M_cap: int | N
     }
     o["err"] = _err_word(err if err is not None else o.get("err"), dev, stream)
     ws_bytes = route_workspace_size(T, k, E)
-    if workspace is None:
-        workspace = _scratch(ws_bytes, dev, stream)
+    workspace = _workspace(workspace, ws_bytes, dev, stream)
     rc = lib().moe_route_offsets(_ptr(topk_idx), T, k, E, align, M_cap, _ptr(o["counts"]),
                                  _ptr(o["offsets"]), _ptr(o["row_of_pair"]), _ptr(o["pair_of_row"]),
                                  _ptr(o["true_total"]), _ptr(workspace), workspace.numel(),
@@ -360,8 +368,7 @@ def route_logits(logits: torch.Tensor, k: int, align: int = 1, M_cap: int | None
     }
     o["err"] = _err_word(err if err is not None else o.get("err"), dev, stream)
     ws_bytes = route_workspace_size(T, k, E)
-    if workspace is None:
-        workspace = _scratch(ws_bytes, dev, stream)
+    workspace = _workspace(workspace, ws_bytes, dev, stream)
     rc = lib().moe_route_logits(_ptr(logits), T, E, k, align, M_cap, _ptr(o["topk_idx"]),
                                 _ptr(o["probs"]), _ptr(o["counts"]), _ptr(o["offsets"]),
                                 _ptr(o["row_of_pair"]), _ptr(o["pair_of_row"]),
@@ -974,8 +981,7 @@ def router_loss(logits: torch.Tensor, topk_idx: torch.Tensor, seg_offsets=None, 
             _need(o[nm], ty, nm)
             _same_shape(o[nm], shape, nm)
     o["err"] = _err_word(err if err is not None else o.get("err"), dev, stream)
-    if workspace is None:
-        workspace = _scratch(router_loss_workspace_size(T, E, S), dev, stream)
+    workspace = _workspace(workspace, router_loss_workspace_size(T, E, S), dev, stream)
     rc = lib().moe_router_loss(_ptr(logits), lt, _ptr(topk_idx), T, E, k, _ptr(seg_offsets), S,
                                _ptr(token_mask), _ptr(o["loss"]), _ptr(o["counts"]),
                                _ptr(o["lse"]), _ptr(o["n_valid"]), _ptr(workspace),
@@ -1112,8 +1118,8 @@ def grouped_linear_bwd(dout: torch.Tensor, a: torch.Tensor, offsets, B: torch.Te
         dB = _empty(B.shape, torch.bfloat16, dev, stream)
     if bias and dbias is None:
         dbias = _empty((E, N), torch.float32, dev, stream)
-    if bias and workspace is None:
-        workspace = _scratch(grouped_linear_bwd_workspace_size(E, M_cap, N), dev, stream)
+    if bias:
+        workspace = _workspace(workspace, grouped_linear_bwd_workspace_size(E, M_cap, N), dev, stream)
     err = _err_word(err, dev, stream)
     rc = lib().moe_grouped_linear_bwd(
         _ptr(dout), _ptr(z), _ptr(a), _ptr(offsets), E, M_cap, K, N, _ptr(B), layout,

@@ -136,3 +136,20 @@ def test_mlp_ckpt_calls_take_buffers_that_fit(L):
     _ckpt_bwd()
     _ckpt_bwd(dh=None, a_scaled=None, ds_part=None, dx_perm=None, dW1=None, dW2=None)
     assert L.calls == ["moe_grouped_mlp_fwd_ckpt"] * 3 + ["moe_grouped_mlp_bwd_routed_ckpt"] * 2
+
+
+@pytest.mark.parametrize("ws", [Fake(1 << 20, U8, is_cuda=False), Fake(1 << 20, U8, contiguous=False)])
+def test_workspaces_must_be_contiguous_cuda_memory(L, ws):
+    z, i = Fake((10, 8), F32), Fake((10, 2), I32)
+    _refused(L, lambda: M.router_loss(z, i, workspace=ws))
+    _refused(L, lambda: M.route_offsets(i, 8, workspace=ws))
+    _refused(L, lambda: M.route_logits(z, 2, workspace=ws))
+    x = Fake((10, 64), BF)
+    _refused(L, lambda: M.grouped_linear_bwd(x, x, None, Fake((64, 64), BF), bias=True, workspace=ws))
+
+
+def test_workspaces_of_any_type(L):
+    z, i, x = Fake((10, 8), F32), Fake((10, 2), I32), Fake((10, 64), BF)
+    M.router_loss(z, i, workspace=Fake(4096, F32))
+    M.grouped_linear_bwd(x, x, None, Fake((64, 64), BF), bias=True, workspace=Fake(4096, I32))
+    assert L.calls == ["moe_router_loss", "moe_grouped_linear_bwd"]

@@ -6,7 +6,7 @@ import os
 
 import dropless_grouped_gemm_gb300 as M
 
-MAKERS = {"_err_word": 2, "_scratch": 2, "_empty": 3}      # name: position of the stream
+MAKERS = {"_err_word": 2, "_scratch": 2, "_workspace": 3, "_empty": 3}      # name: position of the stream
 
 
 def _calls():
