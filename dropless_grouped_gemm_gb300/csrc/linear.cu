@@ -37,6 +37,7 @@
 #include <cuda_runtime.h>
 
 #include "act.cuh"
+#include "drain.cuh"
 #include "linear.cuh"
 #include "ptx.cuh"
 
@@ -240,6 +241,7 @@ __global__ void __launch_bounds__(FT, 1)
   uint64_t* drain_bar = rempty_bar + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint32_t* loads = tmem_slot + 2;    // stages loaded: by this CTA, by the pair's second
   int* s_off = reinterpret_cast<int*>(tmem_slot + 4);
   int* s_ts = s_off + (g.E + 1);
 
@@ -277,6 +279,11 @@ __global__ void __launch_bounds__(FT, 1)
     }
     if constexpr (PAIR) tma_load_2d_pair(sw + W_BYTES, &tmX, fbc, kb * FK, t.row0 + C::x_rows * sh);
     else tma_load_2d(sw + W_BYTES, &tmX, fb, kb * FK, t.row0);
+  };
+  // a role that gives up takes the pair's other CTA with it
+  auto gave_up = [&](bool ok) {
+    if (PAIR && !ok && elect_one())
+      st_cluster_u32(mapa_shared(smem_u32(const_cast<int*>(abort_flag)), crank ^ 1), 1u);
   };
   int ahead = 0;      // stages of the first unit that are already loading
 
@@ -384,22 +391,11 @@ __global__ void __launch_bounds__(FT, 1)
         if (ns == 0) phase ^= 1;
       }
     }
-    if (!ok && elect_one()) {
-      // give up: wait (bounded) for the copies in flight, the last load of
-      // each stage (a pair's second CTA, whose bytes count on the first one's
-      // barriers, waits 1 ms, far longer than a copy takes)
-      if (PAIR && sh != 0) {
-        const uint64_t t0 = globaltimer_ns();
-        while (globaltimer_ns() - t0 < 1000000ull) {}
-      } else {
-        for (uint32_t i = 0; i < NST && i < issued; ++i) {
-          const uint32_t last = issued - 1 - (issued - 1 - i) % NST;
-          const uint32_t a = smem_u32(&full_bar[i]);
-          const uint64_t t0 = globaltimer_ns();
-          while (!mbar_try_wait(a, (last / NST) & 1u) && globaltimer_ns() - t0 < kWaitLimitNs) {}
-        }
-      }
+    if (elect_one()) {
+      if (PAIR && sh != 0) st_cluster_u32(mapa_shared(smem_u32(loads + 1), crank - 1), issued);
+      else loads[0] = issued;
     }
+    gave_up(ok);
     __syncwarp();
     if constexpr (!PAIR) cluster_wait();
   } else if (warp == 1) {
@@ -461,14 +457,7 @@ __global__ void __launch_bounds__(FT, 1)
           __syncwarp();
         }
       }
-      if (!ok && elect_one()) {
-        // give up: the MMAs already issued finish before TMEM is freed
-        if constexpr (PAIR) umma_commit_pair(drain_bar);
-        else umma_commit(drain_bar);
-        const uint32_t a = smem_u32(drain_bar);
-        const uint64_t t0 = globaltimer_ns();
-        while (!mbar_try_wait(a, 0) && globaltimer_ns() - t0 < kWaitLimitNs) {}
-      }
+      gave_up(ok);
     }
     __syncwarp();
     if constexpr (!PAIR) cluster_wait();
@@ -548,6 +537,7 @@ __global__ void __launch_bounds__(FT, 1)
       if (lane < split) mbar_arrive_cluster(mapa_shared(smem_u32(rempty_bar), lane * SH + sh));
     }
     if (!joined) cluster_wait();
+    gave_up(ok);
   }
 
   tc_fence_before();
@@ -557,6 +547,33 @@ __global__ void __launch_bounds__(FT, 1)
   cluster_sync();
   if (*abort_flag && threadIdx.x == 0) set_err(g.err, MOE_DEV_TIMEOUT);
   if (warp == 1) {
+    // Given up (both CTAs of a pair, or neither): what is in flight ends
+    // (waits bounded) before TMEM is freed and shared memory left: the MMAs
+    // already issued, then the copies, a pair's on its first CTA's barriers;
+    // the second waits for the first's word.
+    if (*abort_flag && elect_one()) {
+      const uint64_t t0 = globaltimer_ns();
+      auto ends = [&](uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+        const uint32_t a = smem_u32(bar);
+        for (;;)
+          if (mbar_try_wait(a, parity) || globaltimer_ns() - t0 > limit_ns) break;
+      };
+      if (sh == 0) {
+        if constexpr (PAIR) umma_commit_pair(drain_bar);
+        else umma_commit(drain_bar);
+        ends(drain_bar, 0, kWaitLimitNs);
+        for (uint32_t i = 0; i < NST; ++i) {
+          const StageDrain d = stage_drain(loads[0], PAIR ? loads[1] : loads[0], NST, i);
+          if (d.make_up) mbar_complete_tx(&full_bar[i], C::stage_bytes);
+          if (d.arrive) mbar_arrive_expect_tx(&full_bar[i], C::stage_bytes);
+          if (d.wait) ends(&full_bar[i], d.parity, 2 * kWaitLimitNs);
+        }
+        if constexpr (PAIR) mbar_arrive_cluster(mapa_shared(smem_u32(drain_bar), crank + 1));
+      } else {
+        ends(drain_bar, 0, 3 * kWaitLimitNs);
+      }
+    }
+    __syncwarp();
     tc_fence_after();
     if constexpr (PAIR) tmem_dealloc_pair(tmem_base, C::tmem_cols);
     else tmem_dealloc(tmem_base, C::tmem_cols);

@@ -18,3 +18,12 @@ def test_arrivals_between_ctas_release():
     found = [(n, m.group(0)) for n, s in _sources()
              for m in re.finditer(r"(mbarrier|barrier\.cluster)\.arrive[.\w]*\.relaxed[.\w]*", s)]
     assert not found, found
+
+
+def test_the_few_row_kernel_waits_for_its_copies():
+    """A CTA that gives up leaves after its copies have landed (a bounded wait
+    on their barriers), not after some time."""
+    src = dict(_sources())["linear.cu"]
+    assert "stage_drain(" in src
+    spins = re.findall(r"while \(globaltimer_ns\(\)[^;{]*\)\s*(?:\{\s*\}|;)", src)
+    assert not spins, spins
