@@ -38,7 +38,7 @@ __all__ = [
     "grouped_mlp_bwd_routed_gather", "route_logits", "FLAG_MX_SEPARATE_DH_QUANT",
     "mx_bwd_workspace_layout", "set_pair_mma",
     "LINEAR_ACT", "router_loss", "router_loss_bwd", "router_loss_workspace_size", "grouped_linear",
-    "grouped_linear_bwd", "grouped_linear_bwd_workspace_size", "checkpoint_pack",
+    "grouped_linear_bwd", "grouped_linear_bwd_workspace_size", "grouped_linear_plan", "checkpoint_pack",
     "checkpoint_unpack", "permute_checkpoint", "grouped_mlp_fwd_ckpt",
     "grouped_mlp_bwd_routed_ckpt",
 ]
@@ -169,6 +169,8 @@ def lib():
         L.moe_grouped_linear.restype = i32
         L.moe_grouped_linear.argtypes = [vp, vp, i32, i32, i32, i32, vp, i32, vp, i32, vp, vp, vp,
                                          i32, vp, vp]
+        L.moe_grouped_linear_plan.restype = i32
+        L.moe_grouped_linear_plan.argtypes = [i32, i32, i32, i32, i32, i32, vp]
         L.moe_grouped_linear_bwd_workspace_size.restype = sz
         L.moe_grouped_linear_bwd_workspace_size.argtypes = [i32, i32, i32]
         L.moe_grouped_linear_bwd.restype = i32
@@ -1078,6 +1080,18 @@ def grouped_linear(a: torch.Tensor, offsets, B: torch.Tensor, act: str = "none",
                                   ot, _ptr(err), _stream(stream))
     _check(rc, "moe_grouped_linear")
     return out, z, err
+
+
+def grouped_linear_plan(E: int, M_cap: int, K: int, N: int, ragged: bool,
+                        out_dtype=torch.bfloat16) -> tuple:
+    """Which kernel ``grouped_linear`` runs for these sizes
+    (moe_grouped_linear_plan): (tokens of a few-row tile or 0 for the grouped
+    GEMM, parts of the reduction, whether two CTAs share a tile)."""
+    plan = (ctypes.c_int * 3)()
+    rc = lib().moe_grouped_linear_plan(E, M_cap, K, N, int(ragged), _float_type(out_dtype, "out"),
+                                       ctypes.byref(plan))
+    _check(rc, "moe_grouped_linear_plan")
+    return plan[0], plan[1], bool(plan[2])
 
 
 def grouped_linear_bwd_workspace_size(E: int, M_cap: int, N: int) -> int:

@@ -1253,6 +1253,25 @@ int moe_grouped_linear(const moe_bf16* a, const int32_t* offsets, int E, int M_c
   return MOE_OK;
 }
 
+int moe_grouped_linear_plan(int E, int M_cap, int K, int N, int ragged, int out_type,
+                            int plan[3]) {
+  if (ragged != 0 && ragged != 1) return MOE_E_ARG;
+  static const int32_t some = 0;    // (a non-NULL address: offsets or none)
+  const int rc = check_linear(ragged ? &some : nullptr, E, M_cap, K, N, MOE_B_KN, MOE_ACT_NONE);
+  if (rc) return rc;
+  if (M_cap == 0) return MOE_E_SIZE;
+  if (out_type != MOE_TYPE_F32 && out_type != MOE_TYPE_BF16) return MOE_E_ARG;
+  if (!plan) return MOE_E_NULL;
+  const int sms = num_sms_current();
+  if (sms <= 0) return MOE_E_CUDA;
+  const moe::FewPlan p =
+      moe::few_plan(E, M_cap, K, N, ragged != 0, out_type == MOE_TYPE_F32, sms);
+  plan[0] = p.tn;
+  plan[1] = p.tn ? p.split : 1;
+  plan[2] = p.tn && p.pair ? 1 : 0;
+  return MOE_OK;
+}
+
 size_t moe_grouped_linear_bwd_workspace_size(int E, int M_cap, int N) {
   if (E < 1 || E > MOE_MAX_EXPERTS || M_cap < 0 || N <= 0) return 0;
   return moe::linear_dz_workspace_bytes(E, M_cap, N);

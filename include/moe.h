@@ -781,6 +781,16 @@ int moe_grouped_linear(const moe_bf16* a, const int32_t* offsets, int E, int M_c
                        int32_t* err, void* stream);
 
 /*
+ * moe_grouped_linear_plan - which kernel moe_grouped_linear runs for a product
+ * of these sizes (ragged: 1 with offsets, 0 without) on the current device:
+ * plan[0] the tokens of a tile of the few-row kernel (0: the 128 x 256 or 256
+ * x 256 tiles of the grouped GEMM), plan[1] the parts that the reduction is
+ * split into, plan[2] 1 if two CTAs share a tile of the few-row kernel.  Host
+ * memory; nothing is launched.  For tests and measurements.
+ */
+int moe_grouped_linear_plan(int E, int M_cap, int K, int N, int ragged, int out_type, int plan[3]);
+
+/*
  * moe_grouped_linear_bwd - its backward ([CuTe] kernel family "GroupGemm +
  * dActivation").
  *   dz = act'(z) dout           (bf16; act NONE: dout itself, dz unused)
