@@ -224,6 +224,17 @@ int check_loss(int T, int E, int k, const int32_t* seg, int S, int type) {
   return MOE_OK;
 }
 
+// What the router losses' kernels load or store at a time: 16 bytes of logits
+// where rows are whole numbers of them (and as many gradients), else a value.
+// A contiguous part of a batch begins at any row.
+bool loss_misaligned(const void* logits, int type, const void* dlogits, int dtype, int E) {
+  const size_t in = type == MOE_TYPE_BF16 ? 2 : 4, out = dtype == MOE_TYPE_BF16 ? 2 : 4;
+  const size_t vec = E % static_cast<int>(16 / in) == 0 ? 16 / in : 1;
+  const size_t store = vec * out < 16 ? vec * out : 16;
+  return reinterpret_cast<uintptr_t>(logits) % (vec * in) != 0 ||
+         reinterpret_cast<uintptr_t>(dlogits) % store != 0;
+}
+
 bool linear_gated(int act) { return act == MOE_ACT_SWIGLU || act == MOE_ACT_GEGLU; }
 
 int check_linear(const int32_t* offsets, int E, int M_cap, int K, int N, int b_layout, int act) {
@@ -1147,7 +1158,7 @@ int moe_router_loss(const void* logits, int logits_type, const int32_t* topk_idx
   if (rc) return rc;
   if (!loss || !counts || !n_valid || !err) return MOE_E_NULL;
   if (T > 0 && (!logits || !topk_idx || !lse)) return MOE_E_NULL;
-  if (misaligned(logits)) return MOE_E_ALIGN;
+  if (loss_misaligned(logits, logits_type, nullptr, logits_type, E)) return MOE_E_ALIGN;
   if (ws_bytes < moe::router_loss_workspace_bytes(T, E, S)) return MOE_E_WORKSPACE;
   if (!workspace) return MOE_E_NULL;
   if (misaligned(workspace)) return MOE_E_ALIGN;
@@ -1179,7 +1190,7 @@ int moe_router_loss_bwd(const void* logits, int logits_type, const int32_t* topk
   if (T == 0) return MOE_OK;
   if (!logits || !topk_idx || !lse || !counts || !n_valid || !dloss || !dlogits) return MOE_E_NULL;
   if ((probs == nullptr) != (dprobs == nullptr)) return MOE_E_NULL;
-  if (misaligned(logits) || misaligned(dlogits)) return MOE_E_ALIGN;
+  if (loss_misaligned(logits, logits_type, dlogits, dlogits_type, E)) return MOE_E_ALIGN;
   const int sms = num_sms_current();
   if (sms <= 0) return MOE_E_CUDA;
   moe::RouterLossArgs a{};

@@ -700,7 +700,8 @@ int moe_mx_quantize_tiled(const moe_bf16* src, int rows, int cols,
  * per-expert counts behind them ([TE] "용량 기반 MoE와 드롭리스 MoE": without a
  * capacity nothing but training keeps the experts' loads even; the losses
  * themselves are the common ones, the pages do not fix them).
- *   logits      [T, E] float32 or bf16 (logits_type MOE_TYPE_*)
+ *   logits      [T, E] float32 or bf16 (logits_type MOE_TYPE_*), 16-byte
+ *               aligned where a row is a multiple of 16 bytes, else to its type
  *   topk_idx    [T, k] int32, as moe_router_topk writes it (-1: no route; a
  *               valid token's other ids outside [0, E) are skipped and set
  *               MOE_DEV_BAD_EXPERT)
@@ -744,7 +745,8 @@ int moe_router_loss(const void* logits, int logits_type, const int32_t* topk_idx
  * of both of its sums).  An expert chosen twice by a token gets both terms.
  *   lse, counts, n_valid: as moe_router_loss wrote them; dloss [2] float32
  *   (device); probs, dprobs [T, k] float32 or both NULL; dlogits [T, E]
- *   float32 or bf16.  One launch.
+ *   float32 or bf16, aligned as the logits (bf16 of float32 logits: 8 bytes).
+ *   One launch.
  */
 int moe_router_loss_bwd(const void* logits, int logits_type, const int32_t* topk_idx, int T, int E,
                         int k, const int32_t* seg_offsets, int S, const uint8_t* token_mask,
