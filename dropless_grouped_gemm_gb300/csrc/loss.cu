@@ -575,11 +575,13 @@ __global__ void __launch_bounds__(kBwdThreads) loss_bwd(const RouterLossArgs a, 
     // row's maximum past that (always the maximum: 34.7 us for 65,536 x 256,
     // 32.9 with lse).  An empty or masked token's values are dropped below.
     float shift = lse;
-    if (__any_sync(0xffffffffu, !(fabsf(lse) < 1048576.f))) {
-      shift = v[0];
+    const bool far = !(fabsf(lse) < 1048576.f);
+    if (__any_sync(0xffffffffu, far)) {
+      float m = v[0];
 #pragma unroll
-      for (int i = 1; i < NV; ++i) shift = fmaxf(shift, v[i]);
-      shift = group_max<L>(shift);
+      for (int i = 1; i < NV; ++i) m = fmaxf(m, v[i]);
+      m = group_max<L>(m);
+      if (far) shift = m;     // this row's alone: no row's bits depend on its neighbours
     }
     float tot = 0.f, dot = 0.f;
 #pragma unroll

@@ -135,3 +135,25 @@ def test_gradient_takes_the_corrected_offsets(off):
     for n in ("loss", "counts", "n_valid", "lse"):
         assert torch.equal(a[n], b[n]), n
     assert torch.equal(ga, gb)
+
+
+@pytest.mark.parametrize("E,dtype", [(8, torch.float32), (60, torch.bfloat16), (200, torch.float32)])
+def test_a_row_s_gradient_does_not_depend_on_its_neighbours(E, dtype):
+    """Ordinary rows beside large, empty and NaN ones: the same bits."""
+    import dropless_grouped_gemm_gb300 as M
+    T, k = 64, 2
+    rng = np.random.default_rng(E)
+    z = torch.from_numpy(rng.standard_normal((T, E)) * 3.0).to(dtype).cuda()
+    idx = z.float().topk(k).indices.int()
+    mask = torch.ones(T, dtype=torch.uint8, device="cuda")
+    odd = torch.arange(1, T, 2, device="cuda")
+    mask[odd] = 0
+    other = z.clone()
+    other[odd] = torch.tensor([-1e30, float("-inf"), float("nan"), 1e9], device="cuda").to(dtype).repeat(8)[:, None]
+    dl = _cuda(np.array([1.0, 0.5], np.float32))
+    g = []
+    for x in (z, other):
+        r = M.router_loss(x, idx, token_mask=mask)
+        g.append(M.router_loss_bwd(x, idx, r, dl, token_mask=mask))
+    torch.cuda.synchronize()
+    assert torch.equal(g[0], g[1])
