@@ -606,7 +606,8 @@ __global__ void __launch_bounds__(kBwdThreads) loss_bwd(const RouterLossArgs a, 
       // the group's row in shared memory: each pair leaves its number at its
       // expert and reads it back, so that an expert chosen twice shows; such
       // tokens (no router makes them) take their pairs one after another.
-      // (__match_any_sync in place of the numbers: 34.2 us against 31.7.)
+      // (__match_any_sync in place of the numbers: 34.2 us against 31.7, both
+      // before the row's sum was taken.)
       float* add = s_add + (warp * G + grp) * a.E;
       int* tag = reinterpret_cast<int*>(add);
       for (int j0 = 0; j0 < a.k; j0 += L) {
@@ -718,7 +719,7 @@ cudaError_t go(const RouterLossArgs& a, int num_sms, cudaStream_t s, bool bwd, i
 // forward, bound by its instructions, takes 16 values a lane and half the
 // lanes, which halves the shuffles and the per-token work (65,536 x 256: 26.4
 // -> 22.0 us); the backward, which also holds the counts, 8 (31.7 us, 33.9
-// with 16).
+// with 16, both before the row's sum was taken; 33 with it).
 template <class T, int VEC>
 cudaError_t pick(const RouterLossArgs& a, int num_sms, cudaStream_t s, bool bwd, int chunk,
                  const Ws& w) {

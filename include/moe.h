@@ -795,7 +795,8 @@ int moe_grouped_linear_plan(int E, int M_cap, int K, int N, int ragged, int out_
 /*
  * moe_grouped_linear_bwd - its backward ([CuTe] kernel family "GroupGemm +
  * dActivation").
- *   dz = act'(z) dout           (bf16; act NONE: dout itself, dz unused)
+ *   dz = act'(z) dout           (bf16, which both products read; act NONE:
+ *                               dout itself, dz unused)
  *   da = dz B_e^T               bf16 [M_cap, K], or NULL: not wanted
  *   dB_e = a_e^T dz_e           bf16 in B's layout (zero for experts with no
  *                               rows), or NULL
@@ -852,7 +853,8 @@ int moe_permute_checkpoint(const uint8_t* q, const uint8_t* s, const int32_t* ro
  * moe_grouped_mlp_bwd_routed_ckpt - moe_grouped_mlp_bwd_routed from that
  * checkpoint: FC2-dgrad's epilogue reads h_q / h_s, and every result equals
  * moe_grouped_mlp_bwd_routed's on the unpacked H bit for bit.
- * Arguments, sizes and errors as there; all pointers 16-byte aligned.
+ * Arguments, sizes and errors as there; all pointers 16-byte aligned.  The
+ * unrouted backward, the gather-fused calls and the MXFP8 ones keep H in bf16.
  */
 int moe_grouped_mlp_fwd_ckpt(const moe_bf16* x_perm, const int32_t* offsets, int E, int M_cap,
                              int d, int n, const moe_bf16* W1, const moe_bf16* W2, int act,
