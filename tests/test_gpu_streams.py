@@ -179,3 +179,28 @@ def test_workspaces_are_not_reused_while_the_call_is_still_queued():
     del keep, junk
     for x, y in zip(got[:4], want[:4]):
         assert torch.equal(x, y)
+
+
+def test_a_call_on_a_forked_stream_captures():
+    """Everything that the call makes lies in the graph's memory, the zeroing
+    of its error word in the graph."""
+    import dropless_grouped_gemm_gb300 as M_
+    E, M, K, N, off, a, B, z, dout = _linear_case()
+    want = M_.grouped_linear_bwd(dout, a, off, B, "silu", z, True)
+    bad = cuda_i32([0, 400, 100, 400])
+    torch.cuda.synchronize()
+    main, side, g = torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=main):
+        side.wait_stream(main)
+        got = M_.grouped_linear_bwd(dout, a, off, B, "silu", z, True, stream=side)
+        _, _, err = M_.grouped_linear(a, bad, B, stream=side)
+        main.wait_stream(side)
+    for _ in range(2):
+        for t in got[:4]:
+            t.zero_()
+        err.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert int(got[4].item()) == 0 and int(err.item()) == M_.DEV_BAD_OFFSETS
+        for x, y in zip(got[:4], want[:4]):
+            assert torch.equal(x, y)
