@@ -13,7 +13,11 @@ Functions mirror the C ABI in ``include/moe.h``:
     grouped_mlp_fwd    -> moe_grouped_mlp_fwd
     grouped_mlp_bwd    -> moe_grouped_mlp_bwd
     router_loss        -> moe_router_loss (and router_loss_bwd)
+    router_select      -> moe_router_select (and router_select_bwd)
     grouped_linear     -> moe_grouped_linear (and grouped_linear_bwd)
+    fp4_quantize       -> moe_fp4_quantize (and fp4_tensor_scale, fp4_permute,
+                          fp4_quantize_weights, fp4_dequantize)
+    fp4_linear         -> moe_fp4_linear (and fp4_linear_bwd)
     checkpoint_pack    -> moe_checkpoint_pack (and checkpoint_unpack,
                           permute_checkpoint, grouped_mlp_fwd_ckpt,
                           grouped_mlp_bwd_routed_ckpt)
@@ -41,10 +45,16 @@ __all__ = [
     "grouped_linear_bwd", "grouped_linear_bwd_workspace_size", "grouped_linear_plan", "checkpoint_pack",
     "checkpoint_unpack", "permute_checkpoint", "grouped_mlp_fwd_ckpt",
     "grouped_mlp_bwd_routed_ckpt",
+    "SCORE", "router_select", "router_select_bwd",
+    "FP4", "fp4_scale_bytes", "fp4_tensor_scale", "fp4_quantize", "fp4_permute",
+    "fp4_quantize_weights", "fp4_dequantize", "fp4_linear", "fp4_linear_plan", "fp4_linear_bwd",
+    "fp4_linear_bwd_workspace_size",
 ]
 
 ACT = {"swiglu": 0, "geglu": 1, "srelu": 2}
 LINEAR_ACT = {**ACT, "none": 3, "relu": 4, "silu": 5, "gelu": 6}
+SCORE = {"softmax": 0, "sigmoid": 1}
+FP4 = {"nvfp4": 0, "mxfp4": 1}
 FLAG_SAVE_H = 1
 FLAG_MXFP8 = 2
 FLAG_ACCUMULATE_DW = 4
@@ -166,6 +176,37 @@ def lib():
         L.moe_router_loss_bwd.restype = i32
         L.moe_router_loss_bwd.argtypes = [vp, i32, vp, i32, i32, i32, vp, i32, vp, vp, vp, vp, vp,
                                           vp, vp, vp, i32, vp]
+        f32 = ctypes.c_float
+        L.moe_router_select.restype = i32
+        L.moe_router_select.argtypes = [vp, i32, i32, i32, i32, i32, vp, i32, i32, i32, i32, f32,
+                                        vp, vp, vp]
+        L.moe_router_select_bwd.restype = i32
+        L.moe_router_select_bwd.argtypes = [vp, i32, vp, vp, vp, i32, i32, i32, i32, i32, f32,
+                                            i32, vp, i32, vp]
+        i64 = ctypes.c_longlong
+        L.moe_fp4_scale_bytes.restype = sz
+        L.moe_fp4_scale_bytes.argtypes = [i64, i32, i32, i32]
+        L.moe_fp4_tensor_scale.restype = i32
+        L.moe_fp4_tensor_scale.argtypes = [vp, i32, i64, vp, vp]
+        L.moe_fp4_quantize.restype = i32
+        L.moe_fp4_quantize.argtypes = [vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp]
+        L.moe_fp4_permute.restype = i32
+        L.moe_fp4_permute.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp, vp, vp,
+                                      vp]
+        L.moe_fp4_quantize_weights.restype = i32
+        L.moe_fp4_quantize_weights.argtypes = [vp, i32, i32, i32, i32, i32, vp, vp, vp, vp]
+        L.moe_fp4_dequantize.restype = i32
+        L.moe_fp4_dequantize.argtypes = [vp, vp, vp, i32, i64, i32, i32, vp, i32, vp, i32, vp, vp]
+        L.moe_fp4_linear.restype = i32
+        L.moe_fp4_linear.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, i32, vp, i32,
+                                     vp, vp, vp, i32, vp, vp, vp, vp]
+        L.moe_fp4_linear_plan.restype = i32
+        L.moe_fp4_linear_plan.argtypes = [i32, i32, i32, i32, i32, vp]
+        L.moe_fp4_linear_bwd_workspace_size.restype = sz
+        L.moe_fp4_linear_bwd_workspace_size.argtypes = [i32, i32, i32, i32]
+        L.moe_fp4_linear_bwd.restype = i32
+        L.moe_fp4_linear_bwd.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, i32, i32,
+                                         i32, i32, vp, vp, vp, vp, vp, sz, vp, vp]
         L.moe_grouped_linear.restype = i32
         L.moe_grouped_linear.argtypes = [vp, vp, i32, i32, i32, i32, vp, i32, vp, i32, vp, vp, vp,
                                          i32, vp, vp]
@@ -1025,6 +1066,71 @@ def router_loss_bwd(logits: torch.Tensor, topk_idx: torch.Tensor, fwd: dict, dlo
     return dlogits
 
 
+# ----------------------------------------------------------------- choice by scores
+
+def _select_args(logits, score):
+    lt = _float_type(logits.dtype, "logits")
+    _need(logits, logits.dtype, "logits", 2)
+    if score not in SCORE:
+        raise MoeError(f"score must be one of {sorted(SCORE)}, got {score!r}")
+    return lt, logits.shape[0], logits.shape[1]
+
+
+def router_select(logits: torch.Tensor, k: int, score: str = "softmax", bias=None, groups: int = 1,
+                  top_groups: int | None = None, group_best: int = 1, renorm: bool = True,
+                  scale: float = 1.0, topk_idx=None, probs=None, stream=None):
+    """The router's choice by scores (moe_router_select): "softmax" over all
+    experts or "sigmoid"; ``bias`` [E] float32 moves the choice alone; of
+    ``groups`` groups of experts the ``top_groups`` (None: all) best by the
+    sum of their ``group_best`` largest scores stay; the weights are
+    renormalised over the k chosen (``renorm``) and multiplied by ``scale``.
+    Returns (topk_idx int32 [T, k], probs float32 [T, k])."""
+    lt, T, E = _select_args(logits, score)
+    _need(bias, torch.float32, "bias", 1)
+    _same_shape(bias, (E,), "bias")
+    _buffers((topk_idx, torch.int32, "topk_idx", (T, k)), (probs, torch.float32, "probs", (T, k)))
+    if topk_idx is None:
+        topk_idx = _empty((T, k), torch.int32, logits.device, stream)
+    if probs is None:
+        probs = _empty((T, k), torch.float32, logits.device, stream)
+    rc = lib().moe_router_select(_ptr(logits), lt, T, E, k, SCORE[score], _ptr(bias), groups,
+                                 groups if top_groups is None else top_groups, group_best,
+                                 int(bool(renorm)), scale, _ptr(topk_idx), _ptr(probs),
+                                 _stream(stream))
+    _check(rc, "moe_router_select")
+    return topk_idx, probs
+
+
+def router_select_bwd(logits: torch.Tensor, topk_idx: torch.Tensor, probs: torch.Tensor,
+                      dprobs: torch.Tensor, score: str = "softmax", renorm: bool = True,
+                      scale: float = 1.0, dlogits=None, dtype=None, accumulate: bool = False,
+                      stream=None) -> torch.Tensor:
+    """Gradient of the logits from the weights' gradient dprobs [T, k]
+    (moe_router_select_bwd).  dtype: of dlogits (float32, or bf16);
+    accumulate adds to the given dlogits (``router_loss_bwd``'s, say)."""
+    lt, T, E = _select_args(logits, score)
+    _need(topk_idx, torch.int32, "topk_idx", 2)
+    k = topk_idx.shape[1]
+    if accumulate and dlogits is None:
+        raise ValueError("accumulate needs the dlogits to accumulate into")
+    _buffers((topk_idx, torch.int32, "topk_idx", (T, k)), (probs, torch.float32, "probs", (T, k)),
+             (dprobs, torch.float32, "dprobs", (T, k)))
+    if probs is None or dprobs is None:
+        raise MoeError("probs and dprobs are needed")
+    if dlogits is None:
+        ot = _float_type(dtype or torch.float32, "dlogits")
+        dlogits = _empty((T, E), dtype or torch.float32, logits.device, stream)
+    else:
+        ot = _float_type(dlogits.dtype, "dlogits")
+        _need(dlogits, dlogits.dtype, "dlogits", 2)
+        _same_shape(dlogits, (T, E), "dlogits")
+    rc = lib().moe_router_select_bwd(_ptr(logits), lt, _ptr(topk_idx), _ptr(probs), _ptr(dprobs),
+                                     T, E, k, SCORE[score], int(bool(renorm)), scale,
+                                     int(bool(accumulate)), _ptr(dlogits), ot, _stream(stream))
+    _check(rc, "moe_router_select_bwd")
+    return dlogits
+
+
 # ----------------------------------------------------------------- linear
 
 def _linear_args(a, offsets, B, act, b_layout):
@@ -1142,6 +1248,325 @@ def grouped_linear_bwd(dout: torch.Tensor, a: torch.Tensor, offsets, B: torch.Te
         0 if workspace is None else workspace.numel() * workspace.element_size(), _ptr(err),
         _stream(stream))
     _check(rc, "moe_grouped_linear_bwd")
+    return (dout if act == "none" else dz), da, dB, dbias, err
+
+
+# ----------------------------------------------------------------- 4 bits
+# A tensor in 4 bits is a pair (q, s): packed codes and scale bytes (uint8).
+
+def _fp4_format(fmt):
+    if fmt not in FP4:
+        raise MoeError(f"fmt must be one of {sorted(FP4)}, got {fmt!r}")
+    return FP4[fmt]
+
+
+def fp4_scale_bytes(rows: int, E: int, K: int, fmt: str = "nvfp4") -> int:
+    """Bytes of the scales of E experts' ``rows`` rows of K values (moe_fp4_scale_bytes)."""
+    return int(lib().moe_fp4_scale_bytes(rows, E, K, _fp4_format(fmt)))
+
+
+def _fp4_t(t, n, fmt, name):
+    _need(t, torch.float32, name)
+    if t is not None and fmt != "nvfp4":
+        raise MoeError(f"{name}: only nvfp4 has a tensor scale")
+    if t is not None and t.numel() != n:
+        raise MoeError(f"{name} must hold {n} values, got {t.numel()}")
+
+
+def _fp4_offsets(offsets):
+    _need(offsets, torch.int32, "offsets", 1)
+    if offsets is not None and offsets.numel() < 2:
+        raise MoeError("offsets must hold at least 2 entries")
+    return 1 if offsets is None else offsets.numel() - 1
+
+
+def _fp4_pair(x, name):
+    if not isinstance(x, (tuple, list)) or len(x) != 2:
+        raise MoeError(f"{name} must be a pair (codes, scales)")
+    for t in x:
+        if t is None:
+            raise MoeError(f"{name} must be a pair (codes, scales)")
+        _need(t, torch.uint8, name)
+    return x
+
+
+def _fp4_out(out, q_shape, rows, E, K, fmt, device, stream):
+    """The (q, s) to write: the given pair, or a new one."""
+    n = fp4_scale_bytes(rows, E, K, fmt)
+    if out is None:
+        return (_empty(q_shape, torch.uint8, device, stream),
+                _empty(n, torch.uint8, device, stream))
+    q, s = _fp4_pair(out, "out")
+    _same_shape(q, q_shape, "out's codes")
+    if s.numel() != n:
+        raise MoeError(f"out's scales must hold {n} bytes, got {s.numel()}")
+    return q, s
+
+
+def _fp4_width(K, name):
+    if K <= 0 or K % 64:
+        raise MoeError(f"{name} must have a multiple of 64 columns, got {K}")
+
+
+def fp4_tensor_scale(src: torch.Tensor, per_expert: bool = False, t=None, stream=None):
+    """nvfp4's scale of a bf16 tensor (moe_fp4_tensor_scale): float32 [1], or
+    with ``per_expert`` [E], one for each src[e]: the smallest power of two t
+    with max|v| <= 6 * 448 t."""
+    _need(src, torch.bfloat16, "src")
+    E = src.shape[0] if per_expert else 1
+    n = src.numel() // max(E, 1)
+    _buffers((t, torch.float32, "t", (E,)))
+    if t is None:
+        t = _empty(E, torch.float32, src.device, stream)
+    rc = lib().moe_fp4_tensor_scale(_ptr(src), E, n, _ptr(t), _stream(stream))
+    _check(rc, "moe_fp4_tensor_scale")
+    return t
+
+
+def fp4_quantize(src: torch.Tensor, offsets=None, fmt: str = "nvfp4", scale=None, out=None,
+                 err=None, stream=None):
+    """Rows [rows, K] bf16 in 4 bits (moe_fp4_quantize): "nvfp4" (``scale``:
+    its float32 tensor scale, None: 1) or "mxfp4"; ``offsets`` [E+1] of the
+    experts' rows (None: one block of rows).  Returns (q, s): codes [rows,
+    K/2] and scales, both uint8."""
+    f = _fp4_format(fmt)
+    _need(src, torch.bfloat16, "src", 2)
+    E = _fp4_offsets(offsets)
+    rows, K = src.shape
+    _fp4_width(K, "src")
+    _fp4_t(scale, 1, fmt, "scale")
+    q, s = _fp4_out(out, (rows, K // 2), rows, E, K, fmt, src.device, stream)
+    err = _err_word(err, src.device, stream)
+    rc = lib().moe_fp4_quantize(_ptr(src), _ptr(offsets), E, rows, K, f, _ptr(scale), _ptr(q),
+                                _ptr(s), _ptr(err), _stream(stream))
+    _check(rc, "moe_fp4_quantize")
+    return q, s
+
+
+def fp4_permute(src: torch.Tensor, pair_of_row: torch.Tensor, k: int, offsets: torch.Tensor,
+                fmt: str = "nvfp4", scale=None, row_of_pair=None, out=None, err=None, stream=None):
+    """``permute`` into 4 bits (moe_fp4_permute): token rows [T, K] bf16 to
+    expert-major rows, zeros for pad rows; with row_of_pair each token is read
+    and quantised once.  Returns (q, s)."""
+    f = _fp4_format(fmt)
+    _need(src, torch.bfloat16, "src", 2)
+    _need(pair_of_row, torch.int32, "pair_of_row", 1)
+    _need(row_of_pair, torch.int32, "row_of_pair", 1)
+    if offsets is None or pair_of_row is None:
+        raise MoeError("the routing layout's offsets and pair_of_row are needed")
+    E = _fp4_offsets(offsets)
+    T, K = src.shape
+    _fp4_width(K, "src")
+    _fp4_t(scale, 1, fmt, "scale")
+    if row_of_pair is not None and row_of_pair.numel() != T * k:
+        raise MoeError("row_of_pair must hold T*k entries")
+    M_cap = pair_of_row.numel()
+    q, s = _fp4_out(out, (M_cap, K // 2), M_cap, E, K, fmt, src.device, stream)
+    err = _err_word(err, src.device, stream)
+    rc = lib().moe_fp4_permute(_ptr(src), _ptr(row_of_pair), _ptr(pair_of_row), _ptr(offsets), E, T,
+                               k, K, M_cap, f, _ptr(scale), _ptr(q), _ptr(s), _ptr(err),
+                               _stream(stream))
+    _check(rc, "moe_fp4_permute")
+    return q, s
+
+
+def fp4_quantize_weights(W: torch.Tensor, fmt: str = "nvfp4", along: str = "rows", scale=None,
+                         out=None, stream=None):
+    """Weights [E, rows, cols] (or [rows, cols]) bf16 in 4 bits
+    (moe_fp4_quantize_weights).  along "rows": blocks along rows, for a
+    product that contracts them (W [E, K, N] in the forward), codes [E, cols,
+    rows/2]; "cols": along cols (its data gradient, or W stored [E, N, K]),
+    codes [E, rows, cols/2].  scale float32 [E] or None.  Returns (q, s)."""
+    f = _fp4_format(fmt)
+    _need(W, torch.bfloat16, "W")
+    if along not in ("rows", "cols"):
+        raise MoeError(f"along must be 'rows' or 'cols', got {along!r}")
+    if W.dim() not in (2, 3):
+        raise MoeError("W must have 2 or 3 dims")
+    E = W.shape[0] if W.dim() == 3 else 1
+    R, C = W.shape[-2:]
+    N, K = (C, R) if along == "rows" else (R, C)
+    _fp4_width(R, "W's transpose")
+    _fp4_width(C, "W")
+    _fp4_t(scale, E, fmt, "scale")
+    q, s = _fp4_out(out, (E, N, K // 2), E * N, E, K, fmt, W.device, stream)
+    rc = lib().moe_fp4_quantize_weights(_ptr(W), E, R, C, 1 if along == "rows" else 0, f,
+                                        _ptr(scale), _ptr(q), _ptr(s), _stream(stream))
+    _check(rc, "moe_fp4_quantize_weights")
+    return q, s
+
+
+def fp4_dequantize(x, offsets=None, fmt: str = "nvfp4", scale=None, dtype=torch.bfloat16, out=None,
+                   err=None, stream=None) -> torch.Tensor:
+    """The values of (q, s) (moe_fp4_dequantize), bf16 or float32: rows [rows,
+    K] (offsets as they were quantised with, scale [1]) or weights [E, N, K]
+    (scale [E]).  Rows outside every expert are not written."""
+    f = _fp4_format(fmt)
+    q, s = _fp4_pair(x, "x")
+    if q.dim() not in (2, 3) or (q.dim() == 3 and offsets is not None):
+        raise MoeError("codes must be [rows, K/2], or [E, N, K/2] without offsets")
+    E = q.shape[0] if q.dim() == 3 else _fp4_offsets(offsets)
+    K = q.shape[-1] * 2
+    rows = q.numel() // max(K // 2, 1)
+    _fp4_width(K, "x")
+    _fp4_t(scale, E if q.dim() == 3 else 1, fmt, "scale")
+    if s.numel() != fp4_scale_bytes(rows, E, K, fmt):
+        raise MoeError("x's scales do not fit its codes")
+    shape = tuple(q.shape[:-1]) + (K,)
+    if out is None:
+        ot = _float_type(dtype, "out")
+        out = _empty(shape, dtype, q.device, stream)
+    else:
+        ot = _float_type(out.dtype, "out")
+        _need(out, out.dtype, "out")
+        _same_shape(out, shape, "out")
+    err = _err_word(err, q.device, stream)
+    rc = lib().moe_fp4_dequantize(_ptr(q), _ptr(s), _ptr(offsets), E, rows, K, f, _ptr(scale),
+                                  1 if q.dim() == 3 else 0, _ptr(out), ot, _ptr(err),
+                                  _stream(stream))
+    _check(rc, "moe_fp4_dequantize")
+    return out
+
+
+def _fp4_linear_args(q, offsets, wq, act):
+    if act not in LINEAR_ACT:
+        raise MoeError(f"act must be one of {sorted(LINEAR_ACT)}, got {act!r}")
+    if q.dim() != 2 or wq.dim() != 3:
+        raise MoeError("a's codes must have 2 dims and w's 3")
+    E, N, K2 = wq.shape
+    if _fp4_offsets(offsets) != E or q.shape[1] != K2:
+        raise MoeError("inconsistent shapes")
+    gated = act in ("swiglu", "geglu")
+    return E, q.shape[0], 2 * K2, N, (N // 2 if gated else N)
+
+
+def fp4_linear(a, offsets, w, fmt: str = "nvfp4", act: str = "none", bias=None, residual=None,
+               save_z: bool = False, out=None, z=None, out_dtype=torch.bfloat16, a_scale=None,
+               w_scale=None, out_scale=None, err=None, stream=None):
+    """out = act(a w_e^T + bias_e) + residual of operands in 4 bits
+    (moe_fp4_linear).  a: (q, s) of ``fp4_quantize`` or ``fp4_permute`` with
+    these offsets (None: one expert); w: (q, s) of ``fp4_quantize_weights``,
+    codes [E, N, K/2]; a_scale [1], w_scale [E]: the tensor scales they were
+    quantised with.  act, bias, residual, z as in ``grouped_linear``.
+    out_dtype: bf16, float32, or "fp4": then out is the (q, s) that the next
+    product takes (out_scale [1]: its tensor scale, None: 1).  Returns (out,
+    z, err)."""
+    f = _fp4_format(fmt)
+    q, s = _fp4_pair(a, "a")
+    wq, ws = _fp4_pair(w, "w")
+    E, M_cap, K, N, n_out = _fp4_linear_args(q, offsets, wq, act)
+    _fp4_width(K, "a")
+    if s.numel() != fp4_scale_bytes(M_cap, E, K, fmt) or ws.numel() != fp4_scale_bytes(E * N, E, K, fmt):
+        raise MoeError("scales do not fit their codes")
+    _fp4_t(a_scale, 1, fmt, "a_scale")
+    _fp4_t(w_scale, E, fmt, "w_scale")
+    _need(bias, torch.bfloat16, "bias")
+    _need(residual, torch.bfloat16, "residual")
+    if bias is not None and bias.numel() != E * N:
+        raise MoeError("bias must hold E*N values")
+    _same_shape(residual, (M_cap, n_out), "residual")
+    out_s = None
+    if out_dtype == "fp4" or isinstance(out, (tuple, list)):
+        _fp4_t(out_scale, 1, fmt, "out_scale")
+        _fp4_width(n_out, "out")
+        out, out_s = _fp4_out(out, (M_cap, n_out // 2), M_cap, E, n_out, fmt, q.device, stream)
+        ot = 2
+    else:
+        if out_scale is not None:
+            raise MoeError("out_scale is of a 4-bit output")
+        if out is None:
+            ot = _float_type(out_dtype, "out")
+            out = _empty((M_cap, n_out), out_dtype, q.device, stream)
+        else:
+            ot = _float_type(out.dtype, "out")
+            _need(out, out.dtype, "out")
+            _same_shape(out, (M_cap, n_out), "out")
+    if z is not None:
+        _need(z, torch.bfloat16, "z")
+        _same_shape(z, (M_cap, N), "z")
+    elif save_z:
+        z = _empty((M_cap, N), torch.bfloat16, q.device, stream)
+    err = _err_word(err, q.device, stream)
+    rc = lib().moe_fp4_linear(_ptr(q), _ptr(s), _ptr(a_scale), _ptr(offsets), E, M_cap, K, N,
+                              _ptr(wq), _ptr(ws), _ptr(w_scale), f, _ptr(bias), LINEAR_ACT[act],
+                              _ptr(residual), _ptr(z), _ptr(out), ot, _ptr(out_s), _ptr(out_scale),
+                              _ptr(err), _stream(stream))
+    _check(rc, "moe_fp4_linear")
+    return (out if out_s is None else (out, out_s)), z, err
+
+
+def fp4_linear_plan(E: int, M_cap: int, K: int, N: int, ragged: bool) -> tuple:
+    """Which kernel ``fp4_linear`` runs for these sizes (moe_fp4_linear_plan):
+    (tokens of a few-row tile, or 0 for the 256 x 256 tiles; parts of the
+    reduction)."""
+    plan = (ctypes.c_int * 2)()
+    _check(lib().moe_fp4_linear_plan(E, M_cap, K, N, int(ragged), ctypes.byref(plan)),
+           "moe_fp4_linear_plan")
+    return plan[0], plan[1]
+
+
+def fp4_linear_bwd_workspace_size(E: int, M_cap: int, N: int, fmt: str = "nvfp4") -> int:
+    return int(lib().moe_fp4_linear_bwd_workspace_size(E, M_cap, N, _fp4_format(fmt)))
+
+
+def fp4_linear_bwd(dout: torch.Tensor, a: torch.Tensor, offsets, wt, fmt: str = "nvfp4",
+                   act: str = "none", z=None, bias: bool = False, w_scale=None,
+                   b_layout: str = "kn", dz=None, da=None, dB=None, dbias=None,
+                   accumulate_dw: bool = False, workspace=None, err=None, stream=None):
+    """Backward of ``fp4_linear`` (moe_fp4_linear_bwd).  a: the bf16 rows [M,
+    K] that were quantised; wt: (q, s) of the weights with blocks along N,
+    codes [E, K, N/2], w_scale [E] their tensor scales; z: the saved
+    pre-activation.  da is the product of dz in 4 bits with wt, dB [E, K, N]
+    ("kn") or [E, N, K] ("nk") of the bf16 a and dz.  Returns (dz, da, dB,
+    dbias, err) as ``grouped_linear_bwd`` does."""
+    f = _fp4_format(fmt)
+    wq, ws = _fp4_pair(wt, "wt")
+    if wq.dim() != 3:
+        raise MoeError("wt's codes must have 3 dims")
+    if act not in LINEAR_ACT:
+        raise MoeError(f"act must be one of {sorted(LINEAR_ACT)}, got {act!r}")
+    if b_layout not in ("kn", "nk"):
+        raise MoeError(f"b_layout must be 'kn' or 'nk', got {b_layout!r}")
+    E, K, N = wq.shape[0], wq.shape[1], 2 * wq.shape[2]
+    _need(a, torch.bfloat16, "a", 2)
+    _need(dout, torch.bfloat16, "dout", 2)
+    _need(z, torch.bfloat16, "z")
+    M_cap = a.shape[0]
+    gated = act in ("swiglu", "geglu")
+    if _fp4_offsets(offsets) != E or a.shape[1] != K:
+        raise MoeError("inconsistent shapes")
+    _fp4_width(K, "a")
+    _fp4_width(N, "wt")
+    if ws.numel() != fp4_scale_bytes(E * K, E, N, fmt):
+        raise MoeError("wt's scales do not fit its codes")
+    _fp4_t(w_scale, E, fmt, "w_scale")
+    _same_shape(dout, (M_cap, N // 2 if gated else N), "dout")
+    _same_shape(z, (M_cap, N), "z")
+    if act != "none" and z is None:
+        raise MoeError("act needs the saved pre-activation z")
+    bias = bias or dbias is not None
+    if accumulate_dw and (dB is None or (bias and dbias is None)):
+        raise ValueError("accumulate_dw needs the dB (and dbias) to accumulate into")
+    dev = a.device
+    shape = (E, K, N) if b_layout == "kn" else (E, N, K)
+    _buffers((dz, torch.bfloat16, "dz", (M_cap, N)), (da, torch.bfloat16, "da", (M_cap, K)),
+             (dB, torch.bfloat16, "dB", shape), (dbias, torch.float32, "dbias", (E, N)))
+    if act != "none" and dz is None:
+        dz = _empty((M_cap, N), torch.bfloat16, dev, stream)
+    if da is None:
+        da = _empty((M_cap, K), torch.bfloat16, dev, stream)
+    if dB is None:
+        dB = _empty(shape, torch.bfloat16, dev, stream)
+    if bias and dbias is None:
+        dbias = _empty((E, N), torch.float32, dev, stream)
+    workspace = _workspace(workspace, fp4_linear_bwd_workspace_size(E, M_cap, N, fmt), dev, stream)
+    err = _err_word(err, dev, stream)
+    rc = lib().moe_fp4_linear_bwd(
+        _ptr(dout), _ptr(z), _ptr(a), _ptr(offsets), E, M_cap, K, N, _ptr(wq), _ptr(ws),
+        _ptr(w_scale), f, 0 if b_layout == "kn" else 1, LINEAR_ACT[act],
+        FLAG_ACCUMULATE_DW if accumulate_dw else 0, _ptr(dz), _ptr(da), _ptr(dB), _ptr(dbias),
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(err), _stream(stream))
+    _check(rc, "moe_fp4_linear_bwd")
     return (dout if act == "none" else dz), da, dB, dbias, err
 
 

@@ -18,7 +18,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe.so")
-SOURCES = ["api.cu", "gemm.cu", "gemm_ext.cu", "linear.cu", "loss.cu", "ckpt.cu", "route.cu",
+SOURCES = ["api.cu", "gemm.cu", "gemm_ext.cu", "linear.cu", "loss.cu", "select.cu", "fp4_gemm.cu", "fp4_few.cu",
+           "fp4_quant.cu", "ckpt.cu", "route.cu",
            "permute.cu", "mx.cu", "mx_quant.cu", "act.cu", "selftest.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -6,16 +6,19 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <cmath>
 #include <cstdint>
 #include <mutex>
 
 #include "../../include/moe.h"
 #include "ckpt.cuh"
+#include "fp4.cuh"
 #include "gemm.cuh"
 #include "linear.cuh"
 #include "loss.cuh"
 #include "mxgemm.cuh"
 #include "route.cuh"
+#include "select.cuh"
 
 namespace moe {
 cudaError_t launch_bounded_wait_selftest(int limit_us, int32_t* err, int32_t* waited_us,
@@ -233,6 +236,31 @@ bool loss_misaligned(const void* logits, int type, const void* dlogits, int dtyp
   const size_t store = vec * out < 16 ? vec * out : 16;
   return reinterpret_cast<uintptr_t>(logits) % (vec * in) != 0 ||
          reinterpret_cast<uintptr_t>(dlogits) % store != 0;
+}
+
+bool off_type(const void* p, int type) {
+  return reinterpret_cast<uintptr_t>(p) % (type == MOE_TYPE_BF16 ? 2 : 4) != 0;
+}
+
+int check_select(int T, int E, int k, int score, int renorm, float scale, int type) {
+  if (T < 0 || T > (1 << 30) || E < 1 || E > MOE_MAX_EXPERTS || k < 1 || k > E ||
+      k > moe::kSelectMaxK)
+    return MOE_E_SIZE;
+  if (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID) return MOE_E_ARG;
+  if ((renorm != 0 && renorm != 1) || !(scale > 0.f) || !std::isfinite(scale)) return MOE_E_ARG;
+  if (type != MOE_TYPE_F32 && type != MOE_TYPE_BF16) return MOE_E_ARG;
+  return MOE_OK;
+}
+
+int check_fp4(int E, long long rows, int K, int format) {
+  if (E < 1 || E > MOE_MAX_EXPERTS || rows < 0 || K <= 0 || K % 64 || K > (1 << 23))
+    return MOE_E_SIZE;
+  if (rows > (1LL << 33) || rows * K >= (1LL << 40)) return MOE_E_SIZE;
+  if (format != MOE_FP4_NV && format != MOE_FP4_MX) return MOE_E_ARG;
+  // (the scale chunks' numbers fit the 32-bit coordinates of their loads)
+  if (2 * moe::fp4_tiles(rows, E) * moe::fp4_chunks(format == MOE_FP4_NV, K) >= (1LL << 31))
+    return MOE_E_SIZE;
+  return MOE_OK;
 }
 
 bool linear_gated(int act) { return act == MOE_ACT_SWIGLU || act == MOE_ACT_GEGLU; }
@@ -1208,6 +1236,69 @@ int moe_router_loss_bwd(const void* logits, int logits_type, const int32_t* topk
   return cuda_rc(e);
 }
 
+// ------------------------------------------------ the router's choice by scores
+
+int moe_router_select(const void* logits, int logits_type, int T, int E, int k, int score,
+                      const float* bias, int groups, int top_groups, int group_best, int renorm,
+                      float scale, int32_t* topk_idx, float* probs, void* stream) {
+  g_last_launches = 0;
+  g_split_extra = 0;
+  const int rc = check_select(T, E, k, score, renorm, scale, logits_type);
+  if (rc) return rc;
+  if (groups < 1 || groups > moe::kSelectMaxGroups || E % groups || top_groups < 1 ||
+      top_groups > groups || k > E / groups * top_groups || group_best < 1 || group_best > 2 ||
+      group_best > E / groups)
+    return MOE_E_SIZE;
+  if (T == 0) return MOE_OK;
+  if (!logits || !topk_idx || !probs) return MOE_E_NULL;
+  if (off_type(logits, logits_type) || off_type(bias, MOE_TYPE_F32) ||
+      off_type(topk_idx, MOE_TYPE_F32) || off_type(probs, MOE_TYPE_F32))
+    return MOE_E_ALIGN;
+  const int sms = num_sms_current();
+  if (sms <= 0) return MOE_E_CUDA;
+  moe::SelectArgs a{};
+  a.logits = logits; a.logits_bf16 = logits_type == MOE_TYPE_BF16; a.T = T; a.E = E; a.k = k;
+  a.score = score; a.bias = bias; a.groups = groups; a.top_groups = top_groups;
+  a.best = group_best; a.renorm = renorm; a.scale = scale; a.idx = topk_idx; a.probs = probs;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  ev_begin(s);
+  const cudaError_t e = moe::launch_router_select(a, sms, s);
+  ev_end(s);
+  g_last_launches = 1;
+  return cuda_rc(e);
+}
+
+int moe_router_select_bwd(const void* logits, int logits_type, const int32_t* topk_idx,
+                          const float* probs, const float* dprobs, int T, int E, int k, int score,
+                          int renorm, float scale, int accumulate, void* dlogits,
+                          int dlogits_type, void* stream) {
+  g_last_launches = 0;
+  g_split_extra = 0;
+  int rc = check_select(T, E, k, score, renorm, scale, logits_type);
+  if (rc == MOE_OK) rc = check_select(T, E, k, score, renorm, scale, dlogits_type);
+  if (rc) return rc;
+  if (accumulate != 0 && accumulate != 1) return MOE_E_ARG;
+  if (T == 0) return MOE_OK;
+  if (!logits || !topk_idx || !probs || !dprobs || !dlogits) return MOE_E_NULL;
+  if (off_type(logits, logits_type) || off_type(dlogits, dlogits_type) ||
+      off_type(topk_idx, MOE_TYPE_F32) || off_type(probs, MOE_TYPE_F32) ||
+      off_type(dprobs, MOE_TYPE_F32))
+    return MOE_E_ALIGN;
+  const int sms = num_sms_current();
+  if (sms <= 0) return MOE_E_CUDA;
+  moe::SelectArgs a{};
+  a.logits = logits; a.logits_bf16 = logits_type == MOE_TYPE_BF16; a.T = T; a.E = E; a.k = k;
+  a.score = score; a.renorm = renorm; a.scale = scale;
+  a.idx = const_cast<int32_t*>(topk_idx); a.probs = const_cast<float*>(probs); a.dprobs = dprobs;
+  a.accumulate = accumulate; a.dlogits = dlogits; a.dlogits_bf16 = dlogits_type == MOE_TYPE_BF16;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  ev_begin(s);
+  const cudaError_t e = moe::launch_router_select_bwd(a, sms, s);
+  ev_end(s);
+  g_last_launches = 1;
+  return cuda_rc(e);
+}
+
 // ------------------------------------------------ linear
 
 int moe_grouped_linear(const moe_bf16* a, const int32_t* offsets, int E, int M_cap, int K, int N,
@@ -1368,6 +1459,310 @@ int moe_grouped_linear_bwd(const moe_bf16* dout, const moe_bf16* z, const moe_bf
     ++launches;
   }
   g_last_launches = launches + g_split_extra;
+  return MOE_OK;
+}
+
+// ------------------------------------------------ 4 bits
+
+size_t moe_fp4_scale_bytes(long long rows, int E, int K, int format) {
+  if (check_fp4(E, rows, K, format)) return 0;
+  return static_cast<size_t>(moe::fp4_tiles(rows, E)) * moe::fp4_chunks(format == MOE_FP4_NV, K) *
+         moe::kFp4ChunkBytes;
+}
+
+int moe_fp4_tensor_scale(const moe_bf16* src, int E, long long n, float* t, void* stream) {
+  g_last_launches = 0;
+  g_split_extra = 0;
+  if (E < 1 || E > MOE_MAX_EXPERTS || n < 0 || n % 64 || n >= (1LL << 40)) return MOE_E_SIZE;
+  if (!t || (n > 0 && !src)) return MOE_E_NULL;
+  if (misaligned(src) || off_type(t, MOE_TYPE_F32)) return MOE_E_ALIGN;
+  const int sms = num_sms_current();
+  if (sms <= 0) return MOE_E_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int launches = 0;
+  ev_begin(st);
+  const cudaError_t e = moe::launch_fp4_tensor_scale(src, E, n, t, sms, st, &launches);
+  ev_end(st);
+  g_last_launches = launches;
+  return cuda_rc(e);
+}
+
+int moe_fp4_quantize(const moe_bf16* src, const int32_t* offsets, int E, int rows, int K,
+                     int format, const float* t, uint8_t* q, uint8_t* s, int32_t* err,
+                     void* stream) {
+  g_last_launches = 0;
+  g_split_extra = 0;
+  const int rc = check_fp4(E, rows, K, format);
+  if (rc) return rc;
+  if (!offsets && rows % E) return MOE_E_SIZE;
+  if (t && format == MOE_FP4_MX) return MOE_E_ARG;
+  if (rows == 0) return MOE_OK;
+  if (!src || !q || !s || !err) return MOE_E_NULL;
+  if (misaligned(src) || misaligned(q) || misaligned(s) || off_type(t, MOE_TYPE_F32))
+    return MOE_E_ALIGN;
+  const int sms = num_sms_current();
+  if (sms <= 0) return MOE_E_CUDA;
+  moe::Fp4QuantArgs a{};
+  a.src = src; a.r = moe::Fp4Rows{offsets, E, rows, rows / E}; a.K = K;
+  a.nv = format == MOE_FP4_NV; a.t = t; a.q = q; a.s = s; a.err = err;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  ev_begin(st);
+  const cudaError_t e = moe::launch_fp4_quantize(a, sms, st);
+  ev_end(st);
+  g_last_launches = 1;
+  return cuda_rc(e);
+}
+
+int moe_fp4_permute(const moe_bf16* src, const int32_t* row_of_pair, const int32_t* pair_of_row,
+                    const int32_t* offsets, int E, int T, int k, int K, int M_cap, int format,
+                    const float* t, uint8_t* q, uint8_t* s, int32_t* err, void* stream) {
+  g_last_launches = 0;
+  g_split_extra = 0;
+  const int rc = check_fp4(E, M_cap, K, format);
+  if (rc) return rc;
+  if (T < 0 || k < 1 || static_cast<long long>(T) * k >= (1LL << 31) ||
+      static_cast<long long>(T) * K >= (1LL << 40))
+    return MOE_E_SIZE;
+  if (t && format == MOE_FP4_MX) return MOE_E_ARG;
+  if (M_cap == 0) return MOE_OK;
+  if (!pair_of_row || !offsets || !q || !s || !err || (T > 0 && !src)) return MOE_E_NULL;
+  if (misaligned(src) || misaligned(q) || misaligned(s) || off_type(t, MOE_TYPE_F32))
+    return MOE_E_ALIGN;
+  const int sms = num_sms_current();
+  if (sms <= 0) return MOE_E_CUDA;
+  moe::Fp4QuantArgs a{};
+  a.src = src; a.r = moe::Fp4Rows{offsets, E, M_cap, 0}; a.K = K; a.nv = format == MOE_FP4_NV;
+  a.t = t; a.pair_of_row = pair_of_row; a.row_of_pair = T > 0 ? row_of_pair : nullptr; a.T = T;
+  a.k = k; a.q = q; a.s = s; a.err = err;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  ev_begin(st);
+  const cudaError_t e = moe::launch_fp4_quantize(a, sms, st);
+  ev_end(st);
+  g_last_launches = 1;
+  return cuda_rc(e);
+}
+
+int moe_fp4_quantize_weights(const moe_bf16* W, int E, int rows, int cols, int along, int format,
+                             const float* t, uint8_t* q, uint8_t* s, void* stream) {
+  g_last_launches = 0;
+  g_split_extra = 0;
+  if (along != MOE_FP4_COLS && along != MOE_FP4_ROWS) return MOE_E_ARG;
+  if (rows <= 0 || cols <= 0 || rows % 64 || cols % 64) return MOE_E_SIZE;
+  const int K = along == MOE_FP4_ROWS ? rows : cols, N = along == MOE_FP4_ROWS ? cols : rows;
+  const int rc = check_fp4(E, static_cast<long long>(E) * N, K, format);
+  if (rc) return rc;
+  if (t && format == MOE_FP4_MX) return MOE_E_ARG;
+  if (!W || !q || !s) return MOE_E_NULL;
+  if (misaligned(W) || misaligned(q) || misaligned(s) || off_type(t, MOE_TYPE_F32))
+    return MOE_E_ALIGN;
+  const int sms = num_sms_current();
+  if (sms <= 0) return MOE_E_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool nv = format == MOE_FP4_NV;
+  ev_begin(st);
+  cudaError_t e;
+  if (along == MOE_FP4_ROWS) {
+    e = moe::launch_fp4_quantize_t(W, E, rows, cols, nv, t, q, s, sms, st);
+  } else {
+    moe::Fp4QuantArgs a{};
+    a.src = W; a.r = moe::Fp4Rows{nullptr, E, static_cast<long long>(E) * N, N}; a.K = K;
+    a.nv = nv; a.t = t; a.t_stride = 1; a.q = q; a.s = s;
+    e = moe::launch_fp4_quantize(a, sms, st);
+  }
+  ev_end(st);
+  g_last_launches = 1;
+  return cuda_rc(e);
+}
+
+int moe_fp4_dequantize(const uint8_t* q, const uint8_t* s, const int32_t* offsets, int E,
+                       long long rows, int K, int format, const float* t, int t_per_expert,
+                       void* out, int type, int32_t* err, void* stream) {
+  g_last_launches = 0;
+  g_split_extra = 0;
+  const int rc = check_fp4(E, rows, K, format);
+  if (rc) return rc;
+  if (!offsets && rows % E) return MOE_E_SIZE;
+  if (offsets && rows >= (1LL << 31)) return MOE_E_SIZE;
+  if (type != MOE_TYPE_F32 && type != MOE_TYPE_BF16) return MOE_E_ARG;
+  if ((t && format == MOE_FP4_MX) || (t_per_expert != 0 && t_per_expert != 1)) return MOE_E_ARG;
+  if (rows == 0) return MOE_OK;
+  if (!q || !s || !out || !err) return MOE_E_NULL;
+  if (misaligned(q) || misaligned(s) || misaligned(out) || off_type(t, MOE_TYPE_F32))
+    return MOE_E_ALIGN;
+  const int sms = num_sms_current();
+  if (sms <= 0) return MOE_E_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  ev_begin(st);
+  const cudaError_t e = moe::launch_fp4_dequantize(
+      q, s, moe::Fp4Rows{offsets, E, rows, rows / E}, K, format == MOE_FP4_NV, t, t_per_expert, out,
+      type == MOE_TYPE_F32, err, sms, st);
+  ev_end(st);
+  g_last_launches = 1;
+  return cuda_rc(e);
+}
+
+}  // extern "C"
+
+namespace {
+
+int check_fp4_linear(const int32_t* offsets, int E, int M_cap, int K, int N, int format, int act) {
+  int rc = check_linear(offsets, E, M_cap, K, N, MOE_B_KN, act);
+  if (rc == MOE_OK) rc = check_fp4(E, M_cap, K, format);
+  if (rc == MOE_OK) rc = check_fp4(E, static_cast<long long>(E) * N, K, format);
+  return rc;
+}
+
+// the product's launch, sizes and pointers checked
+int fp4_product(moe::Fp4GemmArgs& g, const uint8_t* a_q, const uint8_t* w_q, int sms,
+                cudaStream_t s) {
+  g.a_tiles = moe::fp4_tiles(g.M_cap, g.E);
+  g.w_tiles = moe::fp4_tiles(static_cast<long long>(g.E) * g.N, g.E);
+  const moe::Fp4Plan plan = moe::fp4_plan(g.E, g.M_cap, g.K, g.N, g.offsets != nullptr, sms);
+  CUtensorMap ta, tw;
+  if (!map_act(&ta, a_q, g.M_cap, g.K / 2, plan.tn ? moe::kFp4FewBox : 128, true) ||
+      !map_w(&tw, w_q, g.E, g.N, g.K / 2, 128, true))
+    return MOE_E_CUDA;
+  ev_begin(s);
+  const cudaError_t e = plan.tn ? moe::launch_fp4_few(ta, tw, g, plan, sms, s)
+                                : moe::launch_fp4_gemm(ta, tw, g, sms, s);
+  ev_end(s);
+  return cuda_rc(e);
+}
+
+// regions of the 4-bit backward's workspace, in carving order
+struct Fp4BwdWs {
+  uint8_t *q, *s;
+  float* t;
+  uint8_t* part;
+  size_t bytes;
+};
+Fp4BwdWs carve_fp4_bwd(void* base, int E, int M_cap, int N, int format) {
+  Carve c{static_cast<uint8_t*>(base), 0};
+  Fp4BwdWs w;
+  w.q = c.take(static_cast<size_t>(M_cap) * (N / 2));
+  w.s = c.take(moe_fp4_scale_bytes(M_cap, E, N, format));
+  w.t = reinterpret_cast<float*>(c.take(sizeof(float)));
+  w.part = c.take(moe::linear_dz_workspace_bytes(E, M_cap, N));
+  w.bytes = c.used;
+  return w;
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_fp4_linear(const uint8_t* a_q, const uint8_t* a_s, const float* a_t,
+                   const int32_t* offsets, int E, int M_cap, int K, int N, const uint8_t* w_q,
+                   const uint8_t* w_s, const float* w_t, int format, const moe_bf16* bias, int act,
+                   const moe_bf16* residual, moe_bf16* z, void* out, int out_type, uint8_t* out_s,
+                   const float* out_t, int32_t* err, void* stream) {
+  g_last_launches = 0;
+  g_split_extra = 0;
+  const int rc = check_fp4_linear(offsets, E, M_cap, K, N, format, act);
+  if (rc) return rc;
+  if (out_type < MOE_TYPE_F32 || out_type > MOE_TYPE_FP4) return MOE_E_ARG;
+  const bool q4 = out_type == MOE_TYPE_FP4;
+  const int n_out = linear_gated(act) ? N / 2 : N;
+  if (q4 && check_fp4(E, M_cap, n_out, format)) return MOE_E_SIZE;
+  if (format == MOE_FP4_MX && (a_t || w_t || out_t)) return MOE_E_ARG;
+  if (!q4 && (out_s || out_t)) return MOE_E_ARG;
+  if (!w_q || !w_s || !err) return MOE_E_NULL;
+  if (M_cap == 0) return MOE_OK;
+  if (!a_q || !a_s || !out || (q4 && !out_s)) return MOE_E_NULL;
+  if (misaligned(a_q) || misaligned(a_s) || misaligned(w_q) || misaligned(w_s) ||
+      misaligned(bias) || misaligned(residual) || misaligned(z) || misaligned(out) ||
+      misaligned(out_s) || off_type(a_t, MOE_TYPE_F32) || off_type(w_t, MOE_TYPE_F32) ||
+      off_type(out_t, MOE_TYPE_F32))
+    return MOE_E_ALIGN;
+  const int sms = num_sms_current();
+  if (sms <= 0) return MOE_E_CUDA;
+  moe::Fp4GemmArgs g{};
+  g.offsets = offsets; g.E = E; g.M_cap = M_cap; g.K = K; g.N = N; g.nv = format == MOE_FP4_NV;
+  g.a_s = a_s; g.w_s = w_s; g.a_t = a_t; g.w_t = w_t; g.bias = bias; g.act = act;
+  g.residual = residual; g.z = z; g.ldo = n_out; g.out_t = out_t; g.err = err;
+  g.out = out_type == MOE_TYPE_BF16 ? static_cast<uint16_t*>(out) : nullptr;
+  g.out_f32 = out_type == MOE_TYPE_F32 ? static_cast<float*>(out) : nullptr;
+  g.out_q = q4 ? static_cast<uint8_t*>(out) : nullptr;
+  g.out_s = out_s;
+  const int r = fp4_product(g, a_q, w_q, sms, static_cast<cudaStream_t>(stream));
+  if (r == MOE_OK) g_last_launches = 1;
+  return r;
+}
+
+int moe_fp4_linear_plan(int E, int M_cap, int K, int N, int ragged, int plan[2]) {
+  if (ragged != 0 && ragged != 1) return MOE_E_ARG;
+  static const int32_t some = 0;    // (a non-NULL address: offsets or none)
+  const int rc = check_fp4_linear(ragged ? &some : nullptr, E, M_cap, K, N, MOE_FP4_NV, MOE_ACT_NONE);
+  if (rc) return rc;
+  if (M_cap == 0) return MOE_E_SIZE;
+  if (!plan) return MOE_E_NULL;
+  const int sms = num_sms_current();
+  if (sms <= 0) return MOE_E_CUDA;
+  const moe::Fp4Plan p = moe::fp4_plan(E, M_cap, K, N, ragged != 0, sms);
+  plan[0] = p.tn;
+  plan[1] = p.tn ? p.split : 1;
+  return MOE_OK;
+}
+
+size_t moe_fp4_linear_bwd_workspace_size(int E, int M_cap, int N, int format) {
+  if (check_fp4(E, M_cap, N, format)) return 0;
+  return carve_fp4_bwd(nullptr, E, M_cap, N, format).bytes;
+}
+
+int moe_fp4_linear_bwd(const moe_bf16* dout, const moe_bf16* z, const moe_bf16* a,
+                       const int32_t* offsets, int E, int M_cap, int K, int N, const uint8_t* wt_q,
+                       const uint8_t* wt_s, const float* wt_t, int format, int b_layout, int act,
+                       int flags, moe_bf16* dz, moe_bf16* da, moe_bf16* dB, float* dbias,
+                       void* workspace, size_t ws_bytes, int32_t* err, void* stream) {
+  g_last_launches = 0;
+  g_split_extra = 0;
+  // (the data gradient's product: [M_cap, N] times [E, K, N])
+  const int rc = check_fp4_linear(offsets, E, M_cap, N, K, format, act);
+  if (rc) return rc;
+  if (wt_t && format == MOE_FP4_MX) return MOE_E_ARG;
+  if (da && (!wt_q || !wt_s)) return MOE_E_NULL;
+  if (da && (misaligned(wt_q) || misaligned(wt_s) || off_type(wt_t, MOE_TYPE_F32) ||
+             misaligned(da)))
+    return MOE_E_ALIGN;
+  if (M_cap > 0 && (da || dbias)) {
+    if (ws_bytes < moe_fp4_linear_bwd_workspace_size(E, M_cap, N, format)) return MOE_E_WORKSPACE;
+    if (!workspace) return MOE_E_NULL;
+    if (misaligned(workspace)) return MOE_E_ALIGN;
+  }
+  const Fp4BwdWs w = carve_fp4_bwd(workspace, E, M_cap, N, format);
+  // dz, the bias gradient and the weights' gradient: the bf16 operator's
+  const int r = moe_grouped_linear_bwd(dout, z, a, offsets, E, M_cap, K, N, nullptr, b_layout, act,
+                                       flags, dz, nullptr, dB, dbias, w.part,
+                                       moe::linear_dz_workspace_bytes(E, M_cap, N), err, stream);
+  if (r != MOE_OK || M_cap == 0 || !da) return r;
+  const int sms = num_sms_current();
+  if (sms <= 0) return MOE_E_CUDA;
+  int launches = g_last_launches;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const moe_bf16* gz = act == MOE_ACT_NONE ? dout : dz;
+  const bool nv = format == MOE_FP4_NV;
+  if (nv) {
+    int n = 0;
+    ev_begin(s);
+    const cudaError_t e = moe::launch_fp4_tensor_scale(gz, 1, static_cast<long long>(M_cap) * N,
+                                                       w.t, sms, s, &n);
+    ev_end(s);
+    if (e != cudaSuccess) return MOE_E_CUDA;
+    launches += n;
+  }
+  moe::Fp4QuantArgs q{};
+  q.src = gz; q.r = moe::Fp4Rows{offsets, E, M_cap, M_cap}; q.K = N; q.nv = nv;
+  q.t = nv ? w.t : nullptr; q.q = w.q; q.s = w.s; q.err = err;
+  ev_begin(s);
+  const cudaError_t e = moe::launch_fp4_quantize(q, sms, s);
+  ev_end(s);
+  if (e != cudaSuccess) return MOE_E_CUDA;
+  moe::Fp4GemmArgs g{};
+  g.offsets = offsets; g.E = E; g.M_cap = M_cap; g.K = N; g.N = K; g.nv = nv; g.a_s = w.s;
+  g.w_s = wt_s; g.a_t = q.t; g.w_t = wt_t; g.act = MOE_ACT_NONE; g.out = da; g.ldo = K; g.err = err;
+  const int rp = fp4_product(g, w.q, wt_q, sms, s);
+  if (rp != MOE_OK) return rp;
+  g_last_launches = launches + 2;
   return MOE_OK;
 }
 

@@ -1,0 +1,516 @@
+// fp4_gemm.cu - block-scaled 4-bit grouped product
+// (tcgen05.mma.kind::mxf4nvf4.block_scale) with bias, activation, residual and
+// a 4-bit output in its epilogue, for many rows.
+//
+//   z = t_a t_e sum_blocks s_a s_w (sum of a block's code products) + bias
+//   out = act(z) + residual
+// Persistent and warp-specialised in CTA pairs, as the MXFP8 grouped GEMM: 256
+// rows x 256 columns a tile, each CTA with 128 rows of a and 128 columns of w
+// in shared memory (2-SM MMAs, M = 256, N = 256, K = 64).  A stage is one
+// 128-byte swizzle row of K (256 values): 32 KB of codes and, NV, 6 KB of
+// scales (MX 3) for 33.5 MFLOP.  TMEM: a 256-column accumulator and each
+// stage's scale columns; the epilogue moves the accumulator to registers and
+// releases it at once, so the next tile's MMAs overlap bias, activation,
+// quantisation and stores.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "drain.cuh"
+#include "fp4_mma.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int GT = 320;                          // threads
+constexpr int GEPI = 8;                          // epilogue warps
+constexpr int GM = 128;                          // rows, and columns of w, that a CTA holds
+constexpr int GN = 256;                          // columns of a tile
+constexpr int OP_BYTES = GM * 128;               // 16 KB: 128 rows x 256 codes
+constexpr int STAGES = 5;
+constexpr int SF_TMEM = GN;                      // scale columns after the accumulator
+
+template <bool NV>
+struct GC {
+  static constexpr int sf_bytes = 3 * Fp4Sf<NV>::bytes;        // a's, and both halves of w's
+  static constexpr int stage_bytes = 2 * OP_BYTES;
+  static constexpr int stage_tx = stage_bytes + sf_bytes;      // a CTA's bytes
+  static constexpr int sf_cols = 3 * Fp4Sf<NV>::cols;
+  static_assert(SF_TMEM + STAGES * sf_cols <= 512, "TMEM columns");
+  static constexpr size_t smem(int E) {
+    return 1024 + static_cast<size_t>(STAGES) * stage_tx + (2 * STAGES + 4) * 8 + 32 +
+           2 * (E + 1) * 4;
+  }
+};
+
+struct GTile {
+  int e, row0, rows, n0;    // first row of this CTA's block, its valid rows, first column
+  long long tile;           // its scale tile
+};
+
+__device__ __forceinline__ GTile gemm_tile(const Fp4GemmArgs& g, const int* s_off, const int* s_ts,
+                                           int u, int rank) {
+  const int e = fp4_expert_of(s_ts, g.E, u);
+  const int nt = (g.N + GN - 1) / GN;
+  const int local = u - s_ts[e];
+  const int pm = local / nt;
+  const int mi = 2 * pm + rank;
+  GTile t;
+  t.e = e;
+  t.row0 = s_off[e] + mi * GM;
+  t.rows = max(0, min(GM, s_off[e + 1] - t.row0));
+  t.n0 = (local - pm * nt) * GN;
+  t.tile = fp4_tile0(s_off[e], e) + mi;
+  return t;
+}
+
+// Epilogue of 32 accumulator columns from `col` of row `row` (one thread):
+// everything but the 4-bit output, which the caller quantises from v (32
+// outputs, or 16 when gated).
+template <bool GATED>
+__device__ __forceinline__ void gemm_out32(const Fp4GemmArgs& g, float alpha, int e, long long row,
+                                           int col, bool on, const uint32_t (&acc)[32],
+                                           float (&v)[32]) {
+  const uint16_t* bias = g.bias ? g.bias + static_cast<long long>(e) * g.N + col : nullptr;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float z[8];
+    uint4 b = make_uint4(0, 0, 0, 0);
+    if (bias) b = __ldg(reinterpret_cast<const uint4*>(bias) + j);
+    const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      z[2 * i] = fmaf(__uint_as_float(acc[8 * j + 2 * i]), alpha, bf16_lo(bw[i]));
+      z[2 * i + 1] = fmaf(__uint_as_float(acc[8 * j + 2 * i + 1]), alpha, bf16_hi(bw[i]));
+    }
+    if (g.z && on)
+      *reinterpret_cast<uint4*>(g.z + row * g.N + col + 8 * j) =
+          make_uint4(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]), pack_bf16x2(z[4], z[5]),
+                     pack_bf16x2(z[6], z[7]));
+    if constexpr (GATED) {
+      float u[4];
+      linear_glu(g.act, z, u);
+      if (g.residual && on) {
+        const uint2 r = *reinterpret_cast<const uint2*>(g.residual + row * g.ldo + col / 2 + 4 * j);
+        u[0] += bf16_lo(r.x); u[1] += bf16_hi(r.x); u[2] += bf16_lo(r.y); u[3] += bf16_hi(r.y);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[4 * j + i] = u[i];
+    } else {
+      linear_act(g.act, z);
+      if (g.residual && on) {
+        const uint4 r = *reinterpret_cast<const uint4*>(g.residual + row * g.ldo + col + 8 * j);
+        const uint32_t rw[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) { z[2 * i] += bf16_lo(rw[i]); z[2 * i + 1] += bf16_hi(rw[i]); }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[8 * j + i] = z[i];
+    }
+  }
+  constexpr int NO = GATED ? 16 : 32;
+  if (!on || g.out_q) return;
+  const long long at = row * g.ldo + (GATED ? col / 2 : col);
+  if (g.out_f32) {
+#pragma unroll
+    for (int i = 0; i < NO / 4; ++i)
+      *reinterpret_cast<float4*>(g.out_f32 + at + 4 * i) =
+          make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NO / 8; ++i)
+      *reinterpret_cast<uint4*>(g.out + at + 8 * i) =
+          make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                     pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+  }
+}
+
+__device__ __forceinline__ uint32_t amax_bits(const float* v, int n) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < n; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+  return m;
+}
+
+template <bool NV, bool GATED>
+__global__ void __launch_bounds__(GT, 1)
+    fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW,
+                    const __grid_constant__ CUtensorMap tmSA,
+                    const __grid_constant__ CUtensorMap tmSW, const Fp4GemmArgs g) {
+  using C = GC<NV>;
+  using SF = Fp4Sf<NV>;
+  constexpr uint32_t IDESC = fp4_idesc<NV>(2 * GM, GN);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* sf_region = smem + STAGES * C::stage_bytes;
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(sf_region + STAGES * C::sf_bytes);
+  uint64_t* empty_bar = full_bar + STAGES;
+  uint64_t* tfull_bar = empty_bar + STAGES;
+  uint64_t* tempty_bar = tfull_bar + 1;
+  uint64_t* drain_bar = tempty_bar + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint32_t* loads = tmem_slot + 2;    // stages loaded: by the first CTA, by the second
+  int* s_off = reinterpret_cast<int*>(tmem_slot + 4);
+  int* s_ts = s_off + (g.E + 1);
+
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+  const int lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int unit0 = blockIdx.x / 2, unit_step = gridDim.x / 2;
+  const int nt = (g.N + GN - 1) / GN;
+  const int kblocks = (g.K + kFp4StageK - 1) / kFp4StageK;
+  const int chunks = fp4_chunks(NV, g.K);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(&full_bar[i], 1);
+      mbar_init(&empty_bar[i], 1);
+    }
+    mbar_init(tfull_bar, 1);
+    mbar_init(tempty_bar, 2 * GEPI);    // the first CTA's MMAs wait for both CTAs' epilogues
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&tmA);
+    prefetch_tmap(&tmW);
+    prefetch_tmap(&tmSA);
+    prefetch_tmap(&tmSW);
+  }
+  if (warp == 1) tmem_alloc_pair(tmem_slot, 512);
+  if (warp == 2)
+    fp4_schedule(g.offsets, g.E, g.M_cap, s_off, s_ts, g.err,
+                 [&](int rows) { return (rows + 2 * GM - 1) / (2 * GM) * nt; });
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int units = s_ts[g.E];
+  // a role that gives up takes the other CTA with it
+  auto gave_up = [&](bool ok) {
+    if (!ok && elect_one())
+      st_cluster_u32(mapa_shared(smem_u32(const_cast<int*>(abort_flag)), rank ^ 1), 1u);
+  };
+
+  if (warp == 0) {
+    // producer: this CTA's rows of a, its columns of w and three runs of scale
+    // chunks; every byte counts on the first CTA's barrier.  Chunks and rows
+    // past a buffer read as zeros, those of a neighbour belong to columns and
+    // rows that are not stored.
+    const uint32_t full0 = mapa_shared(smem_u32(full_bar), 0);
+    int stage = 0;
+    uint32_t phase = 0, issued = 0;
+    bool ok = true;
+    for (int u = unit0; u < units && ok; u += unit_step) {
+      const GTile t = gemm_tile(g, s_off, s_ts, u, rank);
+      const long long ca = t.tile * chunks;
+      const long long cw =
+          (fp4_tile0(static_cast<long long>(t.e) * g.N, t.e) + t.n0 / GM) * chunks;
+      for (int kb = 0; kb < kblocks; ++kb) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&empty_bar[stage], phase ^ 1, abort_flag));
+        if (!ok) break;
+        if (elect_one()) {
+          uint8_t* sa = smem + stage * C::stage_bytes;
+          uint8_t* ss = sf_region + stage * C::sf_bytes;
+          const uint32_t fb = full0 + stage * 8;
+          if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], 2 * C::stage_tx);
+          tma_load_2d_pair(sa, &tmA, fb, kb * 128, t.row0);
+          tma_load_3d_pair(sa + OP_BYTES, &tmW, fb, kb * 128, t.n0 + rank * GM, t.e);
+          const long long c = kb * SF::chunks;
+          tma_load_2d_pair(ss, &tmSA, fb, 0, static_cast<int>(2 * (ca + c)));
+          tma_load_2d_pair(ss + SF::bytes, &tmSW, fb, 0, static_cast<int>(2 * (cw + c)));
+          tma_load_2d_pair(ss + 2 * SF::bytes, &tmSW, fb, 0, static_cast<int>(2 * (cw + chunks + c)));
+        }
+        ++issued;
+        if (++stage == STAGES) { stage = 0; phase ^= 1; }
+      }
+    }
+    if (elect_one()) {
+      if (rank != 0) st_cluster_u32(mapa_shared(smem_u32(loads + 1), 0), issued);
+      else loads[0] = issued;
+    }
+    gave_up(ok);
+  } else if (warp == 1) {
+    // MMA issuer: the first CTA's warp, for both
+    if (rank == 0) {
+      int stage = 0, local = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      const uint32_t a_lo0 = sdesc_lo(smem_u32(smem), 16);
+      const uint32_t w_lo0 = sdesc_lo(smem_u32(smem) + OP_BYTES, 16);
+      const uint32_t sf0 = smem_u32(sf_region);
+      for (int u = unit0; u < units && ok; u += unit_step, ++local) {
+        ok = __all_sync(0xffffffffu, mbar_wait_cluster(tempty_bar, (local & 1) ^ 1, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+        for (int kb = 0; kb < kblocks; ++kb) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&full_bar[stage], phase, abort_flag));
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t ss = sf0 + stage * C::sf_bytes;
+            const uint32_t ta = tmem_base + SF_TMEM + stage * C::sf_cols;
+            const uint32_t tw = ta + SF::cols;
+#pragma unroll
+            for (int c = 0; c < SF::chunks; ++c) {
+              tmem_cp_sf_pair(ta + 4 * c, fp4_sf_desc(ss + c * kFp4ChunkBytes));
+              tmem_cp_sf_pair(tw + 8 * c, fp4_sf_desc(ss + SF::bytes + c * kFp4ChunkBytes));
+              tmem_cp_sf_pair(tw + 8 * c + 4, fp4_sf_desc(ss + 2 * SF::bytes + c * kFp4ChunkBytes));
+            }
+            const uint32_t a_lo = a_lo0 + stage * (C::stage_bytes >> 4);
+            const uint32_t w_lo = w_lo0 + stage * (C::stage_bytes >> 4);
+            auto mma = [&](int kk) {
+              umma_fp4<NV, true>(tmem_base, sdesc_of(a_lo + kk * 2), sdesc_of(w_lo + kk * 2),
+                                 IDESC | fp4_select<NV>(kk), ta + 4 * fp4_step_chunk<NV>(kk),
+                                 tw + 8 * fp4_step_chunk<NV>(kk), (kb > 0 || kk > 0) ? 1u : 0u);
+            };
+            const int steps = min(4, (g.K - kb * kFp4StageK) / kFp4StepK);
+            if (steps == 4) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) mma(kk);
+            } else {          // the end of a K that is no multiple of 256
+#pragma unroll
+              for (int kk = 0; kk < 3; ++kk)
+                if (kk < steps) mma(kk);
+            }
+            umma_commit_pair_mc(&empty_bar[stage]);
+          }
+          __syncwarp();
+          if (++stage == STAGES) { stage = 0; phase ^= 1; }
+        }
+        if (ok && elect_one()) umma_commit_pair_mc(tfull_bar);
+        __syncwarp();
+      }
+      gave_up(ok);
+    }
+  } else {
+    // epilogue: warpgroup wg takes 128 of the tile's columns, warp q of it 32
+    // rows, a thread one row
+    const int q = warp & 3, wg = (warp - 2) >> 2;
+    const int r = q * 32 + lane;
+    const uint32_t tempty0 = mapa_shared(smem_u32(tempty_bar), 0);
+    const int out_chunks = g.out_q ? fp4_chunks(NV, g.ldo) : 0;
+    const float out_t = (g.out_q && g.out_t) ? *g.out_t : 1.f;
+    int local = 0;
+    bool ok = true;
+    for (int u = unit0; u < units && ok; u += unit_step, ++local) {
+      const GTile t = gemm_tile(g, s_off, s_ts, u, rank);
+      const float alpha = fp4_alpha(g, t.e);
+      if (lane == 0) ok = mbar_wait(tfull_bar, local & 1, abort_flag);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      tc_fence_after();
+      const int col0 = t.n0 + wg * GM;
+      const bool mine = col0 < g.N && q * 32 < t.rows;
+      uint32_t v[4][32];
+      if (mine) {
+        const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + wg * GM;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(tb + c * 32, v[c]);
+        tmem_wait_ld();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (rank != 0) mbar_arrive_cluster(tempty0);
+        else mbar_arrive(tempty_bar);
+      }
+      if (!mine) continue;
+      const bool on = r < t.rows;
+      const long long row = static_cast<long long>(t.row0) + r;
+      const int last = min(4, (g.N - col0) / 32);
+      const long long tile0 = fp4_tile0(s_off[t.e], t.e);
+      const long long in_e = row - s_off[t.e];
+      uint32_t bytes = 0;               // scale bytes of up to 64 outputs
+      float held[GATED && !NV ? 16 : 1];
+#pragma unroll 1
+      for (int c = 0; c < last; ++c) {
+        const int col = col0 + 32 * c;
+        float o[32];
+        gemm_out32<GATED>(g, alpha, t.e, row, col, on, v[0], o);
+        if (g.out_q) {
+          uint8_t* q8 = g.out_q + row * (g.ldo / 2);
+          if constexpr (GATED) {
+            const int oc = col / 2;     // 16 outputs
+            if constexpr (NV) {
+              float inv;
+              bytes |= fp4_scale<true>(amax_bits(o, 16), out_t, inv) << (8 * c);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] *= inv;
+              if (on) *reinterpret_cast<uint2*>(q8 + oc / 2) = make_uint2(e2m1x8(o), e2m1x8(o + 8));
+              if (c == 3 && on)
+                *reinterpret_cast<uint32_t*>(g.out_s + fp4_scale_at(tile0, in_e, col0 / 32, out_chunks)) = bytes;
+            } else if ((c & 1) == 0) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) held[i] = o[i];
+            } else {
+              float inv;
+              const uint32_t s = fp4_scale<false>(max(amax_bits(held, 16), amax_bits(o, 16)), 1.f, inv);
+              bytes |= s << (4 * (c - 1));
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                held[i] *= inv;
+                o[i] *= inv;
+              }
+              if (on)
+                *reinterpret_cast<uint4*>(q8 + (oc - 16) / 2) =
+                    make_uint4(e2m1x8(held), e2m1x8(held + 8), e2m1x8(o), e2m1x8(o + 8));
+              if (c == 3 && on)
+                *reinterpret_cast<uint16_t*>(g.out_s + fp4_scale_at(tile0, in_e, col0 / 64, out_chunks)) =
+                    static_cast<uint16_t>(bytes);
+            }
+          } else {                      // 32 outputs, scales stored for 64 at a time
+            const int at = c & 1;
+            if (at == 0) bytes = 0;
+            float inv;
+            if constexpr (NV) {
+#pragma unroll
+              for (int b = 0; b < 2; ++b) {
+                bytes |= fp4_scale<true>(amax_bits(o + 16 * b, 16), out_t, inv) << (8 * (2 * at + b));
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[16 * b + i] *= inv;
+              }
+            } else {
+              bytes |= fp4_scale<false>(amax_bits(o, 32), 1.f, inv) << (8 * at);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] *= inv;
+            }
+            if (on) {
+              *reinterpret_cast<uint4*>(q8 + col / 2) =
+                  make_uint4(e2m1x8(o), e2m1x8(o + 8), e2m1x8(o + 16), e2m1x8(o + 24));
+              if (at == 1) {
+                uint8_t* s8 = g.out_s + fp4_scale_at(tile0, in_e, (col - 32) / (NV ? 16 : 32), out_chunks);
+                if constexpr (NV) *reinterpret_cast<uint32_t*>(s8) = bytes;
+                else *reinterpret_cast<uint16_t*>(s8) = static_cast<uint16_t>(bytes);
+              }
+            }
+          }
+        }
+        // the next 32 columns move up: one body for all four keeps the code small
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          v[0][i] = v[1][i];
+          v[1][i] = v[2][i];
+          v[2][i] = v[3][i];
+        }
+      }
+    }
+    gave_up(ok);
+  }
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync();
+  if (*abort_flag && threadIdx.x == 0) set_err(g.err, MOE_DEV_TIMEOUT);
+  if (warp == 1) {
+    // Given up (both CTAs): what is in flight ends (waits bounded) before TMEM
+    // is freed and shared memory left
+    if (*abort_flag && elect_one()) {
+      const uint64_t t0 = globaltimer_ns();
+      auto ends = [&](uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+        const uint32_t a = smem_u32(bar);
+        for (;;)
+          if (mbar_try_wait(a, parity) || globaltimer_ns() - t0 > limit_ns) break;
+      };
+      if (rank == 0) {
+        umma_commit_pair(drain_bar);
+        ends(drain_bar, 0, kWaitLimitNs);
+        for (uint32_t i = 0; i < STAGES; ++i) {
+          const StageDrain d = stage_drain(loads[0], loads[1], STAGES, i);
+          if (d.make_up) mbar_complete_tx(&full_bar[i], C::stage_tx);
+          if (d.arrive) mbar_arrive_expect_tx(&full_bar[i], C::stage_tx);
+          if (d.wait) ends(&full_bar[i], d.parity, 2 * kWaitLimitNs);
+        }
+        mbar_arrive_cluster(mapa_shared(smem_u32(drain_bar), 1));
+      } else {
+        ends(drain_bar, 0, 3 * kWaitLimitNs);
+      }
+    }
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 512);
+  }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+// a scale buffer as rows of 256 bytes; a box holds `chunks` whole chunks
+bool map_scales(CUtensorMap* m, const uint8_t* base, long long total, int chunks) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t gdim[2] = {256, static_cast<cuuint64_t>(2 * total)};
+  cuuint64_t gstride[1] = {256};
+  cuuint32_t bdim[2] = {256, static_cast<cuuint32_t>(2 * chunks)}, estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(base), gdim, gstride, bdim,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool NV, bool GATED>
+cudaError_t gemm_t(const CUtensorMap& ta, const CUtensorMap& tw, const Fp4GemmArgs& g, int num_sms,
+                   cudaStream_t s) {
+  using C = GC<NV>;
+  static_assert(C::smem(MOE_MAX_EXPERTS) <= 227 * 1024, "shared memory of a CTA");
+  auto kern = fp4_pair_kernel<NV, GATED>;
+  CUtensorMap tsa, tsw;
+  const int chunks = fp4_chunks(NV, g.K);
+  if (!map_scales(&tsa, g.a_s, g.a_tiles * chunks, Fp4Sf<NV>::chunks) ||
+      !map_scales(&tsw, g.w_s, g.w_tiles * chunks, Fp4Sf<NV>::chunks))
+    return cudaErrorInvalidValue;
+  static int clusters_of[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(num_sms / 2 * 2);
+  cfg.blockDim = dim3(GT);
+  cfg.dynamicSmemBytes = C::smem(MOE_MAX_EXPERTS);
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  int& clusters = clusters_of[dev];
+  if (clusters == 0) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(cfg.dynamicSmemBytes));
+    if (e != cudaSuccess) return e;
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+    if (e != cudaSuccess) return e;
+    clusters = n > 0 && n < num_sms / 2 ? n : num_sms / 2;
+  }
+  // at most so many units, however the rows lie
+  const long long units = (static_cast<long long>(g.M_cap) / (2 * GM) + (g.E < g.M_cap ? g.E : g.M_cap)) *
+                          ((g.N + GN - 1) / GN);
+  cfg.gridDim = dim3(2 * static_cast<unsigned>(units < clusters ? units : clusters));
+  return cudaLaunchKernelEx(&cfg, kern, ta, tw, tsa, tsw, g);
+}
+
+}  // namespace
+
+cudaError_t launch_fp4_gemm(const CUtensorMap& ta, const CUtensorMap& tw, const Fp4GemmArgs& g,
+                            int num_sms, cudaStream_t s) {
+  const bool gated = g.act == MOE_ACT_SWIGLU || g.act == MOE_ACT_GEGLU;
+  if (g.nv) return gated ? gemm_t<true, true>(ta, tw, g, num_sms, s) : gemm_t<true, false>(ta, tw, g, num_sms, s);
+  return gated ? gemm_t<false, true>(ta, tw, g, num_sms, s) : gemm_t<false, false>(ta, tw, g, num_sms, s);
+}
+
+}  // namespace moe

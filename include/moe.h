@@ -75,6 +75,19 @@ typedef uint16_t moe_bf16;
 /* element types of the operators that take more than one */
 #define MOE_TYPE_F32 0
 #define MOE_TYPE_BF16 1
+#define MOE_TYPE_FP4 2         /* (an output of moe_fp4_linear) 4 bits          */
+
+/* 4-bit formats */
+#define MOE_FP4_NV 0           /* blocks of 16, E4M3 scales, a float32 scale for
+                                  the tensor                                    */
+#define MOE_FP4_MX 1           /* blocks of 32, E8M0 scales (OCP MX v1.0)       */
+#define MOE_FP4_COLS 0         /* moe_fp4_quantize_weights: blocks along the
+                                  inner index                                   */
+#define MOE_FP4_ROWS 1         /* along the outer one                           */
+
+/* scores of moe_router_select */
+#define MOE_SCORE_SOFTMAX 0    /* softmax over all E logits                     */
+#define MOE_SCORE_SIGMOID 1    /* each logit's own                              */
 
 /* flags */
 #define MOE_FLAG_SAVE_H 1      /* forward also stores H (needed by backward)   */
@@ -755,6 +768,52 @@ int moe_router_loss_bwd(const void* logits, int logits_type, const int32_t* topk
                         void* dlogits, int dlogits_type, void* stream);
 
 /*
+ * moe_router_select - the router's choice by scores ([TE] "Transformer
+ * Engine이 제공하는 세 가지 구성 요소": gate, top-K selection, dispatch; the
+ * scores, the balancing bias and the groups are the common ones, the pages do
+ * not fix them).  topk_idx and probs go where moe_router_topk's go.
+ *   s_te = softmax over the E logits, or sigmoid(z_te)       (score)
+ *   c_te = s_te + bias_e             (bias [E] float32 or NULL; it moves the
+ *                                    choice alone and gets no gradient here)
+ *   groups of E / groups consecutive experts are scored by the sum of their
+ *   group_best (1 or 2) largest c (what a group lacks adds nothing); the
+ *   top_groups best ones stay (groups = top_groups: all)
+ *   topk_idx: the k largest c in them, in decreasing order; of equals, groups
+ *             or experts, the lower index.  The order is that of the real
+ *             numbers c (without a bias, of the logits): where float32 leaves
+ *             it in doubt, 64 bits decide.
+ *   probs:    scale s_tj / sum_i s_ti (renorm), or scale s_tj, i and j over
+ *             the k chosen
+ * An expert whose logit is NaN or at most bf16's lowest finite value (a mask),
+ * or whose c is NaN or -inf, takes no part; where fewer than k are left, the
+ * other picks are -1 with probability 0, and a sum of 0 gives probabilities 0.
+ *   logits [T, E] float32 or bf16 (logits_type MOE_TYPE_*), aligned to their
+ *   type; 1 <= k <= 32, k <= E / groups * top_groups; groups divides E, at most
+ *   32; group_best <= E / groups; scale > 0 and finite; T <= 2^30.  One launch.
+ */
+int moe_router_select(const void* logits, int logits_type, int T, int E, int k, int score,
+                      const float* bias, int groups, int top_groups, int group_best, int renorm,
+                      float scale, int32_t* topk_idx, float* probs, void* stream);
+
+/*
+ * moe_router_select_bwd - the logits' gradient from dprobs [T, k], the
+ * choice being constant ([Sonic] "역전파 계산 그래프 재작성하기": dS is what the
+ * experts' backward hands to the router).  With w = probs:
+ *   g_j = w_j (dprobs_j - sum_i w_i dprobs_i / scale)  (renorm), or w_j dprobs_j
+ *   sigmoid: dlogits_j = g_j (1 - s_j); softmax with renorm: g_j; both zero for
+ *   the experts that were not chosen
+ *   softmax: dlogits_e = [e chosen] g_e - s_e sum_j g_j  for every e
+ * Pairs with an id outside [0, E) take no part; an expert chosen twice by a
+ * token gets both terms.  topk_idx, probs and score, renorm, scale as in
+ * moe_router_select.  accumulate 1: dlogits (moe_router_loss_bwd's, say) +=
+ * the gradient.  dlogits [T, E] float32 or bf16, aligned to its type.  One launch.
+ */
+int moe_router_select_bwd(const void* logits, int logits_type, const int32_t* topk_idx,
+                          const float* probs, const float* dprobs, int T, int E, int k, int score,
+                          int renorm, float scale, int accumulate, void* dlogits,
+                          int dlogits_type, void* stream);
+
+/*
  * moe_grouped_linear - a product with bias, activation and residual in its
  * epilogue, over the experts' ragged rows or dense (E = 1): the router's
  * gate, a shared expert, experts with biases ([TE] "최적화 1: grouped GEMM";
@@ -815,6 +874,122 @@ int moe_grouped_linear_bwd(const moe_bf16* dout, const moe_bf16* z, const moe_bf
                            const moe_bf16* B, int b_layout, int act, int flags, moe_bf16* dz,
                            moe_bf16* da, moe_bf16* dB, float* dbias, void* workspace,
                            size_t ws_bytes, int32_t* err, void* stream);
+
+/*
+ * 4-bit floating point ([TE] "다음 단계: NVFP4, GEMM 융합 양자화, A2A 오버랩":
+ * NVFP4 after MXFP8; [CuTe] "핵심 아이디어 / 구조 / 동작 방식": its per-tensor
+ * statistic taken where the data is written).  A value is an E2M1 code (0,
+ * 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives; two a byte, the first in the low
+ * half) times its block's scale:
+ *   MOE_FP4_NV  blocks of 16: s = E4M3(amax / (6 t)), code = E2M1(v / (s t)),
+ *               value = code s t, t a float32 scale of the tensor (NULL: 1)
+ *   MOE_FP4_MX  blocks of 32: s = 2^(floor(log2 amax) - 2) (E8M0), code =
+ *               E2M1(v / s), value = code s
+ * Roundings are to nearest, ties to even, saturating; of bf16 values by a
+ * power-of-two t (moe_fp4_tensor_scale's) exactly so, by another t and of
+ * float32 values up to 2^-22 of a border.  A block that holds a NaN or an
+ * infinity reads back as NaN.
+ *   codes   [rows, K / 2]
+ *   scales  chunks of 512 bytes: 128 rows x 4 consecutive blocks of K (NV 64
+ *           values, MX 128), row r and block b of a chunk at byte (r % 32) * 16
+ *           + (r / 32) * 4 + b.  Row r of expert e, whose first row is off_e,
+ *           is row r % 128 of tile off_e / 128 + e + r / 128; chunk c of a
+ *           tile is number tile * C + c, C = K / 64 (NV) or ceil(K / 128) (MX).
+ *           Without offsets a buffer of E experts has off_e = e * rows / E.
+ *           moe_fp4_scale_bytes(rows, E, K, format) bytes in all.
+ * K a multiple of 64, at most 2^23; codes and scales 16-byte aligned.  Offsets
+ * that are not in order are clamped and their running maximum taken, in every
+ * call alike, and MOE_DEV_BAD_OFFSETS is set.
+ *
+ * moe_fp4_tensor_scale  t [E]: for src [E, n] bf16, of each e the smallest
+ *                       power of two with max|v| <= 6 * 448 t over its finite
+ *                       values (1 where there are none above 0).  n a multiple
+ *                       of 64.  Two launches.
+ * moe_fp4_quantize      src [rows, K] bf16 -> q, s.  offsets [E+1] (rows outside
+ *                       every expert are not written), or NULL: E experts of
+ *                       rows / E rows.  t [1] or NULL (MX: NULL).  One launch.
+ * moe_fp4_permute       moe_permute's / moe_permute_tokens' expert-major gather
+ *                       of src [T, K] into 4 bits; pad rows inside an expert are
+ *                       zeros, rows outside every expert are not written; with
+ *                       row_of_pair (may be NULL) each token is read and
+ *                       quantised once.  One launch.
+ * moe_fp4_quantize_weights  W [E, rows, cols] bf16, each expert of its own:
+ *                       along MOE_FP4_COLS, blocks along cols: q [E, rows,
+ *                       cols / 2] (a product that contracts cols); MOE_FP4_ROWS:
+ *                       blocks along rows, q [E, cols, rows / 2].  t [E] or
+ *                       NULL.  One launch.
+ * moe_fp4_dequantize    the values [rows, K], bf16 or float32 (type MOE_TYPE_*);
+ *                       offsets as in moe_fp4_quantize, t with t_per_expert 0:
+ *                       [1], 1: [E], or NULL.  One launch.
+ */
+size_t moe_fp4_scale_bytes(long long rows, int E, int K, int format);
+int moe_fp4_tensor_scale(const moe_bf16* src, int E, long long n, float* t, void* stream);
+int moe_fp4_quantize(const moe_bf16* src, const int32_t* offsets, int E, int rows, int K,
+                     int format, const float* t, uint8_t* q, uint8_t* s, int32_t* err,
+                     void* stream);
+int moe_fp4_permute(const moe_bf16* src, const int32_t* row_of_pair, const int32_t* pair_of_row,
+                    const int32_t* offsets, int E, int T, int k, int K, int M_cap, int format,
+                    const float* t, uint8_t* q, uint8_t* s, int32_t* err, void* stream);
+int moe_fp4_quantize_weights(const moe_bf16* W, int E, int rows, int cols, int along, int format,
+                             const float* t, uint8_t* q, uint8_t* s, void* stream);
+int moe_fp4_dequantize(const uint8_t* q, const uint8_t* s, const int32_t* offsets, int E,
+                       long long rows, int K, int format, const float* t, int t_per_expert,
+                       void* out, int type, int32_t* err, void* stream);
+
+/*
+ * moe_fp4_linear - moe_grouped_linear of operands in 4 bits, on block-scaled
+ * MMAs ([TE] "최적화 1: grouped GEMM"; [CuTe] "핵심 아이디어 / 구조 / 동작 방식").
+ * For the rows of each expert:
+ *   z = t_a t_e a_e w_e^T + bias_e     (products of codes and block scales
+ *                                      exact, sums float32)
+ *   out = act(z) + residual            (float32, rounded once)
+ *   a_q, a_s  [M_cap, K] as moe_fp4_quantize / _permute write them with these
+ *             offsets; a_t [1] or NULL
+ *   w_q, w_s  [E, N, K] as moe_fp4_quantize_weights writes them; w_t [E] or NULL
+ *   offsets, bias, act, residual, z as moe_grouped_linear's (offsets of any
+ *   alignment; z is rounded to bf16, act takes it before)
+ *   out  [M_cap, n_out] float32, bf16, or 4 bits (out_type MOE_TYPE_*): then
+ *        codes in `out` and scales in out_s, as moe_fp4_quantize would write
+ *        them of the float32 outputs, with tensor scale out_t [1] (NULL: 1;
+ *        MX: NULL), n_out a multiple of 64: the next product's a
+ * Both operands and a 4-bit output are of one format.  K, N multiples of 64, at
+ * most 2^23; pointers 16-byte aligned (t's to their type).  Rows outside every
+ * expert are not written.  Reruns are bitwise identical.  One launch.
+ *
+ * moe_fp4_linear_plan - which kernel it runs for these sizes on the current
+ * device: plan[0] the tokens of a tile of the few-row kernel (0: the 256 x 256
+ * tiles of CTA pairs), plan[1] the parts that the reduction is split into.  Host
+ * memory; nothing is launched.  For tests and measurements.
+ */
+int moe_fp4_linear(const uint8_t* a_q, const uint8_t* a_s, const float* a_t,
+                   const int32_t* offsets, int E, int M_cap, int K, int N, const uint8_t* w_q,
+                   const uint8_t* w_s, const float* w_t, int format, const moe_bf16* bias, int act,
+                   const moe_bf16* residual, moe_bf16* z, void* out, int out_type, uint8_t* out_s,
+                   const float* out_t, int32_t* err, void* stream);
+int moe_fp4_linear_plan(int E, int M_cap, int K, int N, int ragged, int plan[2]);
+
+/*
+ * moe_fp4_linear_bwd - its backward, straight through the operands'
+ * quantisation ([CuTe] kernel family "GroupGemm + dActivation").
+ *   dz = act'(z) dout          bf16 (act NONE: dout itself, z and dz unused)
+ *   da = dz4 w_e               bf16 [M_cap, K]: dz in 4 bits (NV with a tensor
+ *                              scale of its own), blocks along N, times the
+ *                              weights' copy wt_q, wt_s [E, K, N] with blocks
+ *                              along N; NULL: not wanted
+ *   dB_e = a_e^T dz_e          bf16 [E, K, N] (b_layout MOE_B_KN) or [E, N, K]
+ *                              (MOE_B_NK), from the bf16 a [M_cap, K] and dz on
+ *                              bf16 MMAs: a weight's gradient sums over tokens,
+ *                              whose 4-bit errors a sum of few would keep; or NULL
+ *   dbias_e                    float32 [E, N], from dz before its rounding; or NULL
+ * wt_t [E] or NULL; flags as moe_grouped_linear_bwd's.  workspace:
+ * moe_fp4_linear_bwd_workspace_size bytes, 16-byte aligned.  Up to eight launches.
+ */
+size_t moe_fp4_linear_bwd_workspace_size(int E, int M_cap, int N, int format);
+int moe_fp4_linear_bwd(const moe_bf16* dout, const moe_bf16* z, const moe_bf16* a,
+                       const int32_t* offsets, int E, int M_cap, int K, int N, const uint8_t* wt_q,
+                       const uint8_t* wt_s, const float* wt_t, int format, int b_layout, int act,
+                       int flags, moe_bf16* dz, moe_bf16* da, moe_bf16* dB, float* dbias,
+                       void* workspace, size_t ws_bytes, int32_t* err, void* stream);
 
 /*
  * Activation checkpoints in 8 bits: what the backward needs of the forward
