@@ -1261,8 +1261,9 @@ def _fp4_format(fmt):
 
 
 def fp4_scale_bytes(rows: int, E: int, K: int, fmt: str = "nvfp4") -> int:
-    """Bytes of the scales of E experts' ``rows`` rows of K values (moe_fp4_scale_bytes)."""
-    return int(lib().moe_fp4_scale_bytes(rows, E, K, _fp4_format(fmt)))
+    """Bytes of the scales of E experts' ``rows`` rows of K values
+    (moe_fp4_scale_bytes, without its check of the sizes)."""
+    return (rows // 128 + E) * (K // 64 if _fp4_format(fmt) == 0 else (K + 127) // 128) * 512
 
 
 def _fp4_t(t, n, fmt, name):

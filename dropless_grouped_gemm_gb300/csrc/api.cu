@@ -1562,7 +1562,7 @@ int moe_fp4_quantize_weights(const moe_bf16* W, int E, int rows, int cols, int a
   ev_begin(st);
   cudaError_t e;
   if (along == MOE_FP4_ROWS) {
-    e = moe::launch_fp4_quantize_t(W, E, rows, cols, nv, t, q, s, sms, st);
+    e = moe::launch_fp4_quantize_t(W, E, rows, cols, nv, t, q, s, st);
   } else {
     moe::Fp4QuantArgs a{};
     a.src = W; a.r = moe::Fp4Rows{nullptr, E, static_cast<long long>(E) * N, N}; a.K = K;

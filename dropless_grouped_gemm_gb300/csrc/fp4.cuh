@@ -65,7 +65,7 @@ cudaError_t launch_fp4_quantize(const Fp4QuantArgs& a, int num_sms, cudaStream_t
 
 // W [E, R, C] with blocks along R: q [E, C, R/2]
 cudaError_t launch_fp4_quantize_t(const uint16_t* W, int E, int R, int C, bool nv, const float* t,
-                                  uint8_t* q, uint8_t* s, int num_sms, cudaStream_t st);
+                                  uint8_t* q, uint8_t* s, cudaStream_t st);
 
 // the values [rows, K], bf16 or float32
 cudaError_t launch_fp4_dequantize(const uint8_t* q, const uint8_t* s, const Fp4Rows& r, int K,

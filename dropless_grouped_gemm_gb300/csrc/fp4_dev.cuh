@@ -68,15 +68,55 @@ __device__ __forceinline__ uint32_t fp4_scale(uint32_t amax_bits, float t, float
   }
 }
 
-// v * inv for a bf16 v and a power-of-two t: the quotient v / (s t) of an 8-bit
-// and a 4-bit significand either is one of the halves between two codes, or at
-// least 1/256 away from it, so rounding the float32 product (2^-23 off) to 12
-// bits puts back the ties that the reciprocal's rounding took apart.
-__device__ __forceinline__ float fp4_snap(float u) {
-  return __uint_as_float((__float_as_uint(u) + 0x800u) & ~0xfffu);
+// eight f16 pairs' halves -> eight codes (4 words of pairs)
+__device__ __forceinline__ uint32_t e2m1x8_h(const uint32_t* h) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f16x2 b0, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f16x2 b1, %2;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f16x2 b2, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f16x2 b3, %4;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(r)
+      : "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]));
+  return r;
 }
-__device__ __forceinline__ bool fp4_power_of_two(float t) {
-  return (__float_as_uint(t) & 0x7fffffu) == 0u;
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// A tensor scale as the quantisers of bf16 values use it.  With a power of two
+// (in 2^-100 .. 2^100, so that nothing under- or overflows) quotients need no
+// division: the quotient of an 8-bit significand and a 4-bit one (or 6, or their
+// product) either is one of the halves between two codes, or at least 1/256 away
+// from it, so rounding a float32 product with a reciprocal (2^-22 off at most)
+// to 11 or 12 bits gives the side, and the ties, of the exact quotient.
+struct Fp4Tensor {
+  float t, inv6, inv;
+  bool exact;
+};
+__device__ __forceinline__ Fp4Tensor fp4_tensor(float t) {
+  Fp4Tensor r;
+  r.t = t;
+  const uint32_t b = __float_as_uint(t);
+  r.exact = (b & 0x7fffffu) == 0u && b >= (27u << 23) && b <= (227u << 23);
+  r.inv = __uint_as_float((254u << 23) - b);      // (of a power of two)
+  r.inv6 = r.inv * (1.f / 6.f);
+  return r;
+}
+
+// the scale byte and the multiplier of a block of bf16 values
+template <bool NV>
+__device__ __forceinline__ uint32_t fp4_scale_bf16(uint32_t amax_bits, const Fp4Tensor& t,
+                                                   float& inv) {
+  if (!NV || !t.exact) return fp4_scale<NV>(amax_bits, t.t, inv);
+  if (amax_bits >= 0x7f800000u) { inv = 0.f; return 0x7fu; }
+  const float u = __uint_as_float((__float_as_uint(__uint_as_float(amax_bits) * t.inv6) + 0x800u) & ~0xfffu);
+  const uint32_t s = e4m3x2(u, 0.f) & 0xffu;
+  inv = s ? __fdividef(1.f, e4m3_value(s)) * t.inv : 0.f;
+  return s;
 }
 
 // 8 words of bf16 pairs (16 values) -> the largest magnitude's 16 bits
@@ -87,19 +127,22 @@ __device__ __forceinline__ uint32_t bf16_amax16(const uint32_t* p) {
   return max(m & 0xffffu, m >> 16);
 }
 
-// 16 bf16 values (8 words) -> 16 codes (2 words)
-__device__ __forceinline__ uint2 fp4_codes16(const uint32_t* p, float inv, bool snap) {
-  float u[16];
+// 16 bf16 values (8 words) -> 16 codes (2 words).  exact: through f16's 11 bits
+template <bool NV>
+__device__ __forceinline__ uint2 fp4_codes16(const uint32_t* p, float inv, bool exact) {
+  if (NV && !exact) {
+    float u[16];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    u[2 * i] = bf16_lo(p[i]) * inv;
-    u[2 * i + 1] = bf16_hi(p[i]) * inv;
+    for (int i = 0; i < 8; ++i) {
+      u[2 * i] = bf16_lo(p[i]) * inv;
+      u[2 * i + 1] = bf16_hi(p[i]) * inv;
+    }
+    return make_uint2(e2m1x8(u), e2m1x8(u + 8));
   }
-  if (snap) {
+  uint32_t h[8];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) u[i] = fp4_snap(u[i]);
-  }
-  return make_uint2(e2m1x8(u), e2m1x8(u + 8));
+  for (int i = 0; i < 8; ++i) h[i] = f16x2(bf16_lo(p[i]) * inv, bf16_hi(p[i]) * inv);
+  return make_uint2(e2m1x8_h(h), e2m1x8_h(h + 4));
 }
 
 // an expert's rows and the number of its first scale tile

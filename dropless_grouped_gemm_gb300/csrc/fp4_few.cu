@@ -377,7 +377,9 @@ __global__ void __launch_bounds__(FT, 1)
       if (lane == 0) {
         ok = mbar_wait(&tfull_bar[buf], (local >> 1) & 1, abort_flag);
         // the previous unit's sums have been read
-        if (ok) ok = mbar_wait_cluster(rempty_bar, (local & 1) ^ 1, abort_flag);
+        if (ok)
+          ok = split == 1 ? mbar_wait(rempty_bar, (local & 1) ^ 1, abort_flag)
+                          : mbar_wait_cluster(rempty_bar, (local & 1) ^ 1, abort_flag);
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) break;
@@ -399,16 +401,28 @@ __global__ void __launch_bounds__(FT, 1)
         cluster_wait();
         joined = true;
       }
-      // the tile's sums are in shared memory, a CTA's part in each: tell every
-      // CTA of the cluster, and wait for all
+      // The tile's sums are in shared memory, a CTA's part in each: tell every
+      // CTA of the cluster, and wait for all.  Every lane reads what other warps
+      // wrote, so every lane acquires (after lane 0 has waited the phase is
+      // complete, and the next one needs this warp: no waiting).  A CTA on its
+      // own stays with its own barriers, at CTA scope: a unit of 8 stages took
+      // 4.1 us at cluster scope, most of it here.
       __syncwarp();
-      if (lane < split) mbar_arrive_cluster(mapa_shared(smem_u32(rfull_bar), lane));
-      if (lane == 0) ok = mbar_wait_cluster(rfull_bar, local & 1, abort_flag);
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok) break;
-      // every lane reads what other warps wrote, so every lane acquires (the
-      // phase is complete and the next one needs this warp: no waiting)
-      while (!mbar_try_wait_cluster(smem_u32(rfull_bar), local & 1) && !*abort_flag) {}
+      if (split == 1) {
+        if (lane == 0) {
+          mbar_arrive(rfull_bar);
+          ok = mbar_wait(rfull_bar, local & 1, abort_flag);
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        while (!mbar_try_wait(smem_u32(rfull_bar), local & 1) && !*abort_flag) {}
+      } else {
+        if (lane < split) mbar_arrive_cluster(mapa_shared(smem_u32(rfull_bar), lane));
+        if (lane == 0) ok = mbar_wait_cluster(rfull_bar, local & 1, abort_flag);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        while (!mbar_try_wait_cluster(smem_u32(rfull_bar), local & 1) && !*abort_flag) {}
+      }
       if (c < g.N) {
         const float* src = red + (tid & 15) * 8;
         const int k0 = rank + (tid >> 4) * split;
@@ -424,7 +438,11 @@ __global__ void __launch_bounds__(FT, 1)
       // this warp has read its peers' sums: the arrival releases the reads of
       // all its lanes, after which the peers overwrite what was read
       __syncwarp();
-      if (lane < split) mbar_arrive_cluster(mapa_shared(smem_u32(rempty_bar), lane));
+      if (split == 1) {
+        if (lane == 0) mbar_arrive(rempty_bar);
+      } else if (lane < split) {
+        mbar_arrive_cluster(mapa_shared(smem_u32(rempty_bar), lane));
+      }
     }
     if (!joined) cluster_wait();
   }
@@ -533,6 +551,16 @@ cudaError_t few_t(const CUtensorMap& tw, const CUtensorMap& tx, const Fp4GemmArg
 
 }  // namespace
 
+// The choice, by an estimate of the time in nanoseconds with these measured
+// rates.  This kernel: 3.5 us of launch, prologue and end; a stage (256 of K)
+// 260 ns, 330 with more than 16 tokens, or its 18 KB of weights' share of 6.6 TB/s
+// where no other tile reads them; ending a tile 1 us, joining a split 2.5.  The
+// pairs' kernel: 7.6 us, a stage 320 ns (or its 36 KB's share), a tile's end 2.1
+// us, a tile 4.3 us at least.  Measured, us, this kernel / the pairs': dense 64 x
+// 4096 x 4096 8.7 / 13.4, 256 rows 11.4 / 15.0, 512 rows 16.7 / 15.1, 1024 rows
+// 28.7 / 14.8, 256 x 7168 x 2048 11.3 / 18.6; 57 experts with 128 rows, 2048 x
+// 7168 73.6 / 100.7, with 2000 rows 107.8 / 114.1; 8 experts, 4096 x 4096, 512
+// rows 25.3 / 25.6, 1000 rows 32.2 / 28.9.
 Fp4Plan fp4_plan(int E, int M_cap, int K, int N, bool ragged, int num_sms) {
   const long long active = ragged ? (E < M_cap ? E : M_cap) : 1;
   const long long avg = (M_cap + active - 1) / active;
@@ -545,10 +573,10 @@ Fp4Plan fp4_plan(int E, int M_cap, int K, int N, bool ragged, int num_sms) {
     if (split > 1 && kb < 2 * split) break;
     const long long fit = few_clusters(split, num_sms);
     const long long ctas = (units < fit ? units : fit) * split;
-    long long stage = 200;
+    long long stage = avg <= kFp4FewBox ? 260 : 330;
     if (avg <= TN && ctas * 18432 / 6600 > stage) stage = ctas * 18432 / 6600;
     const long long join = split == 1 ? 1000 : 2500;
-    const long long cost = (units + fit - 1) / fit * ((kb + split - 1) / split * stage + join);
+    const long long cost = 3500 + (units + fit - 1) / fit * ((kb + split - 1) / split * stage + join);
     if (best < 0 || cost < best) {
       best = cost;
       p.split = split;
@@ -556,7 +584,11 @@ Fp4Plan fp4_plan(int E, int M_cap, int K, int N, bool ragged, int num_sms) {
   }
   const long long tiles = (avg + 255) / 256 * active * ((N + 255) / 256);
   const long long places = num_sms / 2;
-  const long long big = (tiles + places - 1) / places * (kb * 330 + 1000) + 5000;
+  long long stage = 320;
+  if (avg <= 256 && (tiles < places ? tiles : places) * 36864 / 6600 > stage)
+    stage = (tiles < places ? tiles : places) * 36864 / 6600;
+  const long long tile = kb * stage + 2100;
+  const long long big = 7600 + (tiles + places - 1) / places * (tile > 4300 ? tile : 4300);
   return big < best ? Fp4Plan{} : p;
 }
 

@@ -5,13 +5,21 @@
 //   z = t_a t_e sum_blocks s_a s_w (sum of a block's code products) + bias
 //   out = act(z) + residual
 // Persistent and warp-specialised in CTA pairs, as the MXFP8 grouped GEMM: 256
-// rows x 256 columns a tile, each CTA with 128 rows of a and 128 columns of w
-// in shared memory (2-SM MMAs, M = 256, N = 256, K = 64).  A stage is one
-// 128-byte swizzle row of K (256 values): 32 KB of codes and, NV, 6 KB of
-// scales (MX 3) for 33.5 MFLOP.  TMEM: a 256-column accumulator and each
-// stage's scale columns; the epilogue moves the accumulator to registers and
-// releases it at once, so the next tile's MMAs overlap bias, activation,
-// quantisation and stores.
+// rows x 256 columns a tile, each CTA with 128 rows of a and 128 columns of w in
+// shared memory (2-SM MMAs, M = 256, N = 256, K = 64).  A stage is one 128-byte
+// swizzle row of K (256 values): 32 KB of codes and, NV, 6 KB of scales (MX 3)
+// for 33.5 MFLOP.  TMEM: a 256-column accumulator and each stage's scale columns;
+// the epilogue moves the accumulator to registers and releases it at once, so
+// the next tile's MMAs overlap bias, activation, quantisation and stores.
+//
+// Measured, with the clock at 1.9 GHz: a stage's four MMAs take 0.274 us (MX, 130
+// cycles each: the rate of 9 PFLOP/s) and 0.32 us (NV, whose twelve copies of
+// scales into TMEM take their part), and about 2 us pass between two tiles'
+// MMAs (commit, TMEM to registers, release in both CTAs).  Tiles of 192 columns
+// leave TMEM for two accumulators and hide those, but an MMA of N = 192 takes 123
+// cycles (142 NV), what one of N = 256 takes: 8192 x 8192 x 4864 109 us in place of
+// 96 (MX), 122 of 105 (NV); 8192 x 1024 x 4864 37 of 41.  Pairs that share a's rows
+// by multicast changed nothing (0.258 us a stage of 192 columns either way).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -24,11 +32,13 @@
 namespace moe {
 namespace {
 
-constexpr int GT = 320;                          // threads
-constexpr int GEPI = 8;                          // epilogue warps
+constexpr int GEPI = 16;                         // epilogue warps
+constexpr int GT = 64 + 32 * GEPI;               // threads
+constexpr int GCOLS = 64;                        // columns of a tile that an epilogue warp takes
 constexpr int GM = 128;                          // rows, and columns of w, that a CTA holds
 constexpr int GN = 256;                          // columns of a tile
 constexpr int OP_BYTES = GM * 128;               // 16 KB: 128 rows x 256 codes
+constexpr int BOX_BYTES = 32 * 64;               // an epilogue warp's, for its stores
 constexpr int STAGES = 5;
 constexpr int SF_TMEM = GN;                      // scale columns after the accumulator
 
@@ -39,10 +49,15 @@ struct GC {
   static constexpr int stage_tx = stage_bytes + sf_bytes;      // a CTA's bytes
   static constexpr int sf_cols = 3 * Fp4Sf<NV>::cols;
   static_assert(SF_TMEM + STAGES * sf_cols <= 512, "TMEM columns");
+  // the tables of many experts leave NV no room for the epilogue's boxes
+  static constexpr int box_experts = NV ? 448 : MOE_MAX_EXPERTS;
+  static __host__ __device__ constexpr bool boxes(int E) { return E <= box_experts; }
   static constexpr size_t smem(int E) {
-    return 1024 + static_cast<size_t>(STAGES) * stage_tx + (2 * STAGES + 4) * 8 + 32 +
-           2 * (E + 1) * 4;
+    return 1024 + static_cast<size_t>(STAGES) * stage_tx + (boxes(E) ? GEPI * BOX_BYTES : 0) +
+           (2 * STAGES + 4) * 8 + 32 + 2 * (E + 1) * 4;
   }
+  static constexpr size_t most =
+      smem(MOE_MAX_EXPERTS) > smem(box_experts) ? smem(MOE_MAX_EXPERTS) : smem(box_experts);
 };
 
 struct GTile {
@@ -50,6 +65,7 @@ struct GTile {
   long long tile;           // its scale tile
 };
 
+// unit u: 256 rows x 256 columns, of which CTA `rank` of the pair has 128 rows
 __device__ __forceinline__ GTile gemm_tile(const Fp4GemmArgs& g, const int* s_off, const int* s_ts,
                                            int u, int rank) {
   const int e = fp4_expert_of(s_ts, g.E, u);
@@ -66,64 +82,103 @@ __device__ __forceinline__ GTile gemm_tile(const Fp4GemmArgs& g, const int* s_of
   return t;
 }
 
-// Epilogue of 32 accumulator columns from `col` of row `row` (one thread):
-// everything but the 4-bit output, which the caller quantises from v (32
-// outputs, or 16 when gated).
-template <bool GATED>
-__device__ __forceinline__ void gemm_out32(const Fp4GemmArgs& g, float alpha, int e, long long row,
-                                           int col, bool on, const uint32_t (&acc)[32],
-                                           float (&v)[32]) {
-  const uint16_t* bias = g.bias ? g.bias + static_cast<long long>(e) * g.N + col : nullptr;
+// What a kernel's epilogue can do: the plain one adds a bias alone (a second
+// product of an MLP, a data gradient), without the tests and the registers of
+// the others.
+enum class Epi { kPlain, kFull, kGated };
+
+// A warp's 32 rows of a tile, from the warp's first column on
+struct GRows {
+  const uint16_t* bias;     // the expert's, or NULL
+  const uint16_t* residual; // this thread's row
+  uint8_t* box;             // the warp's 2 KB of shared memory; NULL: none
+  int rows;                 // valid ones
+  bool on;                  // this thread's is
+};
+
+// 64 bytes of each row (w: this thread's) to `dst` (the first row's), rows
+// `pitch` bytes apart.  Through the box, so that four lanes write one row's 64
+// bytes: half as many requests and whole sectors (8191 x 1024 x 4096 bf16 53 us
+// without, 42 with; 8192 x 1024 x 4864 float32 76 us, 58).
+__device__ __forceinline__ void store_rows(const GRows& p, uint8_t* dst, long long pitch,
+                                           const uint32_t (&w)[16]) {
+  const int lane = threadIdx.x & 31;
+  if (p.box == nullptr) {
+    if (p.on) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<uint4*>(dst + lane * pitch + 16 * j) =
+            make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+    }
+    return;
+  }
+  // 16-byte piece j of row r at place j ^ (r / 2 % 4): free of bank conflicts both ways
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    *reinterpret_cast<uint4*>(p.box + lane * 64 + ((j ^ ((lane >> 1) & 3)) * 16)) =
+        make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+  __syncwarp();
+  const int j = lane & 3;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * i + (lane >> 2);
+    const uint4 v = *reinterpret_cast<const uint4*>(p.box + r * 64 + ((j ^ ((r >> 1) & 3)) * 16));
+    if (r < p.rows) *reinterpret_cast<uint4*>(dst + r * pitch + 16 * j) = v;
+  }
+  __syncwarp();
+}
+
+// 8 pre-activations, the i-th of the warp's columns on
+__device__ __forceinline__ void gemm_z8(const GRows& p, float alpha, int i, const uint32_t* acc,
+                                        float (&z)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) z[j] = __uint_as_float(acc[j]) * alpha;
+  if (p.bias) {
+    const uint4 b = __ldg(reinterpret_cast<const uint4*>(p.bias + i));
+    const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      z[2 * j] += bf16_lo(bw[j]);
+      z[2 * j + 1] += bf16_hi(bw[j]);
+    }
+  }
+}
+// 32 of them in bf16
+__device__ __forceinline__ void gemm_z32(const GRows& p, float alpha, int i, const uint32_t* acc,
+                                         uint32_t (&w)[16]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     float z[8];
-    uint4 b = make_uint4(0, 0, 0, 0);
-    if (bias) b = __ldg(reinterpret_cast<const uint4*>(bias) + j);
-    const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
+    gemm_z8(p, alpha, i + 8 * j, acc + 8 * j, z);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      z[2 * i] = fmaf(__uint_as_float(acc[8 * j + 2 * i]), alpha, bf16_lo(bw[i]));
-      z[2 * i + 1] = fmaf(__uint_as_float(acc[8 * j + 2 * i + 1]), alpha, bf16_hi(bw[i]));
-    }
-    if (g.z && on)
-      *reinterpret_cast<uint4*>(g.z + row * g.N + col + 8 * j) =
-          make_uint4(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]), pack_bf16x2(z[4], z[5]),
-                     pack_bf16x2(z[6], z[7]));
-    if constexpr (GATED) {
-      float u[4];
-      linear_glu(g.act, z, u);
-      if (g.residual && on) {
-        const uint2 r = *reinterpret_cast<const uint2*>(g.residual + row * g.ldo + col / 2 + 4 * j);
-        u[0] += bf16_lo(r.x); u[1] += bf16_hi(r.x); u[2] += bf16_lo(r.y); u[3] += bf16_hi(r.y);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[4 * j + i] = u[i];
-    } else {
-      linear_act(g.act, z);
-      if (g.residual && on) {
-        const uint4 r = *reinterpret_cast<const uint4*>(g.residual + row * g.ldo + col + 8 * j);
-        const uint32_t rw[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) { z[2 * i] += bf16_lo(rw[i]); z[2 * i + 1] += bf16_hi(rw[i]); }
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[8 * j + i] = z[i];
-    }
+    for (int m = 0; m < 4; ++m) w[4 * j + m] = pack_bf16x2(z[2 * m], z[2 * m + 1]);
   }
-  constexpr int NO = GATED ? 16 : 32;
-  if (!on || g.out_q) return;
-  const long long at = row * g.ldo + (GATED ? col / 2 : col);
-  if (g.out_f32) {
+}
+// the outputs of 8 accumulator columns: 8, or 4 when gated
+template <bool GATED>
+__device__ __forceinline__ void gemm_out8(const GRows& p, int act, float alpha, int i,
+                                          const uint32_t* acc, float* v) {
+  float z[8];
+  gemm_z8(p, alpha, i, acc, z);
+  if constexpr (GATED) {
+    float u[4];
+    linear_glu(act, z, u);
+    if (p.residual && p.on) {
+      const uint2 r = *reinterpret_cast<const uint2*>(p.residual + i / 2);
+      u[0] += bf16_lo(r.x); u[1] += bf16_hi(r.x); u[2] += bf16_lo(r.y); u[3] += bf16_hi(r.y);
+    }
 #pragma unroll
-    for (int i = 0; i < NO / 4; ++i)
-      *reinterpret_cast<float4*>(g.out_f32 + at + 4 * i) =
-          make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    for (int j = 0; j < 4; ++j) v[j] = u[j];
   } else {
+    linear_act(act, z);
+    if (p.residual && p.on) {
+      const uint4 r = *reinterpret_cast<const uint4*>(p.residual + i);
+      const uint32_t rw[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-    for (int i = 0; i < NO / 8; ++i)
-      *reinterpret_cast<uint4*>(g.out + at + 8 * i) =
-          make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
-                     pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+      for (int j = 0; j < 4; ++j) { z[2 * j] += bf16_lo(rw[j]); z[2 * j + 1] += bf16_hi(rw[j]); }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = z[j];
   }
 }
 
@@ -134,19 +189,22 @@ __device__ __forceinline__ uint32_t amax_bits(const float* v, int n) {
   return m;
 }
 
-template <bool NV, bool GATED>
+template <bool NV, Epi EPI>
 __global__ void __launch_bounds__(GT, 1)
     fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW,
                     const __grid_constant__ CUtensorMap tmSA,
                     const __grid_constant__ CUtensorMap tmSW, const Fp4GemmArgs g) {
   using C = GC<NV>;
   using SF = Fp4Sf<NV>;
+  constexpr bool GATED = EPI == Epi::kGated;
   constexpr uint32_t IDESC = fp4_idesc<NV>(2 * GM, GN);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sf_region = smem + STAGES * C::stage_bytes;
-  uint64_t* full_bar = reinterpret_cast<uint64_t*>(sf_region + STAGES * C::sf_bytes);
+  uint8_t* boxes = sf_region + STAGES * C::sf_bytes;
+  uint64_t* full_bar =
+      reinterpret_cast<uint64_t*>(boxes + (C::boxes(g.E) ? GEPI * BOX_BYTES : 0));
   uint64_t* empty_bar = full_bar + STAGES;
   uint64_t* tfull_bar = empty_bar + STAGES;
   uint64_t* tempty_bar = tfull_bar + 1;
@@ -287,7 +345,7 @@ __global__ void __launch_bounds__(GT, 1)
       gave_up(ok);
     }
   } else {
-    // epilogue: warpgroup wg takes 128 of the tile's columns, warp q of it 32
+    // epilogue: warpgroup wg takes 64 of the tile's columns, warp q of it 32
     // rows, a thread one row
     const int q = warp & 3, wg = (warp - 2) >> 2;
     const int r = q * 32 + lane;
@@ -299,17 +357,33 @@ __global__ void __launch_bounds__(GT, 1)
     for (int u = unit0; u < units && ok; u += unit_step, ++local) {
       const GTile t = gemm_tile(g, s_off, s_ts, u, rank);
       const float alpha = fp4_alpha(g, t.e);
+      const int col0 = t.n0 + wg * GCOLS;
+      const bool mine = col0 < g.N && q * 32 < t.rows;
+      // the warp's first row, this thread's row, and where their outputs begin
+      const long long row0 = static_cast<long long>(t.row0) + q * 32;
+      const long long row = row0 + lane;
+      const int ocol = GATED ? col0 / 2 : col0;
+      GRows p;
+      p.bias = g.bias ? g.bias + static_cast<long long>(t.e) * g.N + col0 : nullptr;
+      p.residual = g.residual ? g.residual + row * g.ldo + ocol : nullptr;
+      p.box = C::boxes(g.E) ? boxes + (warp - 2) * BOX_BYTES : nullptr;
+      p.rows = min(32, t.rows - q * 32);
+      p.on = r < t.rows;
+      const bool on = p.on;
+      uint8_t* out = g.out ? reinterpret_cast<uint8_t*>(g.out + row0 * g.ldo + ocol)
+                           : reinterpret_cast<uint8_t*>(g.out_f32 + row0 * g.ldo + ocol);
+      const long long pitch = static_cast<long long>(g.ldo) * (g.out ? 2 : 4);
+      uint8_t* zp = g.z ? reinterpret_cast<uint8_t*>(g.z + row0 * g.N + col0) : nullptr;
+      if (p.bias && mine) asm volatile("prefetch.global.L1 [%0];" ::"l"(p.bias));
       if (lane == 0) ok = mbar_wait(tfull_bar, local & 1, abort_flag);
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) break;
       tc_fence_after();
-      const int col0 = t.n0 + wg * GM;
-      const bool mine = col0 < g.N && q * 32 < t.rows;
-      uint32_t v[4][32];
+      uint32_t v[2][32];
       if (mine) {
-        const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + wg * GM;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(tb + c * 32, v[c]);
+        const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + wg * GCOLS;
+        tmem_ld32(tb, v[0]);
+        tmem_ld32(tb + 32, v[1]);
         tmem_wait_ld();
       }
       tc_fence_before();
@@ -319,83 +393,144 @@ __global__ void __launch_bounds__(GT, 1)
         else mbar_arrive(tempty_bar);
       }
       if (!mine) continue;
-      const bool on = r < t.rows;
-      const long long row = static_cast<long long>(t.row0) + r;
-      const int last = min(4, (g.N - col0) / 32);
+      if constexpr (EPI == Epi::kPlain) {
+        if (g.out) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t w[16];
+            gemm_z32(p, alpha, 32 * c, v[c], w);
+            store_rows(p, out + 64 * c, pitch, w);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t w[16];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              float z[8];
+              gemm_z8(p, alpha, 16 * c + 8 * j, v[c / 2] + 16 * (c % 2) + 8 * j, z);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) w[8 * j + i] = __float_as_uint(z[i]);
+            }
+            store_rows(p, out + 64 * c, pitch, w);
+          }
+        }
+        continue;
+      }
       const long long tile0 = fp4_tile0(s_off[t.e], t.e);
       const long long in_e = row - s_off[t.e];
-      uint32_t bytes = 0;               // scale bytes of up to 64 outputs
+      uint32_t bytes = 0;
       float held[GATED && !NV ? 16 : 1];
+      uint32_t half[GATED ? 8 : 1];
+      // one body for both halves keeps the code small
 #pragma unroll 1
-      for (int c = 0; c < last; ++c) {
+      for (int c = 0; c < 2; ++c) {
         const int col = col0 + 32 * c;
-        float o[32];
-        gemm_out32<GATED>(g, alpha, t.e, row, col, on, v[0], o);
-        if (g.out_q) {
-          uint8_t* q8 = g.out_q + row * (g.ldo / 2);
-          if constexpr (GATED) {
-            const int oc = col / 2;     // 16 outputs
+        if (zp) {
+          uint32_t w[16];
+          gemm_z32(p, alpha, 32 * c, v[0], w);
+          store_rows(p, zp + 64 * c, static_cast<long long>(g.N) * 2, w);
+        }
+        if constexpr (GATED) {
+          float o[16];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            gemm_out8<true>(p, g.act, alpha, 32 * c + 8 * j, v[0] + 8 * j, o + 4 * j);
+          if (g.out) {
+            if (c == 0) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) half[i] = pack_bf16x2(o[2 * i], o[2 * i + 1]);
+            } else {
+              uint32_t w[16];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                w[i] = half[i];
+                w[8 + i] = pack_bf16x2(o[2 * i], o[2 * i + 1]);
+              }
+              store_rows(p, out, pitch, w);
+            }
+          } else if (g.out_f32) {
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i]);
+            store_rows(p, out + 64 * c, pitch, w);
+          } else {                      // 16 outputs from oc on
+            const int oc = col / 2;
+            uint8_t* q8 = g.out_q + row * (g.ldo / 2) + oc / 2;
             if constexpr (NV) {
               float inv;
               bytes |= fp4_scale<true>(amax_bits(o, 16), out_t, inv) << (8 * c);
 #pragma unroll
               for (int i = 0; i < 16; ++i) o[i] *= inv;
-              if (on) *reinterpret_cast<uint2*>(q8 + oc / 2) = make_uint2(e2m1x8(o), e2m1x8(o + 8));
-              if (c == 3 && on)
-                *reinterpret_cast<uint32_t*>(g.out_s + fp4_scale_at(tile0, in_e, col0 / 32, out_chunks)) = bytes;
-            } else if ((c & 1) == 0) {
+              if (on) {
+                *reinterpret_cast<uint2*>(q8) = make_uint2(e2m1x8(o), e2m1x8(o + 8));
+                if (c == 1)
+                  *reinterpret_cast<uint16_t*>(g.out_s + fp4_scale_at(tile0, in_e, col0 / 32, out_chunks)) =
+                      static_cast<uint16_t>(bytes);
+              }
+            } else if (c == 0) {
 #pragma unroll
               for (int i = 0; i < 16; ++i) held[i] = o[i];
             } else {
               float inv;
               const uint32_t s = fp4_scale<false>(max(amax_bits(held, 16), amax_bits(o, 16)), 1.f, inv);
-              bytes |= s << (4 * (c - 1));
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
                 held[i] *= inv;
                 o[i] *= inv;
               }
-              if (on)
-                *reinterpret_cast<uint4*>(q8 + (oc - 16) / 2) =
+              if (on) {
+                *reinterpret_cast<uint4*>(q8 - 8) =
                     make_uint4(e2m1x8(held), e2m1x8(held + 8), e2m1x8(o), e2m1x8(o + 8));
-              if (c == 3 && on)
-                *reinterpret_cast<uint16_t*>(g.out_s + fp4_scale_at(tile0, in_e, col0 / 64, out_chunks)) =
-                    static_cast<uint16_t>(bytes);
+                g.out_s[fp4_scale_at(tile0, in_e, col0 / 64, out_chunks)] = static_cast<uint8_t>(s);
+              }
             }
-          } else {                      // 32 outputs, scales stored for 64 at a time
-            const int at = c & 1;
-            if (at == 0) bytes = 0;
+          }
+        } else {
+          float o[32];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            gemm_out8<false>(p, g.act, alpha, 32 * c + 8 * j, v[0] + 8 * j, o + 8 * j);
+          if (g.out) {
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(o[2 * i], o[2 * i + 1]);
+            store_rows(p, out + 64 * c, pitch, w);
+          } else if (g.out_f32) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t w[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[16 * h + i]);
+              store_rows(p, out + 128 * c + 64 * h, pitch, w);
+            }
+          } else {                      // 32 outputs from col on
             float inv;
             if constexpr (NV) {
 #pragma unroll
               for (int b = 0; b < 2; ++b) {
-                bytes |= fp4_scale<true>(amax_bits(o + 16 * b, 16), out_t, inv) << (8 * (2 * at + b));
+                bytes |= fp4_scale<true>(amax_bits(o + 16 * b, 16), out_t, inv) << (8 * (2 * c + b));
 #pragma unroll
                 for (int i = 0; i < 16; ++i) o[16 * b + i] *= inv;
               }
             } else {
-              bytes |= fp4_scale<false>(amax_bits(o, 32), 1.f, inv) << (8 * at);
+              bytes |= fp4_scale<false>(amax_bits(o, 32), 1.f, inv) << (8 * c);
 #pragma unroll
               for (int i = 0; i < 32; ++i) o[i] *= inv;
             }
             if (on) {
-              *reinterpret_cast<uint4*>(q8 + col / 2) =
+              *reinterpret_cast<uint4*>(g.out_q + row * (g.ldo / 2) + col / 2) =
                   make_uint4(e2m1x8(o), e2m1x8(o + 8), e2m1x8(o + 16), e2m1x8(o + 24));
-              if (at == 1) {
-                uint8_t* s8 = g.out_s + fp4_scale_at(tile0, in_e, (col - 32) / (NV ? 16 : 32), out_chunks);
+              if (c == 1) {
+                uint8_t* s8 = g.out_s + fp4_scale_at(tile0, in_e, col0 / (NV ? 16 : 32), out_chunks);
                 if constexpr (NV) *reinterpret_cast<uint32_t*>(s8) = bytes;
                 else *reinterpret_cast<uint16_t*>(s8) = static_cast<uint16_t>(bytes);
               }
             }
           }
         }
-        // the next 32 columns move up: one body for all four keeps the code small
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          v[0][i] = v[1][i];
-          v[1][i] = v[2][i];
-          v[2][i] = v[3][i];
-        }
+        for (int i = 0; i < 32; ++i) v[0][i] = v[1][i];
       }
     }
     gave_up(ok);
@@ -459,18 +594,20 @@ bool map_scales(CUtensorMap* m, const uint8_t* base, long long total, int chunks
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool NV, bool GATED>
+template <bool NV, Epi EPI>
 cudaError_t gemm_t(const CUtensorMap& ta, const CUtensorMap& tw, const Fp4GemmArgs& g, int num_sms,
                    cudaStream_t s) {
   using C = GC<NV>;
-  static_assert(C::smem(MOE_MAX_EXPERTS) <= 227 * 1024, "shared memory of a CTA");
-  auto kern = fp4_pair_kernel<NV, GATED>;
+  static_assert(C::most <= 227 * 1024, "shared memory of a CTA");
+  auto kern = fp4_pair_kernel<NV, EPI>;
   CUtensorMap tsa, tsw;
   const int chunks = fp4_chunks(NV, g.K);
   if (!map_scales(&tsa, g.a_s, g.a_tiles * chunks, Fp4Sf<NV>::chunks) ||
       !map_scales(&tsw, g.w_s, g.w_tiles * chunks, Fp4Sf<NV>::chunks))
     return cudaErrorInvalidValue;
-  static int clusters_of[64] = {};
+  // the pairs that the device holds at once and the shared-memory attribute, set
+  // up once per device and instantiation
+  static int pairs_of[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -483,24 +620,25 @@ cudaError_t gemm_t(const CUtensorMap& ta, const CUtensorMap& tw, const Fp4GemmAr
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(num_sms / 2 * 2);
   cfg.blockDim = dim3(GT);
-  cfg.dynamicSmemBytes = C::smem(MOE_MAX_EXPERTS);
+  cfg.dynamicSmemBytes = C::most;
   cfg.stream = s;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  int& clusters = clusters_of[dev];
-  if (clusters == 0) {
+  int& pairs = pairs_of[dev];
+  if (pairs == 0) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(cfg.dynamicSmemBytes));
+                             static_cast<int>(C::most));
     if (e != cudaSuccess) return e;
     int n = 0;
     e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
     if (e != cudaSuccess) return e;
-    clusters = n > 0 && n < num_sms / 2 ? n : num_sms / 2;
+    pairs = n > 0 && n < num_sms / 2 ? n : num_sms / 2;
   }
   // at most so many units, however the rows lie
   const long long units = (static_cast<long long>(g.M_cap) / (2 * GM) + (g.E < g.M_cap ? g.E : g.M_cap)) *
                           ((g.N + GN - 1) / GN);
-  cfg.gridDim = dim3(2 * static_cast<unsigned>(units < clusters ? units : clusters));
+  cfg.gridDim = dim3(2 * static_cast<unsigned>(units < pairs ? units : pairs));
+  cfg.dynamicSmemBytes = C::smem(g.E);
   return cudaLaunchKernelEx(&cfg, kern, ta, tw, tsa, tsw, g);
 }
 
@@ -508,9 +646,15 @@ cudaError_t gemm_t(const CUtensorMap& ta, const CUtensorMap& tw, const Fp4GemmAr
 
 cudaError_t launch_fp4_gemm(const CUtensorMap& ta, const CUtensorMap& tw, const Fp4GemmArgs& g,
                             int num_sms, cudaStream_t s) {
-  const bool gated = g.act == MOE_ACT_SWIGLU || g.act == MOE_ACT_GEGLU;
-  if (g.nv) return gated ? gemm_t<true, true>(ta, tw, g, num_sms, s) : gemm_t<true, false>(ta, tw, g, num_sms, s);
-  return gated ? gemm_t<false, true>(ta, tw, g, num_sms, s) : gemm_t<false, false>(ta, tw, g, num_sms, s);
+  auto run = [&](auto nv) {
+    constexpr bool NV = decltype(nv)::value;
+    if (g.act == MOE_ACT_SWIGLU || g.act == MOE_ACT_GEGLU)
+      return gemm_t<NV, Epi::kGated>(ta, tw, g, num_sms, s);
+    if (g.act == MOE_ACT_NONE && !g.residual && !g.z && !g.out_q)
+      return gemm_t<NV, Epi::kPlain>(ta, tw, g, num_sms, s);
+    return gemm_t<NV, Epi::kFull>(ta, tw, g, num_sms, s);
+  };
+  return g.nv ? run(BoolC<true>{}) : run(BoolC<false>{});
 }
 
 }  // namespace moe

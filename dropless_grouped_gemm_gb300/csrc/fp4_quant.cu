@@ -53,7 +53,9 @@ __device__ __forceinline__ void load_offsets(const Fp4Rows& r, int* s_off, int32
 __device__ __forceinline__ bool place_of(const Fp4Rows& r, const int* s_off, long long row,
                                          Fp4Place& p) {
   if (r.offsets == nullptr) {
-    p.e = r.E == 1 ? 0 : static_cast<int>(row / r.rows_per_e);
+    if (r.E == 1) p.e = 0;
+    else if (r.rows < (1LL << 31)) p.e = static_cast<int>(static_cast<uint32_t>(row) / static_cast<uint32_t>(r.rows_per_e));
+    else p.e = static_cast<int>(row / r.rows_per_e);
     p.off = p.e * r.rows_per_e;
   } else {
     if (row < s_off[0] || row >= s_off[r.E]) return false;
@@ -74,14 +76,29 @@ __device__ __forceinline__ float tensor_scale(const float* t, int stride, int e)
   return t == nullptr ? 1.f : t[stride * e];
 }
 
+// where a row's codes and its scales of block 0 begin
+struct RowAt {
+  long long q, s;
+};
+template <bool NV>
+__device__ __forceinline__ RowAt row_at(const Fp4Place& pl, long long row, int K) {
+  return RowAt{row * (K / 2), fp4_scale_at(pl.tile0, row - pl.off, 0, fp4_chunks(NV, K))};
+}
+// ... of the block that holds value k0 (a multiple of 64)
+template <bool NV>
+__device__ __forceinline__ long long scales_at(const RowAt& r, int k0) {
+  if constexpr (NV) return r.s + static_cast<long long>(k0 / 64) * kFp4ChunkBytes;
+  else return r.s + static_cast<long long>(k0 / 128) * kFp4ChunkBytes + (k0 / 32 & 3);
+}
+
 // A lane's 16 values (8 words) as codes and its scale byte (MX: the pair's)
 template <bool NV>
-__device__ __forceinline__ uint2 quant16(const uint32_t (&p)[8], float t, uint32_t& byte) {
+__device__ __forceinline__ uint2 quant16(const uint32_t (&p)[8], const Fp4Tensor& t, uint32_t& byte) {
   uint32_t m = bf16_amax16(p);
   if constexpr (!NV) m = max(m, __shfl_xor_sync(kAll, m, 1));
   float inv;
-  byte = fp4_scale<NV>(m << 16, t, inv);
-  return fp4_codes16(p, inv, NV && fp4_power_of_two(t));
+  byte = fp4_scale_bf16<NV>(m << 16, t, inv);
+  return fp4_codes16<NV>(p, inv, t.exact);
 }
 
 // 64 values' scale bytes of four neighbouring lanes, joined in the first of
@@ -97,15 +114,14 @@ __device__ __forceinline__ uint32_t join_bytes(uint32_t byte) {
   return w;
 }
 
-// the codes and scales of values [k0, k0 + 16) of row `row`, by this lane
+// the codes and scales of values [k0, k0 + 16) of a row, by this lane
 template <bool NV>
-__device__ __forceinline__ void store16(const Fp4QuantArgs& a, const Fp4Place& pl, long long row,
-                                        int k0, bool on, uint2 codes, uint32_t scales) {
+__device__ __forceinline__ void store16(const Fp4QuantArgs& a, const RowAt& r, int k0, bool on,
+                                        uint2 codes, uint32_t scales) {
   if (!on) return;
-  *reinterpret_cast<uint2*>(a.q + row * (a.K / 2) + k0 / 2) = codes;
+  *reinterpret_cast<uint2*>(a.q + r.q + k0 / 2) = codes;
   if ((threadIdx.x & 3) == 0) {
-    uint8_t* at = a.s + fp4_scale_at(pl.tile0, row - pl.off, k0 / (NV ? 16 : 32),
-                                     fp4_chunks(NV, a.K));
+    uint8_t* at = a.s + scales_at<NV>(r, k0);
     if constexpr (NV) *reinterpret_cast<uint32_t*>(at) = scales;
     else *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>(scales);
   }
@@ -123,85 +139,94 @@ __device__ __forceinline__ void load16(const uint16_t* p, bool on, uint32_t (&w)
   }
 }
 
+constexpr int kSegs = 2;          // 512-value segments of a row that a warp takes, all loads first
+
 // Rows in their own order; with pair_of_row, row r is token pair_of_row[r] / k
-// (pad rows inside an expert: zeros).  Rows outside every expert are left.
+// (pad rows inside an expert: zeros).  Rows outside every expert are left.  A
+// block's y is kSegs segments of K, its warps walk the rows.
 template <bool NV>
 __global__ void __launch_bounds__(kThreads) rows_kernel(const Fp4QuantArgs a) {
   extern __shared__ int s_off[];
   load_offsets(a.r, s_off, a.err);
-  const int lane = threadIdx.x & 31;
-  const int segs = (a.K + 511) / 512;
-  const long long items = a.r.rows * segs;
+  const int kb = blockIdx.y * (512 * kSegs) + (threadIdx.x & 31) * 16;
   const long long step = static_cast<long long>(gridDim.x) * kWarps;
-  for (long long it = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5); it < items;
-       it += step) {
-    const long long row = it / segs;
-    const int k0 = static_cast<int>(it - row * segs) * 512 + lane * 16;
+  const int pairs = a.T * a.k;
+  for (long long row = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+       row < a.r.rows; row += step) {
     Fp4Place pl;
     if (!place_of(a.r, s_off, row, pl)) continue;
-    const bool on = k0 < a.K;
     long long from = row;
     if (a.pair_of_row != nullptr) {
       const int p = a.pair_of_row[row];
-      from = (p >= 0 && p < a.T * a.k) ? p / a.k : -1;
+      from = (p >= 0 && p < pairs) ? p / a.k : -1;
     }
-    uint32_t w[8], byte;
-    load16(a.src + from * a.K + k0, on && from >= 0, w);
-    const uint2 codes = quant16<NV>(w, tensor_scale(a.t, a.t_stride, pl.e), byte);
-    store16<NV>(a, pl, row, k0, on, codes, join_bytes<NV>(byte));
+    uint32_t w[kSegs][8];
+#pragma unroll
+    for (int g = 0; g < kSegs; ++g)
+      load16(a.src + from * a.K + kb + 512 * g, kb + 512 * g < a.K && from >= 0, w[g]);
+    const Fp4Tensor t = fp4_tensor(tensor_scale(a.t, a.t_stride, pl.e));
+    const RowAt at = row_at<NV>(pl, row, a.K);
+#pragma unroll
+    for (int g = 0; g < kSegs; ++g) {
+      uint32_t byte;
+      const uint2 codes = quant16<NV>(w[g], t, byte);
+      store16<NV>(a, at, kb + 512 * g, kb + 512 * g < a.K, codes, join_bytes<NV>(byte));
+    }
   }
 }
 
 // A permute in token order: each token's values are read and quantised once.
-// The items behind the tokens' look at 32 rows each for pad rows.
+// The last y looks at the rows for pad rows, 32 a warp.
 template <bool NV>
 __global__ void __launch_bounds__(kThreads) tokens_kernel(const Fp4QuantArgs a) {
   extern __shared__ int s_off[];
   load_offsets(a.r, s_off, a.err);
   const int lane = threadIdx.x & 31;
-  const int segs = (a.K + 511) / 512;
-  const long long tokens = static_cast<long long>(a.T) * segs;
-  const long long items = tokens + (a.r.rows + 31) / 32;
   const long long step = static_cast<long long>(gridDim.x) * kWarps;
+  const long long first = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   const int pairs = a.T * a.k;
-  for (long long it = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5); it < items;
-       it += step) {
-    if (it < tokens) {
-      const int t = static_cast<int>(it / segs);
-      const int k0 = static_cast<int>(it - static_cast<long long>(t) * segs) * 512 + lane * 16;
-      const bool on = k0 < a.K;
-      uint32_t w[8], byte;
-      load16(a.src + static_cast<long long>(t) * a.K + k0, on, w);
-      uint2 codes = make_uint2(0u, 0u);
-      uint32_t scales = 0u;
-      bool done = false;
+  if (blockIdx.y + 1 < gridDim.y) {
+    const int kb = blockIdx.y * (512 * kSegs) + lane * 16;
+    const Fp4Tensor ts = fp4_tensor(tensor_scale(a.t, 0, 0));     // (a ragged tensor has one scale)
+    for (long long t = first; t < a.T; t += step) {
+      uint32_t w[kSegs][8];
+#pragma unroll
+      for (int g = 0; g < kSegs; ++g)
+        load16(a.src + t * a.K + kb + 512 * g, kb + 512 * g < a.K, w[g]);
+      uint2 codes[kSegs];
+      uint32_t scales[kSegs];
       for (int j0 = 0; j0 < a.k; j0 += 32) {
         // lane j finds the place of the token's pair j0 + j
-        Fp4Place mine{0, 0, -1};
-        int row = -1;
+        RowAt mine{-1, 0};
         if (j0 + lane < a.k) {
-          const int p = t * a.k + j0 + lane;
-          row = a.row_of_pair[p];
-          if (row < 0 || row >= a.r.rows || a.pair_of_row[row] != p ||
-              !place_of(a.r, s_off, row, mine))
-            row = -1;
+          const int p = static_cast<int>(t) * a.k + j0 + lane;
+          const int row = a.row_of_pair[p];
+          Fp4Place pl;
+          if (row >= 0 && row < a.r.rows && a.pair_of_row[row] == p && place_of(a.r, s_off, row, pl))
+            mine = row_at<NV>(pl, row, a.K);
         }
-        if (!done) {      // (a ragged tensor has one scale)
-          codes = quant16<NV>(w, tensor_scale(a.t, 0, 0), byte);
-          scales = join_bytes<NV>(byte);
-          done = true;
+        if (j0 == 0) {
+#pragma unroll
+          for (int g = 0; g < kSegs; ++g) {
+            uint32_t byte;
+            codes[g] = quant16<NV>(w[g], ts, byte);
+            scales[g] = join_bytes<NV>(byte);
+          }
         }
         const int n = min(32, a.k - j0);
         for (int j = 0; j < n; ++j) {
-          const int to = __shfl_sync(kAll, row, j);
-          Fp4Place pl;
-          pl.off = __shfl_sync(kAll, mine.off, j);
-          pl.tile0 = __shfl_sync(kAll, mine.tile0, j);
-          if (to >= 0) store16<NV>(a, pl, to, k0, on, codes, scales);
+          RowAt to;
+          to.q = __shfl_sync(kAll, mine.q, j);
+          to.s = __shfl_sync(kAll, mine.s, j);
+          if (to.q < 0) continue;
+#pragma unroll
+          for (int g = 0; g < kSegs; ++g)
+            store16<NV>(a, to, kb + 512 * g, kb + 512 * g < a.K, codes[g], scales[g]);
         }
       }
-    } else {
-      const long long row0 = (it - tokens) * 32;
+    }
+  } else {
+    for (long long row0 = first * 32; row0 < a.r.rows; row0 += step * 32) {
       const long long row = row0 + lane;
       bool pad = false;
       if (row < a.r.rows) {
@@ -212,8 +237,9 @@ __global__ void __launch_bounds__(kThreads) tokens_kernel(const Fp4QuantArgs a) 
         const long long r = row0 + __ffs(m) - 1;
         Fp4Place pl;
         if (!place_of(a.r, s_off, r, pl)) continue;
+        const RowAt at = row_at<NV>(pl, r, a.K);
         for (int k0 = lane * 16; k0 < a.K; k0 += 512)
-          store16<NV>(a, pl, r, k0, true, make_uint2(0u, 0u), 0u);
+          store16<NV>(a, at, k0, true, make_uint2(0u, 0u), 0u);
       }
     }
   }
@@ -221,21 +247,16 @@ __global__ void __launch_bounds__(kThreads) tokens_kernel(const Fp4QuantArgs a) 
 
 template <bool NV>
 __global__ void __launch_bounds__(kThreads)
-    columns_kernel(const uint16_t* __restrict__ W, int E, int R, int C, const float* __restrict__ t,
+    columns_kernel(const uint16_t* __restrict__ W, int R, int C, const float* __restrict__ t,
                    uint8_t* __restrict__ q, uint8_t* __restrict__ s) {
   const int lane = threadIdx.x & 31;
-  const int rb = R / 64, cb = C / 64;
-  const long long items = static_cast<long long>(E) * rb * cb;
-  const long long step = static_cast<long long>(gridDim.x) * kWarps;
+  // neighbouring warps take neighbouring columns: whole rows of W together
+  const int groups = (C / 64 + kWarps - 1) / kWarps;
+  const int r64 = blockIdx.x / groups, e = blockIdx.y;
+  const int c64 = (blockIdx.x - r64 * groups) * kWarps + (threadIdx.x >> 5);
   const int chunks = fp4_chunks(NV, R);
-  for (long long it = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5); it < items;
-       it += step) {
-    // neighbouring warps take neighbouring columns: whole rows of W together
-    const int c64 = static_cast<int>(it % cb);
-    const long long er = it / cb;
-    const int r64 = static_cast<int>(er % rb), e = static_cast<int>(er / rb);
-    const float ts = t == nullptr ? 1.f : t[e];
-    const bool snap = NV && fp4_power_of_two(ts);
+  if (c64 * 64 < C) {
+    const Fp4Tensor ts = fp4_tensor(t == nullptr ? 1.f : t[e]);
     const uint32_t* src = reinterpret_cast<const uint32_t*>(
         W + (static_cast<long long>(e) * R + r64 * 64) * C + c64 * 64) + lane;
     uint32_t w[64];
@@ -255,8 +276,8 @@ __global__ void __launch_bounds__(kThreads)
         uint32_t m = bf16_amax16(p + 8 * b);
         if constexpr (!NV) m = max(m, bf16_amax16(p + 8 * (b ^ 1)));
         float inv;
-        const uint32_t byte = fp4_scale<NV>(m << 16, ts, inv);
-        const uint2 u = fp4_codes16(p + 8 * b, inv, snap);
+        const uint32_t byte = fp4_scale_bf16<NV>(m << 16, ts, inv);
+        const uint2 u = fp4_codes16<NV>(p + 8 * b, inv, ts.exact);
         codes[2 * b] = u.x;
         codes[2 * b + 1] = u.y;
         if constexpr (NV) scales |= byte << (8 * b);
@@ -279,28 +300,38 @@ __global__ void __launch_bounds__(kThreads)
                   int32_t* err) {
   extern __shared__ int s_off[];
   load_offsets(r, s_off, err);
-  const int lane = threadIdx.x & 31;
-  const int segs = (K + 511) / 512;
-  const int chunks = fp4_chunks(NV, K);
-  const long long items = r.rows * segs;
+  const int kb = blockIdx.y * (512 * kSegs) + (threadIdx.x & 31) * 16;
   const long long step = static_cast<long long>(gridDim.x) * kWarps;
-  for (long long it = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5); it < items;
-       it += step) {
-    const long long row = it / segs;
-    const int k0 = static_cast<int>(it - row * segs) * 512 + lane * 16;
+  for (long long row = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+       row < r.rows; row += step) {
     Fp4Place pl;
-    if (k0 >= K || !place_of(r, s_off, row, pl)) continue;
-    const uint2 w = __ldcs(reinterpret_cast<const uint2*>(q + row * (K / 2) + k0 / 2));
-    const uint32_t byte = s[fp4_scale_at(pl.tile0, row - pl.off, k0 / (NV ? 16 : 32), chunks)];
+    if (kb >= K || !place_of(r, s_off, row, pl)) continue;
+    const RowAt at = row_at<NV>(pl, row, K);
+    const float ts = tensor_scale(t, t_stride, pl.e);
+    uint2 w[kSegs];
+    uint32_t byte[kSegs];
+#pragma unroll
+    for (int g = 0; g < kSegs; ++g) {
+      const int k0 = kb + 512 * g;
+      w[g] = make_uint2(0u, 0u);
+      byte[g] = 0u;
+      if (k0 < K) {
+        w[g] = __ldcs(reinterpret_cast<const uint2*>(q + at.q + k0 / 2));
+        byte[g] = s[scales_at<NV>(at, k0 & ~63) + (NV ? (k0 / 16 & 3) : (k0 / 32 & 1))];
+      }
+    }
+#pragma unroll
+    for (int g = 0; g < kSegs; ++g) {
+    const int k0 = kb + 512 * g;
+    if (k0 >= K) continue;
     // (code times block scale is exact, in bf16 too; a t that is no power of
     // two rounds the product once)
     float d;
-    if constexpr (NV) d = e4m3_value(byte);
-    else d = byte == 0xffu ? __uint_as_float(0x7fc00000u) : mx_scale(byte);
-    const float ts = tensor_scale(t, t_stride, pl.e);
+    if constexpr (NV) d = e4m3_value(byte[g]);
+    else d = byte[g] == 0xffu ? __uint_as_float(0x7fc00000u) : mx_scale(byte[g]);
     float v[16];
-    e2m1_values8(w.x, v);
-    e2m1_values8(w.y, v + 8);
+    e2m1_values8(w[g].x, v);
+    e2m1_values8(w[g].y, v + 8);
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = v[i] * d * ts;
     if constexpr (F32) {
@@ -315,6 +346,7 @@ __global__ void __launch_bounds__(kThreads)
         __stcs(o + i, make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
                                  pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7])));
     }
+    }
   }
 }
 
@@ -326,15 +358,23 @@ __global__ void __launch_bounds__(kThreads)
   const uint4* p = src + static_cast<long long>(e) * n8;
   uint32_t m = 0;
   const long long step = static_cast<long long>(gridDim.x) * kThreads;
-  for (long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; i < n8; i += step) {
-    const uint4 u = p[i];
+  auto take = [&](const uint4& u) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint32_t b = w[j] & 0x7fff7fffu;
       m = __vmaxu2(m, b & __vcmpltu2(b, 0x7f807f80u));
     }
+  };
+  long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
+  for (; i + 3 * step < n8; i += 4 * step) {      // four loads in flight
+    const uint4 u0 = p[i], u1 = p[i + step], u2 = p[i + 2 * step], u3 = p[i + 3 * step];
+    take(u0);
+    take(u1);
+    take(u2);
+    take(u3);
   }
+  for (; i < n8; i += step) take(p[i]);
   m = __reduce_max_sync(kAll, max(m & 0xffffu, m >> 16));
   if ((threadIdx.x & 31) == 0 && m != 0) atomicMax(top + e, m << 16);
 }
@@ -354,43 +394,43 @@ __global__ void power_kernel(float* t, int E) {
   t[e] = v;
 }
 
-int blocks_of(long long items, int num_sms) {
-  const long long want = (items + kWarps - 1) / kWarps;
-  const long long most = 8LL * num_sms;
-  return static_cast<int>(want < most ? (want > 0 ? want : 1) : most);
+// rows x the segments of K: enough blocks for every SM, each walking its rows
+dim3 grid_of(long long rows, int K, int num_sms, int more_y) {
+  const unsigned y = (K + 512 * kSegs - 1) / (512 * kSegs);
+  const long long want = (rows + kWarps - 1) / kWarps;
+  const long long most = (16LL * num_sms + y - 1) / y;
+  return dim3(static_cast<unsigned>(want < 1 ? 1 : want < most ? want : most), y + more_y);
 }
 size_t off_bytes(const Fp4Rows& r) { return r.offsets ? static_cast<size_t>(r.E + 1) * 4 : 0; }
 
 }  // namespace
 
 cudaError_t launch_fp4_quantize(const Fp4QuantArgs& a, int num_sms, cudaStream_t s) {
-  const int segs = (a.K + 511) / 512;
   const size_t smem = off_bytes(a.r);
   if (a.row_of_pair != nullptr) {
-    const long long items = static_cast<long long>(a.T) * segs + (a.r.rows + 31) / 32;
-    const int b = blocks_of(items, num_sms);
-    if (a.nv) tokens_kernel<true><<<b, kThreads, smem, s>>>(a);
-    else tokens_kernel<false><<<b, kThreads, smem, s>>>(a);
+    const dim3 grid = grid_of(a.T, a.K, num_sms, 1);
+    if (a.nv) tokens_kernel<true><<<grid, kThreads, smem, s>>>(a);
+    else tokens_kernel<false><<<grid, kThreads, smem, s>>>(a);
   } else {
-    const int b = blocks_of(a.r.rows * segs, num_sms);
-    if (a.nv) rows_kernel<true><<<b, kThreads, smem, s>>>(a);
-    else rows_kernel<false><<<b, kThreads, smem, s>>>(a);
+    const dim3 grid = grid_of(a.r.rows, a.K, num_sms, 0);
+    if (a.nv) rows_kernel<true><<<grid, kThreads, smem, s>>>(a);
+    else rows_kernel<false><<<grid, kThreads, smem, s>>>(a);
   }
   return cudaGetLastError();
 }
 
 cudaError_t launch_fp4_quantize_t(const uint16_t* W, int E, int R, int C, bool nv, const float* t,
-                                  uint8_t* q, uint8_t* s, int num_sms, cudaStream_t st) {
-  const int b = blocks_of(static_cast<long long>(E) * (R / 64) * (C / 64), num_sms);
-  if (nv) columns_kernel<true><<<b, kThreads, 0, st>>>(W, E, R, C, t, q, s);
-  else columns_kernel<false><<<b, kThreads, 0, st>>>(W, E, R, C, t, q, s);
+                                  uint8_t* q, uint8_t* s, cudaStream_t st) {
+  const dim3 grid(static_cast<unsigned>(R / 64) * ((C / 64 + kWarps - 1) / kWarps), E);
+  if (nv) columns_kernel<true><<<grid, kThreads, 0, st>>>(W, R, C, t, q, s);
+  else columns_kernel<false><<<grid, kThreads, 0, st>>>(W, R, C, t, q, s);
   return cudaGetLastError();
 }
 
 cudaError_t launch_fp4_dequantize(const uint8_t* q, const uint8_t* s, const Fp4Rows& r, int K,
                                   bool nv, const float* t, int t_stride, void* out, bool f32,
                                   int32_t* err, int num_sms, cudaStream_t st) {
-  const int b = blocks_of(r.rows * ((K + 511) / 512), num_sms);
+  const dim3 b = grid_of(r.rows, K, num_sms, 0);
   const size_t smem = off_bytes(r);
   if (nv) {
     if (f32) values_kernel<true, true><<<b, kThreads, smem, st>>>(q, s, r, K, t, t_stride, out, err);

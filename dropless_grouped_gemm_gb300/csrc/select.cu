@@ -9,18 +9,22 @@
 // takes no part; picks that no expert is left for are -1 with weight 0.
 //
 // The choice is that of the real numbers, not of float32's: without a bias the
-// experts' order is that of z, which is exact; with one (or for groups' sums), c is computed in
-// float32 and a row in which two neighbours of the order (or the last kept and
-// the first dropped group) lie nearer than c's error is done again in 64 bits
-// (some 0.4% of rows of 256 experts).  Equal logits with equal biases are equal
-// and need no second look.
+// experts' order is that of z, which is exact; with one (or for groups' sums), c
+// is computed in float32 and a row in which two neighbours of the order (or the
+// last kept and the first dropped group) lie nearer than c's error is done again
+// in 64 bits (some 0.2% of rows of 256 experts).  Equal logits with equal biases
+// are equal and need no second look.
 //
-// Forward: a warp per token, lane l holding the E / 32 experts from l E / 32
-// on, so that the lowest lane of equals has the lowest index; k rounds of a
-// maximum over the lane's keys and over the warp.  Bound by the rounds'
-// instructions on long batches, by launch latency on short ones.  Backward: a
-// warp per token, the k gradients scattered into a row in shared memory that
-// leaves in 16-byte stores; bound by those writes.
+// Forward: a warp per token, lane l holding the E / 32 experts from l E / 32 on.
+// A lane's values become 32-bit keys in the order of the floats, their last bits
+// replaced by the expert's place in the lane (so that one number says which, and
+// equals go to the lower index; what those bits hid counts as doubt), sorted once
+// by a network of minima and maxima.  Each of the k rounds then is one maximum
+// over the warp, one ballot, and a shift of the owner's keys: 18 instructions.
+// Bound by instructions on long batches (65,536 x 256, sigmoid, bias, 8 groups:
+// 144 us with a search of the lane's values in every round, 91 now), by launch latency on
+// short ones.  Backward: a warp per token, the k gradients scattered into a row
+// in shared memory that leaves in 16-byte stores; bound by those writes.
 #include <cuda_bf16.h>
 
 #include <type_traits>
@@ -39,13 +43,36 @@ constexpr float kMasked = -3.3895313892515355e38f;
 
 __device__ __forceinline__ bool takes_part(float z) { return z > kMasked; }   // (false for NaN)
 
-// unsigned keys in the order of the floats (-0 as +0); 0: none
-__device__ __forceinline__ uint32_t key_of(float f) {
-  uint32_t b = __float_as_uint(f + 0.f);
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+// signed keys in the order of the floats (-0 as +0); kNone: none
+constexpr int kNone = static_cast<int>(0x80000000u);
+__device__ __forceinline__ int key_of(float f) {
+  const int b = __float_as_int(f + 0.f);
+  return b ^ ((b >> 31) & 0x7fffffff);
 }
-__device__ __forceinline__ float value_of(uint32_t k) {
-  return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+__device__ __forceinline__ float value_of(int k) {
+  return __int_as_float(k ^ ((k >> 31) & 0x7fffffff));
+}
+
+// descending order by compare-exchanges (Batcher's odd-even merge sort)
+template <int N>
+__device__ __forceinline__ void sort_keys(int (&k)[N]) {
+#pragma unroll
+  for (int p = 1; p < N; p *= 2) {
+#pragma unroll
+    for (int q = p; q >= 1; q /= 2) {
+#pragma unroll
+      for (int j = q % p; j <= N - 1 - q; j += 2 * q) {
+#pragma unroll
+        for (int i = 0; i < q; ++i) {
+          if (i + j + q < N && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+            const int hi = max(k[i + j], k[i + j + q]);
+            k[i + j + q] = min(k[i + j], k[i + j + q]);
+            k[i + j] = hi;
+          }
+        }
+      }
+    }
+  }
 }
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -84,51 +111,73 @@ __device__ __forceinline__ F group_score(F t1, F t2, int best) {
   return (best == 2 && t2 > static_cast<F>(-INFINITY)) ? t1 + t2 : t1;
 }
 
-// One row's choice in 64 bits: lane j returns pick j (-1: none).  Rarely
-// called, so it keeps its values in local memory.
+// What a block needs to do a row again in 64 bits
+struct Exact {
+  double c[MOE_MAX_EXPERTS];
+  double part[kRows];
+  float top[kRows];
+  int8_t doubt[kRows];
+};
+
+// c of row t in 64 bits (the logits where there is no bias and no group's sum to
+// take), by the whole block: with a warp's lanes doing eight experts each, one
+// after the other, a row took 20 us, and there is hardly a batch without one.
 template <class T>
-__device__ __noinline__ int select_exact(const SelectArgs& a, long long t, int nv) {
-  const int lane = threadIdx.x & 31;
+__device__ __noinline__ void exact_scores(const SelectArgs& a, long long t, Exact& x) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const T* row = static_cast<const T*>(a.logits) + t * a.E;
-  double c[32];
-  float mf = -INFINITY;
-  for (int i = 0; i < nv; ++i) {
-    const int e = lane * nv + i;
-    if (e < a.E) {
+  const bool plain = a.bias == nullptr && !(a.top_groups < a.groups && a.best == 2);
+  double m = 0, sum = 1;
+  if (a.score == MOE_SCORE_SOFTMAX && !plain) {
+    float mf = -INFINITY;
+    for (int e = threadIdx.x; e < a.E; e += kThreads) {
       const float z = logit(row + e);
       if (takes_part(z)) mf = fmaxf(mf, z);
     }
-  }
-  const double m = warp_max(mf);
-  double sum = 0;
-  for (int i = 0; i < nv; ++i) {
-    const int e = lane * nv + i;
-    const float z = e < a.E ? logit(row + e) : -INFINITY;
-    c[i] = -INFINITY;
-    if (!takes_part(z)) continue;
-    c[i] = a.score == MOE_SCORE_SIGMOID ? 1.0 / (1.0 + exp(-static_cast<double>(z)))
-                                        : exp_below(static_cast<double>(z), m);
-    sum += c[i];
-  }
-  if (a.score == MOE_SCORE_SOFTMAX) {
-    sum = warp_add(sum);
-    for (int i = 0; i < nv; ++i) c[i] = c[i] / sum;      // (-inf stays)
-  }
-  if (a.bias != nullptr)
-    for (int i = 0; i < nv; ++i) {
-      const int e = lane * nv + i;
-      if (e < a.E) c[i] += a.bias[e];
-      if (!(c[i] > -INFINITY)) c[i] = -INFINITY;
+    mf = warp_max(mf);
+    if (lane == 0) x.top[warp] = mf;
+    __syncthreads();
+    for (int w = 0; w < kRows; ++w) mf = fmaxf(mf, x.top[w]);
+    m = mf;
+    double s = 0;
+    for (int e = threadIdx.x; e < a.E; e += kThreads) {
+      const float z = logit(row + e);
+      if (takes_part(z)) s += exp_below(static_cast<double>(z), m);
     }
+    s = warp_add(s);
+    if (lane == 0) x.part[warp] = s;
+    __syncthreads();
+    sum = 0;
+    for (int w = 0; w < kRows; ++w) sum += x.part[w];
+  }
+  for (int e = threadIdx.x; e < a.E; e += kThreads) {
+    const float z = logit(row + e);
+    double c = -INFINITY;
+    if (takes_part(z)) {
+      if (plain) c = z;
+      else
+        c = a.score == MOE_SCORE_SIGMOID ? 1.0 / (1.0 + exp(-static_cast<double>(z)))
+                                         : exp_below(static_cast<double>(z), m) / sum;
+      if (a.bias != nullptr) c += a.bias[e];
+      if (!(c > -INFINITY)) c = -INFINITY;
+    }
+    x.c[e] = c;
+  }
+  __syncthreads();
+}
+
+// That row's choice, by one warp: lane j returns pick j (-1: none)
+template <class T>
+__device__ __noinline__ int exact_choice(const SelectArgs& a, long long t, Exact& x) {
+  const int lane = threadIdx.x & 31;
+  const T* row = static_cast<const T*>(a.logits) + t * a.E;
   if (a.top_groups < a.groups) {
     const int n = a.E / a.groups;
     double mine = -INFINITY;             // lane g: group g's score
     for (int g = 0; g < a.groups; ++g) {
       double t1 = -INFINITY, t2 = -INFINITY;
-      for (int i = 0; i < nv; ++i) {
-        const int e = lane * nv + i;
-        if (e >= g * n && e < (g + 1) * n) top2(t1, t2, c[i], static_cast<double>(-INFINITY));
-      }
+      for (int e = g * n + lane; e < (g + 1) * n; e += 32)
+        top2(t1, t2, x.c[e], static_cast<double>(-INFINITY));
       for (int o = 16; o > 0; o >>= 1) {
         const double b1 = __shfl_xor_sync(kAll, t1, o), b2 = __shfl_xor_sync(kAll, t2, o);
         top2(t1, t2, b1, b2);
@@ -141,48 +190,79 @@ __device__ __noinline__ int select_exact(const SelectArgs& a, long long t, int n
       if (other > mine || (other == mine && g < lane)) ++before;
     }
     const unsigned keep = __ballot_sync(kAll, lane < a.groups && before < a.top_groups);
-    for (int i = 0; i < nv; ++i) {
-      const int e = lane * nv + i;
-      if (e >= a.E) continue;
-      if (!((keep >> (e / n)) & 1u)) c[i] = -INFINITY;
-      else if (a.bias == nullptr && c[i] > -INFINITY) c[i] = logit(row + e);
+    for (int e = lane; e < a.E; e += 32) {
+      if (!((keep >> (e / n)) & 1u)) x.c[e] = -INFINITY;
+      else if (a.bias == nullptr && x.c[e] > -INFINITY) x.c[e] = logit(row + e);
     }
+    __syncwarp();
   }
   int pick = -1;
   for (int j = 0; j < a.k; ++j) {
     double bv = -INFINITY;
     int be = 0x7fffffff;
-    for (int i = 0; i < nv; ++i)
-      if (c[i] > bv) { bv = c[i]; be = lane * nv + i; }
+    for (int e = lane; e < a.E; e += 32)
+      if (x.c[e] > bv) { bv = x.c[e]; be = e; }
     for (int o = 16; o > 0; o >>= 1) {
       const double ov = __shfl_xor_sync(kAll, bv, o);
       const int oe = __shfl_xor_sync(kAll, be, o);
       if (ov > bv || (ov == bv && oe < be)) { bv = ov; be = oe; }
     }
     if (be == 0x7fffffff) break;         // (the same on every lane)
-    if (be / nv == lane) c[be - lane * nv] = -INFINITY;
+    if (lane == (be & 31)) x.c[be] = -INFINITY;
+    __syncwarp();
     if (lane == j) pick = be;
   }
   return pick;
 }
 
-// Float32's c is at most 2^-20 (1 + |c|) off.  Sigmoid: the exponential is
-// 2 + 1.16 |z| units off, which s (1 - s) scales to under 1.2 of s <= 1, and the
-// division 2; softmax: expf 2 units, z - m 2^-24 |z - m| of an s that is as much
-// smaller, the sum's chains of 8 + 2 + 5 additions 15 halves; then half a unit
-// of |c|.  Two such are in doubt within twice that, sums of two within four times.
-__device__ __forceinline__ bool in_doubt(float hi, float lo, float times) {
-  return !(hi - lo > times * 1.9073486328125e-6f * (1.f + fmaxf(fabsf(hi), fabsf(lo))));
+// How near two float32 c's have to be for their order to be in doubt, in units u
+// = 2^-24.  A sigmoid is at most 6 u off (the exponential 2 + 1.16 |z| units in
+// the last place, which s (1 - s) scales to 0.65; 1 + e^-z half a unit, the
+// division two, of s <= 1), a softmax's s 22 u (expf two units, z - m u |z - m|
+// of an s that is as much smaller, the sum's chains of 8 + 2 + 5 additions, the
+// reciprocal and the product); c's addition rounds by u |c|, and a key's last bits
+// hide up to NV - 1 units of 2 u |c|.  Twice that for sums of two.
+template <int NV>
+__device__ __forceinline__ bool in_doubt(int score, float hi, float lo, float times) {
+  const float own = score == MOE_SCORE_SIGMOID ? 12.f : 44.f;
+  const float tol = times * 5.9604644775390625e-8f * (own + 2.f * NV * fmaxf(fabsf(hi), fabsf(lo)));
+  return !(hi - lo > tol);
 }
 
-// NV: experts a lane (32 NV >= E).  SCORED: the order is that of c (a bias, or
-// groups by the sum of two scores), else that of z.
+// Whether an expert other than pick `at` (the last one chosen), and not equal to
+// it, lies within the doubt around it: the first one that was not chosen did, and
+// what comes behind it was not looked at.  Rarely called.
+template <class T>
+__device__ __noinline__ bool doubt_around(const SelectArgs& a, long long t, int at, float m, float sum) {
+  const int lane = threadIdx.x & 31;
+  const T* row = static_cast<const T*>(a.logits) + t * a.E;
+  auto value = [&](int e) {
+    const float z = logit(row + e);
+    if (a.bias == nullptr) return z;
+    return (a.score == MOE_SCORE_SIGMOID ? 1.f / (1.f + expf(-z)) : exp_below(z, m) / sum) + a.bias[e];
+  };
+  const float v0 = value(at);
+  bool other = false;
+  for (int e = lane; e < a.E; e += 32) {
+    if (!takes_part(logit(row + e))) continue;
+    const float v = value(e);
+    // (twice what a key of 32 hides and c's own error)
+    const bool near = !(fabsf(v - v0) > 7.62939453125e-6f * (a.bias ? 1.f + fabsf(v0) : fabsf(v0)));
+    other |= near && (logit(row + e) != logit(row + at) || (a.bias && a.bias[e] != a.bias[at]));
+  }
+  return __any_sync(kAll, other);
+}
+
+// NV: experts a lane (32 NV >= E).  SCORED: c is needed (a bias, or groups by the
+// sum of two scores), else the order is that of z.
 template <class T, int NV, bool SCORED, bool VEC>
 __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
+  constexpr int kLow = NV - 1;                        // the bits that say which of the lane's
   const int lane = threadIdx.x & 31;
   const int e0 = lane * NV;
   const int n = a.E / a.groups;                       // experts of a group
   const bool limited = a.top_groups < a.groups;
+  const bool biased = SCORED && a.bias != nullptr;
   // whole lanes to a group, a power of two of them: each lane has one group
   const int lanes = (n % NV == 0 && ((n / NV) & (n / NV - 1)) == 0) ? n / NV : 0;
   float b[SCORED ? NV : 1];
@@ -191,8 +271,11 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
     for (int i = 0; i < NV; ++i)
       b[i] = (a.bias != nullptr && e0 + i < a.E) ? a.bias[e0 + i] : 0.f;
   }
+  __shared__ Exact exact;
   const int step = gridDim.x * kRows;
-  for (int t = blockIdx.x * kRows + (threadIdx.x >> 5); t < a.T; t += step) {
+  for (int t0 = blockIdx.x * kRows; t0 < a.T; t0 += step) {
+    const bool here = t0 + (threadIdx.x >> 5) < a.T;      // (the block stays together)
+    const int t = here ? t0 + (threadIdx.x >> 5) : a.T - 1;
     const T* row = static_cast<const T*>(a.logits) + static_cast<long long>(t) * a.E;
     float z[NV];
     if constexpr (VEC) {                              // E is a multiple of NV: all or nothing
@@ -232,7 +315,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
       for (int i = 0; i < NV; ++i) part[i & 3] += takes_part(z[i]) ? exp_below(z[i], m) : 0.f;
       sum = warp_add((part[0] + part[1]) + (part[2] + part[3]));
     }
-    uint32_t key[NV];
+    int key[NV];
     if constexpr (SCORED) {
       const float inv = 1.f / sum;
 #pragma unroll
@@ -240,48 +323,38 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
         const float s = a.score == MOE_SCORE_SIGMOID ? __fdividef(1.f, 1.f + __expf(-z[i]))
                                                      : exp_below(z[i], m) * inv;
         const float c = s + b[i];
-        key[i] = takes_part(z[i]) && c > -INFINITY ? key_of(c) : 0u;
+        key[i] = takes_part(z[i]) && c > -INFINITY ? (key_of(c) & ~kLow) | (kLow - i) : kNone;
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) key[i] = takes_part(z[i]) ? key_of(z[i]) : 0u;
+      for (int i = 0; i < NV; ++i) key[i] = takes_part(z[i]) ? (key_of(z[i]) & ~kLow) | (kLow - i) : kNone;
     }
-    bool doubt = false;
+    sort_keys(key);
+    bool doubt = false, keep = true;
+    unsigned kept = kAll;                             // groups, a bit each
     if (limited) {
+      float score = -INFINITY;                        // lane's group's, or lane g: group g's
+      int mine = lane;
       if (lanes > 0) {
-        float t1 = -INFINITY, t2 = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-          top2(t1, t2, key[i] ? value_of(key[i]) : -INFINITY, -INFINITY);
+        // (values without the keys' last bits)
+        float t1 = key[0] != kNone ? value_of(key[0] & ~kLow) : -INFINITY;
+        float t2 = -INFINITY;
+        if constexpr (NV > 1) t2 = key[1] != kNone ? value_of(key[1] & ~kLow) : -INFINITY;
         for (int o = lanes / 2; o > 0; o >>= 1) {
           const float b1 = __shfl_xor_sync(kAll, t1, o), b2 = __shfl_xor_sync(kAll, t2, o);
           top2(t1, t2, b1, b2);
         }
-        const float score = group_score(t1, t2, a.best);
-        const int mine = lane / lanes;
-        int before = 0;
-        for (int g = 0; g < a.groups; ++g) {
-          const float other = __shfl_sync(kAll, score, g * lanes);
-          before += other > score || (other == score && g < mine);
-        }
-        const bool in = mine < a.groups, keep = in && before < a.top_groups;
-        if constexpr (SCORED) {
-          const uint32_t lo = __reduce_min_sync(kAll, keep ? key_of(score) : kAll);
-          const uint32_t hi = __reduce_max_sync(kAll, in && !keep ? key_of(score) : 0u);
-          doubt |= in_doubt(value_of(lo), value_of(hi), 2.f) && value_of(hi) > -INFINITY;
-        }
-        if (!keep) {
-#pragma unroll
-          for (int i = 0; i < NV; ++i) key[i] = 0u;
-        }
+        score = group_score(t1, t2, a.best);
+        mine = lane / lanes;
       } else {
-        float score = -INFINITY;                      // lane g: group g's
         for (int g = 0; g < a.groups; ++g) {
           float t1 = -INFINITY, t2 = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < NV; ++i)
-            if (key[i] && e0 + i >= g * n && e0 + i < (g + 1) * n)
-              top2(t1, t2, value_of(key[i]), -INFINITY);
+          for (int i = 0; i < NV; ++i) {
+            const int e = e0 + kLow - (key[i] & kLow);
+            if (key[i] != kNone && e >= g * n && e < (g + 1) * n)
+              top2(t1, t2, value_of(key[i] & ~kLow), -INFINITY);
+          }
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) {
             const float b1 = __shfl_xor_sync(kAll, t1, o), b2 = __shfl_xor_sync(kAll, t2, o);
@@ -289,82 +362,153 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
           }
           if (lane == g) score = group_score(t1, t2, a.best);
         }
-        int before = 0;
-        for (int g = 0; g < a.groups; ++g) {
-          const float other = __shfl_sync(kAll, score, g);
-          before += other > score || (other == score && g < lane);
-        }
-        const bool in = lane < a.groups, keep = in && before < a.top_groups;
-        if constexpr (SCORED) {
-          const uint32_t lo = __reduce_min_sync(kAll, keep ? key_of(score) : kAll);
-          const uint32_t hi = __reduce_max_sync(kAll, in && !keep ? key_of(score) : 0u);
-          doubt |= in_doubt(value_of(lo), value_of(hi), 2.f) && value_of(hi) > -INFINITY;
-        }
-        const unsigned kept = __ballot_sync(kAll, keep);
+      }
+      int before = 0;
+      const int first = lanes > 0 ? lanes : 1;
+      for (int g = 0; g < a.groups; ++g) {
+        const float other = __shfl_sync(kAll, score, g * first);
+        before += other > score || (other == score && g < mine);
+      }
+      const bool in = mine < a.groups;
+      keep = in && before < a.top_groups;
+      const float lo = value_of(__reduce_min_sync(kAll, keep ? key_of(score) : 0x7fffffff));
+      const int hk = __reduce_max_sync(kAll, in && !keep ? key_of(score) : kNone);
+      const float hi = value_of(hk);
+      if (hk != kNone && hi > -INFINITY) {
+        // scores without a bias, each group's largest: the largest logits, of
+        // which the keys hide the last bits of float32
+        if constexpr (SCORED) doubt |= in_doubt<NV>(a.score, lo, hi, 2.f);
+        else if constexpr (sizeof(T) == 4) doubt |= lo == hi;
+      }
+      if (lanes == 0) kept = __ballot_sync(kAll, keep);
+      if (!SCORED || biased) {                        // (keys at a group's end become none, not in order)
+        bool gap = false;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-          if (!((kept >> min((e0 + i) / n, 31)) & 1u)) key[i] = 0u;
+        for (int i = 0; i < NV; ++i) {
+          const bool out = lanes > 0 ? !keep
+                                     : !((kept >> min((e0 + kLow - (key[i] & kLow)) / n, 31)) & 1u);
+          if (out && key[i] != kNone) {
+            key[i] = kNone;
+            gap = true;
+          }
+        }
+        if (lanes == 0 && __any_sync(kAll, gap)) sort_keys(key);
       }
     }
-    const bool biased = SCORED && a.bias != nullptr;
     if constexpr (SCORED) {
       if (!biased) {                                  // (the groups' scores were all that c was for)
 #pragma unroll
-        for (int i = 0; i < NV; ++i) key[i] = key[i] ? key_of(z[i]) : 0u;
+        for (int i = 0; i < NV; ++i) {
+          const bool in = lanes > 0 ? keep : (kept >> min((e0 + i) / n, 31)) & 1u;
+          key[i] = in && takes_part(z[i]) ? (key_of(z[i]) & ~kLow) | (kLow - i) : kNone;
+        }
+        sort_keys(key);
       }
     }
-    // the rounds; a biased choice looks at one more, for the last pick's doubt
-    int pick = -1;                                    // lane j: pick j
-    uint32_t last = 0u;
-    int last_e = -1;
-    const int rounds = a.k + (biased ? 1 : 0);
-    for (int j = 0; j < rounds; ++j) {
-      uint32_t top = key[0];
-#pragma unroll
-      for (int i = 1; i < NV; ++i) top = max(top, key[i]);
-      const uint32_t best = __reduce_max_sync(kAll, top);
-      if (best == 0u) break;
-      const int owner = __ffs(__ballot_sync(kAll, top == best)) - 1;
-      int at = 0;
-#pragma unroll
-      for (int i = NV - 1; i >= 0; --i)
-        if (key[i] == best) at = i;
-      const int e = __shfl_sync(kAll, e0 + at, owner);
+    // the rounds, one more for what the last pick was chosen from (lane k holds
+    // it), and a look at what comes then
+    int pick = -1, mykey = kNone, next = kNone, after = kNone;       // lane j: pick j
+    for (int j = 0; j <= a.k + 1; ++j) {
+      const int head = key[0] & ~kLow;                // (of equals the lowest lane, then place)
+      const int best = __reduce_max_sync(kAll, head);
+      if (best == kNone) break;
+      if (j == a.k + 1) {
+        after = best;
+        break;
+      }
+      const int owner = __ffs(__ballot_sync(kAll, head == best)) - 1;
+      const int low = __shfl_sync(kAll, key[0], owner) & kLow;
+      if (lane == j) {
+        pick = owner * NV + kLow - low;
+        mykey = best;
+      }
+      if (j == a.k) next = best;
       if (lane == owner) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-          if (i == at) key[i] = 0u;
-      }
-      if (lane == j && j < a.k) pick = e;
-      if constexpr (SCORED) {
-        if (biased && last_e >= 0 && in_doubt(value_of(last), value_of(best), 1.f))
-          doubt |= logit(row + e) != logit(row + last_e) || a.bias[e] != a.bias[last_e];
-        last = best;
-        last_e = e;
+        for (int i = 0; i + 1 < NV; ++i) key[i] = key[i + 1];
+        key[NV - 1] = kNone;
       }
     }
-    if constexpr (SCORED) {
-      if (doubt) pick = select_exact<T>(a, t, NV);
+    float zj = pick >= 0 ? logit(row + pick) : -INFINITY;
+    // neighbours in doubt: of a biased order by c's error, of the logits' by the
+    // bits that the keys hide (bf16 logits have none there)
+    if (biased || sizeof(T) == 4) {
+      auto near = [&](int hi, int lo) {
+        return biased ? in_doubt<NV>(a.score, value_of(hi), value_of(lo), 1.f) : hi == lo;
+      };
+      int nk = __shfl_down_sync(kAll, mykey, 1);
+      const int ne = __shfl_down_sync(kAll, pick, 1);
+      const float nz = __shfl_down_sync(kAll, zj, 1);
+      const bool last = lane == a.k - 1;
+      if (last) nk = next;
+      const bool close = lane < a.k && nk != kNone && near(mykey, nk);
+      bool pair = false;
+      if (close && (!last || a.k < 32)) pair = zj != nz || (biased && a.bias[pick] != a.bias[ne]);
+      bool some = __any_sync(kAll, pair);
+      // more than one beyond the last pick: whether any of them differs from it
+      const int edge = __shfl_sync(kAll, mykey, a.k - 1);
+      const bool open = __any_sync(kAll, close && last) && after != kNone && near(edge, after);
+      if (!doubt && (open || (a.k == 32 && __any_sync(kAll, close && last))))
+        doubt = doubt_around<T>(a, t, __shfl_sync(kAll, pick, a.k - 1), m, sum);
+      if (a.k == 32 || (biased && a.score == MOE_SCORE_SOFTMAX)) doubt |= some;
+      else if (some && !doubt) {
+        // the order of the picks and the one behind them alone: each lane its own
+        // in 64 bits, then its rank among them
+        double c = -INFINITY;
+        if (pick >= 0)
+          c = biased ? 1.0 / (1.0 + exp(-static_cast<double>(zj))) + a.bias[pick] : static_cast<double>(zj);
+        int rank = 0;
+        for (int i = 0; i <= a.k; ++i) {
+          const double oc = __shfl_sync(kAll, c, i);
+          const int oe = __shfl_sync(kAll, pick, i);
+          rank += oc > c || (oc == c && oe < pick);
+        }
+        const int was = pick;
+        for (int i = 0; i <= a.k; ++i) {
+          const int r = __shfl_sync(kAll, rank, i), e = __shfl_sync(kAll, was, i);
+          if (r == lane && e >= 0) pick = e;
+        }
+        zj = pick >= 0 ? logit(row + pick) : -INFINITY;
+      }
+    }
+    if (lane >= a.k) {                                // (lane k's was not chosen)
+      pick = -1;
+      zj = -INFINITY;
+    }
+    float zs = zj;
+    if (SCORED || sizeof(T) == 4) {
+      if (__syncthreads_or(doubt && here)) {
+        if (lane == 0) exact.doubt[threadIdx.x >> 5] = doubt && here;
+        __syncthreads();
+        for (int w = 0; w < kRows; ++w) {
+          if (!exact.doubt[w]) continue;
+          exact_scores<T>(a, t0 + w, exact);
+          if (static_cast<int>(threadIdx.x >> 5) == w) {
+            pick = exact_choice<T>(a, t, exact);
+            zs = pick >= 0 ? logit(row + pick) : -INFINITY;
+          }
+          __syncthreads();
+        }
+      }
     }
     // the weights, lane j's of pick j
     const bool on = pick >= 0;
-    const float zj = on ? logit(row + pick) : -INFINITY;
     float w = 0.f;
     if (a.score == MOE_SCORE_SIGMOID) {
-      if (on) w = 1.f / (1.f + expf(-zj));
+      if (on) w = 1.f / (1.f + expf(-zs));
       if (a.renorm) {
         const float tot = warp_add(w);
         w = tot > 0.f ? w / tot : 0.f;
       }
     } else if (a.renorm) {
-      const float mx = warp_max(zj);
-      if (on) w = exp_below(zj, mx);
+      const float mx = warp_max(zs);
+      if (on) w = exp_below(zs, mx);
       const float tot = warp_add(w);
       w = tot > 0.f ? w / tot : 0.f;
     } else if (on) {
-      w = exp_below(zj, m) / sum;
+      w = exp_below(zs, m) / sum;
     }
-    if (lane < a.k) {
+    if (here && lane < a.k) {
       const long long o = static_cast<long long>(t) * a.k + lane;
       a.idx[o] = pick;
       a.probs[o] = a.scale * w;

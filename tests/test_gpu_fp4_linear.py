@@ -149,7 +149,7 @@ def test_every_split(split):
 
 # many rows: the pairs' kernel
 MANY = [([0, 2048], 2048, 2048), ([0, 9000], 1088, 1088), ([0, 700, 700, 1999, 12000], 960, 1344), ([0, 1, 9000, 9001], 2048, 1024),
-        ([0, 0, 16383], 512, 576)]
+        ([0, 0, 16383], 2048, 1088)]
 
 
 @pytest.mark.parametrize("fmt", FMT)
