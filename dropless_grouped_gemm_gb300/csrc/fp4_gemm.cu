@@ -89,7 +89,9 @@ enum class Epi { kPlain, kFull, kGated };
 
 // A warp's 32 rows of a tile, from the warp's first column on
 struct GRows {
-  const uint16_t* bias;     // the expert's, or NULL
+  bool biased;
+  uint32_t bias;            // columns 2 lane and 2 lane + 1: one register, where each thread's own
+                            // loads of all 64 took 32 (and spilled others)
   const uint16_t* residual; // this thread's row
   uint8_t* box;             // the warp's 2 KB of shared memory; NULL: none
   int rows;                 // valid ones
@@ -100,14 +102,14 @@ struct GRows {
 // `pitch` bytes apart.  Through the box, so that four lanes write one row's 64
 // bytes: half as many requests and whole sectors (8191 x 1024 x 4096 bf16 53 us
 // without, 42 with; 8192 x 1024 x 4864 float32 76 us, 58).
-__device__ __forceinline__ void store_rows(const GRows& p, uint8_t* dst, long long pitch,
+__device__ __forceinline__ void store_rows(const GRows& p, uint8_t* dst, uint32_t pitch,
                                            const uint32_t (&w)[16]) {
-  const int lane = threadIdx.x & 31;
+  const uint32_t lane = threadIdx.x & 31;
   if (p.box == nullptr) {
     if (p.on) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<uint4*>(dst + lane * pitch + 16 * j) =
+        *reinterpret_cast<uint4*>(dst + static_cast<uint64_t>(lane) * pitch + 16 * j) =
             make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
     }
     return;
@@ -118,12 +120,13 @@ __device__ __forceinline__ void store_rows(const GRows& p, uint8_t* dst, long lo
     *reinterpret_cast<uint4*>(p.box + lane * 64 + ((j ^ ((lane >> 1) & 3)) * 16)) =
         make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
   __syncwarp();
-  const int j = lane & 3;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 8 * i + (lane >> 2);
+  const uint32_t j = lane & 3;
+#pragma unroll 2
+  for (uint32_t i = 0; i < 4; ++i) {
+    const uint32_t r = 8 * i + (lane >> 2);
     const uint4 v = *reinterpret_cast<const uint4*>(p.box + r * 64 + ((j ^ ((r >> 1) & 3)) * 16));
-    if (r < p.rows) *reinterpret_cast<uint4*>(dst + r * pitch + 16 * j) = v;
+    if (static_cast<int>(r) < p.rows)
+      *reinterpret_cast<uint4*>(dst + static_cast<uint64_t>(r) * pitch + 16 * j) = v;
   }
   __syncwarp();
 }
@@ -133,13 +136,12 @@ __device__ __forceinline__ void gemm_z8(const GRows& p, float alpha, int i, cons
                                         float (&z)[8]) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) z[j] = __uint_as_float(acc[j]) * alpha;
-  if (p.bias) {
-    const uint4 b = __ldg(reinterpret_cast<const uint4*>(p.bias + i));
-    const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
+  if (p.biased) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      z[2 * j] += bf16_lo(bw[j]);
-      z[2 * j + 1] += bf16_hi(bw[j]);
+      const uint32_t b = __shfl_sync(0xffffffffu, p.bias, i / 2 + j);
+      z[2 * j] += bf16_lo(b);
+      z[2 * j + 1] += bf16_hi(b);
     }
   }
 }
@@ -154,12 +156,17 @@ __device__ __forceinline__ void gemm_z32(const GRows& p, float alpha, int i, con
     for (int m = 0; m < 4; ++m) w[4 * j + m] = pack_bf16x2(z[2 * m], z[2 * m + 1]);
   }
 }
-// the outputs of 8 accumulator columns: 8, or 4 when gated
+// the outputs of 8 accumulator columns: 8, or 4 when gated; and, where wanted,
+// the pre-activations in bf16
 template <bool GATED>
 __device__ __forceinline__ void gemm_out8(const GRows& p, int act, float alpha, int i,
-                                          const uint32_t* acc, float* v) {
+                                          const uint32_t* acc, float* v, bool keep, uint32_t* zw) {
   float z[8];
   gemm_z8(p, alpha, i, acc, z);
+  if (keep) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) zw[j] = pack_bf16x2(z[2 * j], z[2 * j + 1]);
+  }
   if constexpr (GATED) {
     float u[4];
     linear_glu(act, z, u);
@@ -359,60 +366,75 @@ __global__ void __launch_bounds__(GT, 1)
       const float alpha = fp4_alpha(g, t.e);
       const int col0 = t.n0 + wg * GCOLS;
       const bool mine = col0 < g.N && q * 32 < t.rows;
-      // the warp's first row, this thread's row, and where their outputs begin
-      const long long row0 = static_cast<long long>(t.row0) + q * 32;
-      const long long row = row0 + lane;
       const int ocol = GATED ? col0 / 2 : col0;
       GRows p;
-      p.bias = g.bias ? g.bias + static_cast<long long>(t.e) * g.N + col0 : nullptr;
-      p.residual = g.residual ? g.residual + row * g.ldo + ocol : nullptr;
-      p.box = C::boxes(g.E) ? boxes + (warp - 2) * BOX_BYTES : nullptr;
-      p.rows = min(32, t.rows - q * 32);
-      p.on = r < t.rows;
-      const bool on = p.on;
-      uint8_t* out = g.out ? reinterpret_cast<uint8_t*>(g.out + row0 * g.ldo + ocol)
-                           : reinterpret_cast<uint8_t*>(g.out_f32 + row0 * g.ldo + ocol);
-      const long long pitch = static_cast<long long>(g.ldo) * (g.out ? 2 : 4);
-      uint8_t* zp = g.z ? reinterpret_cast<uint8_t*>(g.z + row0 * g.N + col0) : nullptr;
-      if (p.bias && mine) asm volatile("prefetch.global.L1 [%0];" ::"l"(p.bias));
+      p.biased = g.bias != nullptr;
+      p.bias = 0u;
+      if (p.biased && mine)
+        p.bias = *reinterpret_cast<const uint32_t*>(g.bias + static_cast<long long>(t.e) * g.N + col0 + 2 * lane);
       if (lane == 0) ok = mbar_wait(tfull_bar, local & 1, abort_flag);
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) break;
       tc_fence_after();
-      uint32_t v[2][32];
-      if (mine) {
-        const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + wg * GCOLS;
-        tmem_ld32(tb, v[0]);
-        tmem_ld32(tb + 32, v[1]);
-        tmem_wait_ld();
+      const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + wg * GCOLS;
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (rank != 0) mbar_arrive_cluster(tempty0);
+          else mbar_arrive(tempty_bar);
+        }
+      };
+      if (!mine) {
+        release();
+        continue;
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (rank != 0) mbar_arrive_cluster(tempty0);
-        else mbar_arrive(tempty_bar);
-      }
-      if (!mine) continue;
+      p.box = C::boxes(g.E) ? boxes + (warp - 2) * BOX_BYTES : nullptr;
+      p.rows = min(32, t.rows - q * 32);
+      p.on = r < t.rows;
+      const long long row0 = static_cast<long long>(t.row0) + q * 32;     // the warp's first row
       if constexpr (EPI == Epi::kPlain) {
-        if (g.out) {
+        if (g.out) {      // packed at once: half the registers, and none spilled
+          uint32_t w[2][16];
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            uint32_t w[16];
-            gemm_z32(p, alpha, 32 * c, v[c], w);
-            store_rows(p, out + 64 * c, pitch, w);
+            uint32_t v[32];
+            tmem_ld32(tb + 32 * c, v);
+            tmem_wait_ld();
+            gemm_z32(p, alpha, 32 * c, v, w[c]);
           }
-        } else {
+          release();
+          uint8_t* out = reinterpret_cast<uint8_t*>(g.out + row0 * g.ldo + ocol);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < 2; ++c) store_rows(p, out + 64 * c, 2 * g.ldo, w[c]);
+          continue;
+        }
+      }
+      const long long row = row0 + lane;
+      const bool on = p.on;
+      const long long at = row0 * g.ldo + ocol;
+      p.residual = g.residual ? g.residual + at + static_cast<long long>(lane) * g.ldo : nullptr;
+      uint8_t* out = g.out ? reinterpret_cast<uint8_t*>(g.out + at) : reinterpret_cast<uint8_t*>(g.out_f32 + at);
+      const uint32_t pitch = g.ldo * (g.out ? 2 : 4);
+      uint8_t* zp = g.z ? reinterpret_cast<uint8_t*>(g.z + row0 * g.N + col0) : nullptr;
+      if constexpr (EPI == Epi::kPlain) {     // float32
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          uint32_t v[32];
+          tmem_ld32(tb + 32 * c, v);
+          tmem_wait_ld();
+          if (c == 1) release();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
             uint32_t w[16];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               float z[8];
-              gemm_z8(p, alpha, 16 * c + 8 * j, v[c / 2] + 16 * (c % 2) + 8 * j, z);
+              gemm_z8(p, alpha, 32 * c + 16 * h + 8 * j, v + 16 * h + 8 * j, z);
 #pragma unroll
               for (int i = 0; i < 8; ++i) w[8 * j + i] = __float_as_uint(z[i]);
             }
-            store_rows(p, out + 64 * c, pitch, w);
+            store_rows(p, out + 128 * c + 64 * h, pitch, w);
           }
         }
         continue;
@@ -422,20 +444,23 @@ __global__ void __launch_bounds__(GT, 1)
       uint32_t bytes = 0;
       float held[GATED && !NV ? 16 : 1];
       uint32_t half[GATED ? 8 : 1];
-      // one body for both halves keeps the code small
+      // 32 columns at a time from TMEM, which is released with the second load:
+      // both at once spill registers (8192 x 1024 x 4864, geglu with z: 68 us, 52
+      // so; where K is long it costs a little, 32,768 x 8,192 x 4,096 400 us, 412 so)
 #pragma unroll 1
       for (int c = 0; c < 2; ++c) {
         const int col = col0 + 32 * c;
-        if (zp) {
-          uint32_t w[16];
-          gemm_z32(p, alpha, 32 * c, v[0], w);
-          store_rows(p, zp + 64 * c, static_cast<long long>(g.N) * 2, w);
-        }
+        uint32_t v[32];
+        tmem_ld32(tb + 32 * c, v);
+        tmem_wait_ld();
+        if (c == 1) release();
+        uint32_t zw[16];
         if constexpr (GATED) {
           float o[16];
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            gemm_out8<true>(p, g.act, alpha, 32 * c + 8 * j, v[0] + 8 * j, o + 4 * j);
+            gemm_out8<true>(p, g.act, alpha, 32 * c + 8 * j, v + 8 * j, o + 4 * j, zp != nullptr, zw + 4 * j);
+          if (zp) store_rows(p, zp + 64 * c, 2 * g.N, zw);
           if (g.out) {
             if (c == 0) {
 #pragma unroll
@@ -490,7 +515,8 @@ __global__ void __launch_bounds__(GT, 1)
           float o[32];
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            gemm_out8<false>(p, g.act, alpha, 32 * c + 8 * j, v[0] + 8 * j, o + 8 * j);
+            gemm_out8<false>(p, g.act, alpha, 32 * c + 8 * j, v + 8 * j, o + 8 * j, zp != nullptr, zw + 4 * j);
+          if (zp) store_rows(p, zp + 64 * c, 2 * g.N, zw);
           if (g.out) {
             uint32_t w[16];
 #pragma unroll
@@ -529,8 +555,6 @@ __global__ void __launch_bounds__(GT, 1)
             }
           }
         }
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[0][i] = v[1][i];
       }
     }
     gave_up(ok);
