@@ -47,7 +47,7 @@ CASES = [(1, 1, 1), (3, 2, 2), (7, 8, 3), (33, 31, 5), (16, 60, 4), (19, 64, 6),
 
 @pytest.mark.parametrize("T,E,k", CASES)
 @pytest.mark.parametrize("dt", [F32, BF])
-@pytest.mark.parametrize("score,biased,renorm", itertools.product(["softmax", "sigmoid"], [False, True], [False, True]))
+@pytest.mark.parametrize("score,biased,renorm", list(itertools.product(["softmax", "sigmoid"], [False, True], [False, True])))
 def test_select(T, E, k, dt, score, biased, renorm):
     bias = 0.1 * torch.randn(E, generator=torch.Generator().manual_seed(7)) if biased else None
     _check(_logits(T, E, dt, T * E + k), k, bias, score=score, renorm=renorm, scale=2.5)
@@ -56,7 +56,7 @@ def test_select(T, E, k, dt, score, biased, renorm):
 @pytest.mark.parametrize("E,groups,top,k", [(8, 2, 1, 3), (64, 8, 4, 6), (256, 8, 4, 8), (60, 6, 2, 5), (96, 3, 2, 8),
                                             (1024, 32, 5, 16), (30, 30, 7, 7), (512, 4, 3, 8), (33, 11, 4, 9)])
 @pytest.mark.parametrize("best", [1, 2])
-@pytest.mark.parametrize("score,biased", itertools.product(["softmax", "sigmoid"], [False, True]))
+@pytest.mark.parametrize("score,biased", list(itertools.product(["softmax", "sigmoid"], [False, True])))
 def test_groups(E, groups, top, k, best, score, biased):
     if best > E // groups:
         pytest.skip("a group of one expert")
@@ -122,7 +122,7 @@ def test_masks_infinities_and_nan(score, biased, renorm):
 
 @pytest.mark.parametrize("T,E,k", [(1, 1, 1), (5, 3, 2), (33, 60, 4), (17, 64, 8), (40, 256, 8), (3, 1001, 32), (6, 1024, 10)])
 @pytest.mark.parametrize("dt,ot", [(F32, F32), (F32, BF), (BF, BF), (BF, F32)])
-@pytest.mark.parametrize("score,renorm", itertools.product(["softmax", "sigmoid"], [False, True]))
+@pytest.mark.parametrize("score,renorm", list(itertools.product(["softmax", "sigmoid"], [False, True])))
 def test_gradient(T, E, k, dt, ot, score, renorm):
     z = _logits(T, E, dt, T + E)
     dw = torch.randn((T, k), generator=torch.Generator().manual_seed(2))
