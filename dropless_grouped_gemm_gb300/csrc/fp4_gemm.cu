@@ -60,6 +60,15 @@ struct GC {
       smem(MOE_MAX_EXPERTS) > smem(box_experts) ? smem(MOE_MAX_EXPERTS) : smem(box_experts);
 };
 
+// an arrival on a barrier of the cluster that orders no memory: the accumulator
+// has been read when tcgen05.wait::ld returns, and nothing else is handed over.
+// (With release semantics it waits for the warp's stores of the tile before: 1000
+// to 2000 cycles.)
+__device__ __forceinline__ void mbar_arrive_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
+}
+
 struct GTile {
   int e, row0, rows, n0;    // first row of this CTA's block, its valid rows, first column
   long long tile;           // its scale tile
@@ -255,9 +264,11 @@ __global__ void __launch_bounds__(GT, 1)
   const uint32_t tmem_base = *tmem_slot;
   const int units = s_ts[g.E];
   // a role that gives up takes the other CTA with it
+  auto tell_other = [&]() {
+    st_cluster_u32(mapa_shared(smem_u32(const_cast<int*>(abort_flag)), rank ^ 1), 1u);
+  };
   auto gave_up = [&](bool ok) {
-    if (!ok && elect_one())
-      st_cluster_u32(mapa_shared(smem_u32(const_cast<int*>(abort_flag)), rank ^ 1), 1u);
+    if (!ok && elect_one()) tell_other();
   };
 
   if (warp == 0) {
@@ -299,8 +310,9 @@ __global__ void __launch_bounds__(GT, 1)
     }
     gave_up(ok);
   } else if (warp == 1) {
-    // MMA issuer: the first CTA's warp, for both
-    if (rank == 0) {
+    // MMA issuer: one thread of the first CTA, for both (no other thread of the
+    // warp to agree with between the stages)
+    if (rank == 0 && elect_one()) {
       int stage = 0, local = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -308,14 +320,14 @@ __global__ void __launch_bounds__(GT, 1)
       const uint32_t w_lo0 = sdesc_lo(smem_u32(smem) + OP_BYTES, 16);
       const uint32_t sf0 = smem_u32(sf_region);
       for (int u = unit0; u < units && ok; u += unit_step, ++local) {
-        ok = __all_sync(0xffffffffu, mbar_wait_cluster(tempty_bar, (local & 1) ^ 1, abort_flag));
+        ok = mbar_wait_cluster(tempty_bar, (local & 1) ^ 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
         for (int kb = 0; kb < kblocks; ++kb) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&full_bar[stage], phase, abort_flag));
+          ok = mbar_wait(&full_bar[stage], phase, abort_flag);
           if (!ok) break;
           tc_fence_after();
-          if (elect_one()) {
+          {
             const uint32_t ss = sf0 + stage * C::sf_bytes;
             const uint32_t ta = tmem_base + SF_TMEM + stage * C::sf_cols;
             const uint32_t tw = ta + SF::cols;
@@ -343,14 +355,13 @@ __global__ void __launch_bounds__(GT, 1)
             }
             umma_commit_pair_mc(&empty_bar[stage]);
           }
-          __syncwarp();
           if (++stage == STAGES) { stage = 0; phase ^= 1; }
         }
-        if (ok && elect_one()) umma_commit_pair_mc(tfull_bar);
-        __syncwarp();
+        if (ok) umma_commit_pair_mc(tfull_bar);
       }
-      gave_up(ok);
+      if (!ok) tell_other();
     }
+    __syncwarp();
   } else {
     // epilogue: warpgroup wg takes 64 of the tile's columns, warp q of it 32
     // rows, a thread one row
@@ -381,7 +392,7 @@ __global__ void __launch_bounds__(GT, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          if (rank != 0) mbar_arrive_cluster(tempty0);
+          if (rank != 0) mbar_arrive_relaxed(tempty0);
           else mbar_arrive(tempty_bar);
         }
       };
