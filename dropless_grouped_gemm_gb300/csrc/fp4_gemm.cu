@@ -108,11 +108,13 @@ struct GRows {
 };
 
 // 64 bytes of each row (w: this thread's) to `dst` (the first row's), rows
-// `pitch` bytes apart.  Through the box, so that four lanes write one row's 64
-// bytes: half as many requests and whole sectors (8191 x 1024 x 4096 bf16 53 us
-// without, 42 with; 8192 x 1024 x 4864 float32 76 us, 58).
-__device__ __forceinline__ void store_rows(const GRows& p, uint8_t* dst, uint32_t pitch,
-                                           const uint32_t (&w)[16]) {
+// `pitch` bytes apart: row y and column x of `map`.  Through the box and a TMA
+// store, which runs on while the warp goes on: stores from registers hold a warp
+// until L2 has taken them, some 2500 cycles where all SMs end a tile at once.
+// 16-byte piece j of row r lies at place j ^ (r / 2 % 4): the 64-byte swizzle.  A
+// block that ends early goes row by row.
+__device__ __forceinline__ void store_rows(const GRows& p, const CUtensorMap* map, int x, int y,
+                                           uint8_t* dst, uint32_t pitch, const uint32_t (&w)[16]) {
   const uint32_t lane = threadIdx.x & 31;
   if (p.box == nullptr) {
     if (p.on) {
@@ -123,21 +125,26 @@ __device__ __forceinline__ void store_rows(const GRows& p, uint8_t* dst, uint32_
     }
     return;
   }
-  // 16-byte piece j of row r at place j ^ (r / 2 % 4): free of bank conflicts both ways
+  if (lane == 0) bulk_wait_read_0();      // the box's store before has read it
+  __syncwarp();
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     *reinterpret_cast<uint4*>(p.box + lane * 64 + ((j ^ ((lane >> 1) & 3)) * 16)) =
         make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+  fence_proxy_async_smem();
   __syncwarp();
-  const uint32_t j = lane & 3;
-#pragma unroll 2
-  for (uint32_t i = 0; i < 4; ++i) {
-    const uint32_t r = 8 * i + (lane >> 2);
-    const uint4 v = *reinterpret_cast<const uint4*>(p.box + r * 64 + ((j ^ ((r >> 1) & 3)) * 16));
-    if (static_cast<int>(r) < p.rows)
-      *reinterpret_cast<uint4*>(dst + static_cast<uint64_t>(r) * pitch + 16 * j) = v;
+  if (p.rows == 32) {
+    if (lane == 0) {
+      tma_store_2d(map, p.box, x, y);
+      bulk_commit();
+    }
+    return;
   }
-  __syncwarp();
+  const uint32_t j = lane & 3;
+#pragma unroll 1
+  for (uint32_t r = lane >> 2; static_cast<int>(r) < p.rows; r += 8)
+    *reinterpret_cast<uint4*>(dst + static_cast<uint64_t>(r) * pitch + 16 * j) =
+        *reinterpret_cast<const uint4*>(p.box + r * 64 + ((j ^ ((r >> 1) & 3)) * 16));
 }
 
 // 8 pre-activations, the i-th of the warp's columns on
@@ -209,7 +216,9 @@ template <bool NV, Epi EPI>
 __global__ void __launch_bounds__(GT, 1)
     fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW,
                     const __grid_constant__ CUtensorMap tmSA,
-                    const __grid_constant__ CUtensorMap tmSW, const Fp4GemmArgs g) {
+                    const __grid_constant__ CUtensorMap tmSW,
+                    const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmZ,
+                    const Fp4GemmArgs g) {
   using C = GC<NV>;
   using SF = Fp4Sf<NV>;
   constexpr bool GATED = EPI == Epi::kGated;
@@ -403,7 +412,8 @@ __global__ void __launch_bounds__(GT, 1)
       p.box = C::boxes(g.E) ? boxes + (warp - 2) * BOX_BYTES : nullptr;
       p.rows = min(32, t.rows - q * 32);
       p.on = r < t.rows;
-      const long long row0 = static_cast<long long>(t.row0) + q * 32;     // the warp's first row
+      const int y = t.row0 + q * 32;                  // the warp's first row
+      const long long row0 = y;
       if constexpr (EPI == Epi::kPlain) {
         if (g.out) {      // packed at once: half the registers, and none spilled
           uint32_t w[2][16];
@@ -417,7 +427,7 @@ __global__ void __launch_bounds__(GT, 1)
           release();
           uint8_t* out = reinterpret_cast<uint8_t*>(g.out + row0 * g.ldo + ocol);
 #pragma unroll
-          for (int c = 0; c < 2; ++c) store_rows(p, out + 64 * c, 2 * g.ldo, w[c]);
+          for (int c = 0; c < 2; ++c) store_rows(p, &tmO, ocol + 32 * c, y, out + 64 * c, 2 * g.ldo, w[c]);
           continue;
         }
       }
@@ -445,7 +455,7 @@ __global__ void __launch_bounds__(GT, 1)
 #pragma unroll
               for (int i = 0; i < 8; ++i) w[8 * j + i] = __float_as_uint(z[i]);
             }
-            store_rows(p, out + 128 * c + 64 * h, pitch, w);
+            store_rows(p, &tmO, ocol + 32 * c + 16 * h, y, out + 128 * c + 64 * h, pitch, w);
           }
         }
         continue;
@@ -471,7 +481,7 @@ __global__ void __launch_bounds__(GT, 1)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             gemm_out8<true>(p, g.act, alpha, 32 * c + 8 * j, v + 8 * j, o + 4 * j, zp != nullptr, zw + 4 * j);
-          if (zp) store_rows(p, zp + 64 * c, 2 * g.N, zw);
+          if (zp) store_rows(p, &tmZ, col, y, zp + 64 * c, 2 * g.N, zw);
           if (g.out) {
             if (c == 0) {
 #pragma unroll
@@ -483,13 +493,13 @@ __global__ void __launch_bounds__(GT, 1)
                 w[i] = half[i];
                 w[8 + i] = pack_bf16x2(o[2 * i], o[2 * i + 1]);
               }
-              store_rows(p, out, pitch, w);
+              store_rows(p, &tmO, ocol, y, out, pitch, w);
             }
           } else if (g.out_f32) {
             uint32_t w[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i]);
-            store_rows(p, out + 64 * c, pitch, w);
+            store_rows(p, &tmO, ocol + 16 * c, y, out + 64 * c, pitch, w);
           } else {                      // 16 outputs from oc on
             const int oc = col / 2;
             uint8_t* q8 = g.out_q + row * (g.ldo / 2) + oc / 2;
@@ -527,19 +537,19 @@ __global__ void __launch_bounds__(GT, 1)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             gemm_out8<false>(p, g.act, alpha, 32 * c + 8 * j, v + 8 * j, o + 8 * j, zp != nullptr, zw + 4 * j);
-          if (zp) store_rows(p, zp + 64 * c, 2 * g.N, zw);
+          if (zp) store_rows(p, &tmZ, col, y, zp + 64 * c, 2 * g.N, zw);
           if (g.out) {
             uint32_t w[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(o[2 * i], o[2 * i + 1]);
-            store_rows(p, out + 64 * c, pitch, w);
+            store_rows(p, &tmO, ocol + 32 * c, y, out + 64 * c, pitch, w);
           } else if (g.out_f32) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               uint32_t w[16];
 #pragma unroll
               for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[16 * h + i]);
-              store_rows(p, out + 128 * c + 64 * h, pitch, w);
+              store_rows(p, &tmO, ocol + 32 * c + 16 * h, y, out + 128 * c + 64 * h, pitch, w);
             }
           } else {                      // 32 outputs from col on
             float inv;
@@ -568,6 +578,8 @@ __global__ void __launch_bounds__(GT, 1)
         }
       }
     }
+    if (lane == 0) bulk_wait_all();       // (shared memory is left behind them)
+    __syncwarp();
     gave_up(ok);
   }
   tc_fence_before();
@@ -629,6 +641,19 @@ bool map_scales(CUtensorMap* m, const uint8_t* base, long long total, int chunks
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// [rows, cols] outputs, bf16 or float32, written 32 rows x 64 bytes at a time
+bool map_rows(CUtensorMap* m, const void* base, int rows, int cols, bool f32) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t gdim[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t gstride[1] = {static_cast<cuuint64_t>(cols) * (f32 ? 4 : 2)};
+  const cuuint32_t bdim[2] = {f32 ? 16u : 32u, 32u}, estr[2] = {1, 1};
+  return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+            const_cast<void*>(base), gdim, gstride, bdim, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <bool NV, Epi EPI>
 cudaError_t gemm_t(const CUtensorMap& ta, const CUtensorMap& tw, const Fp4GemmArgs& g, int num_sms,
                    cudaStream_t s) {
@@ -639,6 +664,10 @@ cudaError_t gemm_t(const CUtensorMap& ta, const CUtensorMap& tw, const Fp4GemmAr
   const int chunks = fp4_chunks(NV, g.K);
   if (!map_scales(&tsa, g.a_s, g.a_tiles * chunks, Fp4Sf<NV>::chunks) ||
       !map_scales(&tsw, g.w_s, g.w_tiles * chunks, Fp4Sf<NV>::chunks))
+    return cudaErrorInvalidValue;
+  CUtensorMap to = tsa, tz = tsa;       // (not used where there is no such output)
+  if ((!g.out_q && !map_rows(&to, g.out ? static_cast<const void*>(g.out) : g.out_f32, g.M_cap, g.ldo, !g.out)) ||
+      (g.z && !map_rows(&tz, g.z, g.M_cap, g.N, false)))
     return cudaErrorInvalidValue;
   // the pairs that the device holds at once and the shared-memory attribute, set
   // up once per device and instantiation
@@ -674,7 +703,7 @@ cudaError_t gemm_t(const CUtensorMap& ta, const CUtensorMap& tw, const Fp4GemmAr
                           ((g.N + GN - 1) / GN);
   cfg.gridDim = dim3(2 * static_cast<unsigned>(units < pairs ? units : pairs));
   cfg.dynamicSmemBytes = C::smem(g.E);
-  return cudaLaunchKernelEx(&cfg, kern, ta, tw, tsa, tsw, g);
+  return cudaLaunchKernelEx(&cfg, kern, ta, tw, tsa, tsw, to, tz, g);
 }
 
 }  // namespace
