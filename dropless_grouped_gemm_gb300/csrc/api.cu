@@ -1481,7 +1481,7 @@ int moe_fp4_tensor_scale(const moe_bf16* src, int E, long long n, float* t, void
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int launches = 0;
   ev_begin(st);
-  const cudaError_t e = moe::launch_fp4_tensor_scale(src, E, n, t, sms, st, &launches);
+  const cudaError_t e = moe::launch_fp4_tensor_scale(src, E, n, moe::Fp4Rows{}, 0, t, sms, st, &launches);
   ev_end(st);
   g_last_launches = launches;
   return cuda_rc(e);
@@ -1745,6 +1745,7 @@ int moe_fp4_linear_bwd(const moe_bf16* dout, const moe_bf16* z, const moe_bf16* 
     int n = 0;
     ev_begin(s);
     const cudaError_t e = moe::launch_fp4_tensor_scale(gz, 1, static_cast<long long>(M_cap) * N,
+                                                       moe::Fp4Rows{offsets, E, M_cap, M_cap}, N,
                                                        w.t, sms, s, &n);
     ev_end(s);
     if (e != cudaSuccess) return MOE_E_CUDA;
