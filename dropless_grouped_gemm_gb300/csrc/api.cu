@@ -1379,11 +1379,16 @@ size_t moe_grouped_linear_bwd_workspace_size(int E, int M_cap, int N) {
   return moe::linear_dz_workspace_bytes(E, M_cap, N);
 }
 
-int moe_grouped_linear_bwd(const moe_bf16* dout, const moe_bf16* z, const moe_bf16* a,
-                           const int32_t* offsets, int E, int M_cap, int K, int N,
-                           const moe_bf16* B, int b_layout, int act, int flags, moe_bf16* dz,
-                           moe_bf16* da, moe_bf16* dB, float* dbias, void* workspace,
-                           size_t ws_bytes, int32_t* err, void* stream) {
+}  // extern "C"
+
+namespace {
+
+// moe_grouped_linear_bwd; top: dz's largest finite magnitude (bits), or NULL.
+// (Act none without a bias gradient makes no dz and leaves it.)
+int linear_bwd(const moe_bf16* dout, const moe_bf16* z, const moe_bf16* a, const int32_t* offsets,
+               int E, int M_cap, int K, int N, const moe_bf16* B, int b_layout, int act, int flags,
+               moe_bf16* dz, moe_bf16* da, moe_bf16* dB, float* dbias, void* workspace,
+               size_t ws_bytes, uint32_t* top, int32_t* err, void* stream) {
   g_last_launches = 0;
   g_split_extra = 0;
   const int rc = check_linear(offsets, E, M_cap, K, N, b_layout, act);
@@ -1420,7 +1425,8 @@ int moe_grouped_linear_bwd(const moe_bf16* dout, const moe_bf16* z, const moe_bf
     q.dout = dout; q.z = act == MOE_ACT_NONE ? nullptr : z; q.offsets = offsets; q.E = E;
     q.M_cap = M_cap; q.N = N; q.act = act; q.dz = act == MOE_ACT_NONE ? nullptr : dz;
     q.dbias = dbias; q.accumulate = accumulate; q.part = static_cast<float*>(workspace);
-    q.err = err;
+    q.top = top; q.err = err;
+    if (top && cudaMemsetAsync(top, 0, sizeof(*top), s) != cudaSuccess) return MOE_E_CUDA;
     ev_begin(s);
     const cudaError_t e = moe::launch_linear_dz(q, s, &launches);
     ev_end(s);
@@ -1460,6 +1466,19 @@ int moe_grouped_linear_bwd(const moe_bf16* dout, const moe_bf16* z, const moe_bf
   }
   g_last_launches = launches + g_split_extra;
   return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_grouped_linear_bwd(const moe_bf16* dout, const moe_bf16* z, const moe_bf16* a,
+                           const int32_t* offsets, int E, int M_cap, int K, int N,
+                           const moe_bf16* B, int b_layout, int act, int flags, moe_bf16* dz,
+                           moe_bf16* da, moe_bf16* dB, float* dbias, void* workspace,
+                           size_t ws_bytes, int32_t* err, void* stream) {
+  return linear_bwd(dout, z, a, offsets, E, M_cap, K, N, B, b_layout, act, flags, dz, da, dB, dbias,
+                    workspace, ws_bytes, nullptr, err, stream);
 }
 
 // ------------------------------------------------ 4 bits
@@ -1730,23 +1749,26 @@ int moe_fp4_linear_bwd(const moe_bf16* dout, const moe_bf16* z, const moe_bf16* 
     if (misaligned(workspace)) return MOE_E_ALIGN;
   }
   const Fp4BwdWs w = carve_fp4_bwd(workspace, E, M_cap, N, format);
-  // dz, the bias gradient and the weights' gradient: the bf16 operator's
-  const int r = moe_grouped_linear_bwd(dout, z, a, offsets, E, M_cap, K, N, nullptr, b_layout, act,
-                                       flags, dz, nullptr, dB, dbias, w.part,
-                                       moe::linear_dz_workspace_bytes(E, M_cap, N), err, stream);
+  // dz, the bias gradient and the weights' gradient: the bf16 operator's; with
+  // dz's largest magnitude, where it makes dz
+  const bool nv = format == MOE_FP4_NV;
+  const bool top = nv && da && M_cap > 0 && (act != MOE_ACT_NONE || dbias);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int r = linear_bwd(dout, z, a, offsets, E, M_cap, K, N, nullptr, b_layout, act, flags, dz,
+                           nullptr, dB, dbias, w.part, moe::linear_dz_workspace_bytes(E, M_cap, N),
+                           top ? reinterpret_cast<uint32_t*>(w.t) : nullptr, err, stream);
   if (r != MOE_OK || M_cap == 0 || !da) return r;
   const int sms = num_sms_current();
   if (sms <= 0) return MOE_E_CUDA;
   int launches = g_last_launches;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
   const moe_bf16* gz = act == MOE_ACT_NONE ? dout : dz;
-  const bool nv = format == MOE_FP4_NV;
   if (nv) {
-    int n = 0;
+    int n = 1;
     ev_begin(s);
-    const cudaError_t e = moe::launch_fp4_tensor_scale(gz, 1, static_cast<long long>(M_cap) * N,
-                                                       moe::Fp4Rows{offsets, E, M_cap, M_cap}, N,
-                                                       w.t, sms, s, &n);
+    const cudaError_t e =
+        top ? moe::launch_fp4_power(w.t, 1, s)
+            : moe::launch_fp4_tensor_scale(gz, 1, static_cast<long long>(M_cap) * N,
+                                           moe::Fp4Rows{offsets, E, M_cap, M_cap}, N, w.t, sms, s, &n);
     ev_end(s);
     if (e != cudaSuccess) return MOE_E_CUDA;
     launches += n;

@@ -77,6 +77,8 @@ cudaError_t launch_fp4_dequantize(const uint8_t* q, const uint8_t* s, const Fp4R
 // r.offsets (E 1, n = r.rows K) of the experts' rows alone
 cudaError_t launch_fp4_tensor_scale(const uint16_t* src, int E, long long n, const Fp4Rows& r,
                                     int K, float* t, int num_sms, cudaStream_t st, int* launches);
+// ... t [E] holding the largest magnitudes
+cudaError_t launch_fp4_power(float* t, int E, cudaStream_t st);
 
 // ------------------------------------------------------------- products
 // out_e = act(t_a t_e a4_e w4_e^T + bias_e) + residual, w4 [E, N, K]

@@ -36,6 +36,8 @@
 // output pass, and slowed the streaming of many tiles by 4 to 6%.)
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "act.cuh"
 #include "drain.cuh"
 #include "linear.cuh"
@@ -768,7 +770,9 @@ __device__ __forceinline__ void dz8(const uint4& z, const uint32_t* d, float (&o
   }
 }
 
-template <int ACT>
+// TOP: with the largest finite magnitude of dz (for a scale of its 4-bit copy; one
+// more read of 67 MB of dz took 15.5 us)
+template <int ACT, bool TOP>
 __global__ void __launch_bounds__(kDzThreads, 4) dz_kernel(const LinearDzArgs g) {
   constexpr bool GATED = (ACT == MOE_ACT_SWIGLU || ACT == MOE_ACT_GEGLU);
   __shared__ int s_e, s_r0, s_r1, s_have;
@@ -783,6 +787,7 @@ __global__ void __launch_bounds__(kDzThreads, 4) dz_kernel(const LinearDzArgs g)
   const int c8 = threadIdx.x & 31, rl = threadIdx.x >> 5;
   const int col = blockIdx.y * 256 + c8 * 8;
   float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  uint32_t top = 0;
   if (col < g.N) {
     const int ldd = GATED ? g.N / 2 : g.N;
     const uint16_t* zp = g.z + col;
@@ -810,8 +815,18 @@ __global__ void __launch_bounds__(kDzThreads, 4) dz_kernel(const LinearDzArgs g)
           const uint32_t dw[4] = {dv[u].x, dv[u].y, dv[u].z, dv[u].w};
           float o[8];
           dz8<ACT>(zv[u], dw, o);
-          if (ACT != MOE_ACT_NONE)
-            *reinterpret_cast<uint4*>(g.dz + row * g.N + col) = pack8(o);
+          if (ACT != MOE_ACT_NONE || TOP) {
+            const uint4 w = pack8(o);
+            if (ACT != MOE_ACT_NONE) *reinterpret_cast<uint4*>(g.dz + row * g.N + col) = w;
+            if constexpr (TOP) {
+              const uint32_t wv[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t b = wv[i] & 0x7fff7fffu;
+                top = __vmaxu2(top, b & __vcmpltu2(b, 0x7f807f80u));
+              }
+            }
+          }
 #pragma unroll
           for (int i = 0; i < 8; ++i) sum[i] += o[i];
         }
@@ -819,6 +834,15 @@ __global__ void __launch_bounds__(kDzThreads, 4) dz_kernel(const LinearDzArgs g)
     }
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if constexpr (TOP) {
+    __shared__ uint32_t s_top;
+    if (threadIdx.x == 0) s_top = 0;
+    __syncthreads();
+    top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+    if ((threadIdx.x & 31) == 0 && top != 0) atomicMax(&s_top, top);
+    __syncthreads();
+    if (threadIdx.x == 0 && s_top != 0) atomicMax(g.top, s_top << 16);
+  }
   if (g.dbias == nullptr) return;
 #pragma unroll
   for (int i = 0; i < 8; ++i) s_sum[rl][c8 * 8 + i] = sum[i];
@@ -943,14 +967,19 @@ cudaError_t launch_linear_dz(const LinearDzArgs& in, cudaStream_t s, int* launch
   g.blocks = dz_blocks_cap(g.E, g.M_cap);
   const dim3 grid(g.blocks, (g.N + 255) / 256);
   if (g.M_cap > 0) {
+    auto run = [&](auto act) {
+      constexpr int ACT = decltype(act)::value;
+      if (g.top) dz_kernel<ACT, true><<<grid, kDzThreads, 0, s>>>(g);
+      else dz_kernel<ACT, false><<<grid, kDzThreads, 0, s>>>(g);
+    };
     switch (g.act) {
-      case MOE_ACT_SWIGLU: dz_kernel<MOE_ACT_SWIGLU><<<grid, kDzThreads, 0, s>>>(g); break;
-      case MOE_ACT_GEGLU: dz_kernel<MOE_ACT_GEGLU><<<grid, kDzThreads, 0, s>>>(g); break;
-      case MOE_ACT_SRELU: dz_kernel<MOE_ACT_SRELU><<<grid, kDzThreads, 0, s>>>(g); break;
-      case MOE_ACT_NONE: dz_kernel<MOE_ACT_NONE><<<grid, kDzThreads, 0, s>>>(g); break;
-      case MOE_ACT_RELU: dz_kernel<MOE_ACT_RELU><<<grid, kDzThreads, 0, s>>>(g); break;
-      case MOE_ACT_SILU: dz_kernel<MOE_ACT_SILU><<<grid, kDzThreads, 0, s>>>(g); break;
-      case MOE_ACT_GELU: dz_kernel<MOE_ACT_GELU><<<grid, kDzThreads, 0, s>>>(g); break;
+      case MOE_ACT_SWIGLU: run(std::integral_constant<int, MOE_ACT_SWIGLU>{}); break;
+      case MOE_ACT_GEGLU: run(std::integral_constant<int, MOE_ACT_GEGLU>{}); break;
+      case MOE_ACT_SRELU: run(std::integral_constant<int, MOE_ACT_SRELU>{}); break;
+      case MOE_ACT_NONE: run(std::integral_constant<int, MOE_ACT_NONE>{}); break;
+      case MOE_ACT_RELU: run(std::integral_constant<int, MOE_ACT_RELU>{}); break;
+      case MOE_ACT_SILU: run(std::integral_constant<int, MOE_ACT_SILU>{}); break;
+      case MOE_ACT_GELU: run(std::integral_constant<int, MOE_ACT_GELU>{}); break;
       default: return cudaErrorInvalidValue;
     }
     const cudaError_t e = cudaGetLastError();

@@ -52,6 +52,7 @@ struct LinearDzArgs {
   float* dbias;              // [E, N] or NULL
   int accumulate;            // dbias += the sums
   float* part;               // workspace
+  uint32_t* top;             // dz's largest finite magnitude, as bits: raised to it; or NULL
   int blocks;                // row blocks of the grid (set by the launcher)
   int32_t* err;
 };
