@@ -553,14 +553,14 @@ cudaError_t few_t(const CUtensorMap& tw, const CUtensorMap& tx, const Fp4GemmArg
 
 // The choice, by an estimate of the time in nanoseconds with these measured
 // rates.  This kernel: 3.5 us of launch, prologue and end; a stage (256 of K)
-// 260 ns, 330 with more than 16 tokens; ending a tile 1 us, joining a split 2.5;
+// 260 ns, 350 with more than 16 tokens; ending a tile 1.5 us, joining a split 2.5;
 // where no other tile reads a tile's weights, their share of 6.6 TB/s at least.
-// The pairs' kernel: 4.6 us, a stage 320 ns, a tile's end 2.6 us, and the same
-// share.  Measured, us, this kernel / the pairs': dense 64 x 4096 x 4096 8.8 /
-// 10.8, 256 rows 11.5 / 11.8, 512 rows 16.8 / 11.9, 1024 rows 28.7 / 13.7, 256 x
-// 7168 x 2048 11.6 / 15.3; 57 experts with 128 rows, 2048 x 7168 77.2 / 106, 7168 x
-// 4096 142 / 160, with 2000 rows, 2048 x 7168 83.7 / 108.6; 8 experts, 4096 x
-// 4096, 512 rows 24.4 / 22.4, 1000 rows 31.1 / 24.6.
+// The pairs' kernel: 4 us, a stage 300 ns, a tile's end 1.9 us, and the same
+// share.  Measured, us, this kernel / the pairs': dense 64 x 4096 x 4096 8.7 /
+// 10.1, 128 rows 9.6 / 10.7, 256 rows 11.5 / 10.7, 512 rows 16.7 / 10.8, 1024 rows
+// 28.7 / 12.3, 256 x 7168 x 2048 11.5 / 13.9; 57 experts with 128 rows, 2048 x 7168
+// 77.2 / 90.3, 7168 x 4096 142 / 153, with 2000 rows, 2048 x 7168 83.7 / 96.4; 8
+// experts, 4096 x 4096, 512 rows 24.4 / 21.7, 1000 rows 30.9 / 23.6.
 Fp4Plan fp4_plan(int E, int M_cap, int K, int N, bool ragged, int num_sms) {
   const long long active = ragged ? (E < M_cap ? E : M_cap) : 1;
   const long long avg = (M_cap + active - 1) / active;
@@ -574,7 +574,7 @@ Fp4Plan fp4_plan(int E, int M_cap, int K, int N, bool ragged, int num_sms) {
     const long long fit = few_clusters(split, num_sms);
     const long long ctas = (units < fit ? units : fit) * split;
     const long long stages = (kb + split - 1) / split;
-    long long tile = stages * (avg <= kFp4FewBox ? 260 : 330) + (split == 1 ? 1000 : 2500);
+    long long tile = stages * (avg <= kFp4FewBox ? 260 : 350) + (split == 1 ? 1500 : 2500);
     const long long read = stages * (ctas * 18432 / 6600);
     if (avg <= TN && read > tile) tile = read;
     const long long cost = 3500 + (units + fit - 1) / fit * tile;
@@ -585,10 +585,10 @@ Fp4Plan fp4_plan(int E, int M_cap, int K, int N, bool ragged, int num_sms) {
   }
   const long long tiles = (avg + 255) / 256 * active * ((N + 255) / 256);
   const long long places = num_sms / 2;
-  long long tile = kb * 320 + 2600;
+  long long tile = kb * 300 + 1900;
   const long long read = kb * ((tiles < places ? tiles : places) * 36864 / 6600);
   if (avg <= 256 && read > tile) tile = read;
-  const long long big = 4600 + (tiles + places - 1) / places * tile;
+  const long long big = 4000 + (tiles + places - 1) / places * tile;
   return big < best ? Fp4Plan{} : p;
 }
 

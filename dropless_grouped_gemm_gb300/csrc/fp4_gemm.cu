@@ -12,14 +12,19 @@
 // the epilogue moves the accumulator to registers and releases it at once, so
 // the next tile's MMAs overlap bias, activation, quantisation and stores.
 //
-// Measured, with the clock at 1.9 GHz: a stage's four MMAs take 0.274 us (MX, 130
-// cycles each: the rate of 9 PFLOP/s) and 0.32 us (NV, whose twelve copies of
-// scales into TMEM take their part), and about 2 us pass between two tiles'
-// MMAs (commit, TMEM to registers, release in both CTAs).  Tiles of 192 columns
-// leave TMEM for two accumulators and hide those, but an MMA of N = 192 takes 123
-// cycles (142 NV), what one of N = 256 takes: 8192 x 8192 x 4864 109 us in place of
-// 96 (MX), 122 of 105 (NV); 8192 x 1024 x 4864 37 of 41.  Pairs that share a's rows
-// by multicast changed nothing (0.258 us a stage of 192 columns either way).
+// Measured: a stage's four MMAs take 0.280 us (MX: 9.1 PFLOP/s while they run) and
+// 0.288 us (NV, with twelve copies of scales into TMEM a stage where MX has six),
+// and 1.6 to 2.1 us pass between two tiles' MMAs (commit, TMEM to registers,
+// release in both CTAs).  Bound by the MMAs where K is long (32,768 x 8,192 x 4,096
+// over 8 experts, bf16 out: 326 us NV, 309 MX, 7.1 PFLOP/s, at the power cap), by
+// those gaps where it is short (8,192 x 1,024 x 4,864 27 us).
+//   Tiles of 192 columns leave TMEM for two accumulators and hide the gaps, but
+// an MMA of N = 192 takes 123 cycles (142 NV), nearly what one of N = 256 takes (130):
+// 36.9 us against 33.2 (8,192 x 1,024 x 4,864) and 134 against 103 (K = 8,192, both
+// with stores from registers).  Pairs that share a's rows by multicast changed
+// nothing.  Eight epilogue warps that hold 128 columns each, with room for 32 KB
+// more of boxes and four stages in place of five: 8,192 x 1,024 x 4,864 26 us plain but 58
+// gated (37 with 16 warps), and K = 8,192 104 in place of 96.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -466,8 +471,8 @@ __global__ void __launch_bounds__(GT, 1)
       float held[GATED && !NV ? 16 : 1];
       uint32_t half[GATED ? 8 : 1];
       // 32 columns at a time from TMEM, which is released with the second load:
-      // both at once spill registers (8192 x 1024 x 4864, geglu with z: 68 us, 52
-      // so; where K is long it costs a little, 32,768 x 8,192 x 4,096 400 us, 412 so)
+      // both at once spill registers (8192 x 1024 x 4864, geglu with z and stores from
+      // registers: 68 us, 52 so; where K is long it costs 3%)
 #pragma unroll 1
       for (int c = 0; c < 2; ++c) {
         const int col = col0 + 32 * c;
