@@ -292,45 +292,46 @@ __global__ void __launch_bounds__(FT, 1)
   const int units = g.offsets != nullptr ? s_ts[g.E] : nt * ((g.M_cap + TN - 1) / TN);
 
   if (warp == 0) {
-    int stage = 0;
-    uint32_t phase = 0, issued = 0;
-    bool ok = true;
-    for (int u = unit0; u < units && ok; u += unit_step) {
-      const FTile t = few_tile(g, s_off, s_ts, u);
-      for (int kb = kb0; kb < kb1; ++kb) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&empty_bar[stage], phase ^ 1, abort_flag));
-        if (!ok) break;
-        if (elect_one()) load(t, kb, stage);
-        __syncwarp();
-        ++issued;
-        if (++stage == NST) { stage = 0; phase ^= 1; }
+    if (elect_one()) {          // (one thread throughout: none to agree with between stages)
+      int stage = 0;
+      uint32_t phase = 0, issued = 0;
+      bool ok = true;
+      for (int u = unit0; u < units && ok; u += unit_step) {
+        const FTile t = few_tile(g, s_off, s_ts, u);
+        for (int kb = kb0; kb < kb1; ++kb) {
+          ok = mbar_wait(&empty_bar[stage], phase ^ 1, abort_flag);
+          if (!ok) break;
+          load(t, kb, stage);
+          ++issued;
+          if (++stage == NST) { stage = 0; phase ^= 1; }
+        }
       }
+      loads[0] = issued;
     }
-    if (elect_one()) loads[0] = issued;
     __syncwarp();
     cluster_wait();
   } else if (warp == 1) {
-    int stage = 0, local = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    const uint32_t w_lo0 = sdesc_lo(smem_u32(smem), 16);
-    const uint32_t x_lo0 = sdesc_lo(smem_u32(smem) + W_BYTES, 16);
-    const uint32_t sf0 = smem_u32(sf_region);
-    for (int u = unit0; u < units && ok; u += unit_step, ++local) {
-      const FTile t = few_tile(g, s_off, s_ts, u);
-      const int buf = local & 1;
-      ok = __all_sync(0xffffffffu, mbar_wait(&tempty_bar[buf], ((local >> 1) & 1) ^ 1, abort_flag));
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t d = tmem_base + buf * TN;
-      const uint32_t idesc =
-          fp4_idesc<NV>(FM, (t.rows + kFp4FewBox - 1) / kFp4FewBox * kFp4FewBox);
-      const uint32_t half = 2 * (t.ti & 1);
-      for (int kb = kb0; kb < kb1; ++kb) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&full_bar[stage], phase, abort_flag));
+    if (elect_one()) {
+      int stage = 0, local = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      const uint32_t w_lo0 = sdesc_lo(smem_u32(smem), 16);
+      const uint32_t x_lo0 = sdesc_lo(smem_u32(smem) + W_BYTES, 16);
+      const uint32_t sf0 = smem_u32(sf_region);
+      for (int u = unit0; u < units && ok; u += unit_step, ++local) {
+        const FTile t = few_tile(g, s_off, s_ts, u);
+        const int buf = local & 1;
+        ok = mbar_wait(&tempty_bar[buf], ((local >> 1) & 1) ^ 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
-        if (elect_one()) {
+        const uint32_t d = tmem_base + buf * TN;
+        const uint32_t idesc =
+            fp4_idesc<NV>(FM, (t.rows + kFp4FewBox - 1) / kFp4FewBox * kFp4FewBox);
+        const uint32_t half = 2 * (t.ti & 1);
+        for (int kb = kb0; kb < kb1; ++kb) {
+          ok = mbar_wait(&full_bar[stage], phase, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
           const uint32_t ss = sf0 + stage * C::sf_bytes;
           const uint32_t tw = tmem_base + SF_TMEM + stage * C::sf_cols;
           const uint32_t tx = tw + SF::cols;
@@ -351,12 +352,10 @@ __global__ void __launch_bounds__(FT, 1)
                                   tx + 4 * fp4_step_chunk<NV>(kk) + half,
                                   (kb > kb0 || kk > 0) ? 1u : 0u);
           umma_commit(&empty_bar[stage]);
+          if (++stage == NST) { stage = 0; phase ^= 1; }
         }
-        __syncwarp();
-        if (++stage == NST) { stage = 0; phase ^= 1; }
+        if (ok) umma_commit(&tfull_bar[buf]);
       }
-      if (ok && elect_one()) umma_commit(&tfull_bar[buf]);
-      __syncwarp();
     }
     __syncwarp();
     cluster_wait();

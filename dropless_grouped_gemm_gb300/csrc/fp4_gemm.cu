@@ -341,34 +341,32 @@ __global__ void __launch_bounds__(GT, 1)
           ok = mbar_wait(&full_bar[stage], phase, abort_flag);
           if (!ok) break;
           tc_fence_after();
-          {
-            const uint32_t ss = sf0 + stage * C::sf_bytes;
-            const uint32_t ta = tmem_base + SF_TMEM + stage * C::sf_cols;
-            const uint32_t tw = ta + SF::cols;
+          const uint32_t ss = sf0 + stage * C::sf_bytes;
+          const uint32_t ta = tmem_base + SF_TMEM + stage * C::sf_cols;
+          const uint32_t tw = ta + SF::cols;
 #pragma unroll
-            for (int c = 0; c < SF::chunks; ++c) {
-              tmem_cp_sf_pair(ta + 4 * c, fp4_sf_desc(ss + c * kFp4ChunkBytes));
-              tmem_cp_sf_pair(tw + 8 * c, fp4_sf_desc(ss + SF::bytes + c * kFp4ChunkBytes));
-              tmem_cp_sf_pair(tw + 8 * c + 4, fp4_sf_desc(ss + 2 * SF::bytes + c * kFp4ChunkBytes));
-            }
-            const uint32_t a_lo = a_lo0 + stage * (C::stage_bytes >> 4);
-            const uint32_t w_lo = w_lo0 + stage * (C::stage_bytes >> 4);
-            auto mma = [&](int kk) {
-              umma_fp4<NV, true>(tmem_base, sdesc_of(a_lo + kk * 2), sdesc_of(w_lo + kk * 2),
-                                 IDESC | fp4_select<NV>(kk), ta + 4 * fp4_step_chunk<NV>(kk),
-                                 tw + 8 * fp4_step_chunk<NV>(kk), (kb > 0 || kk > 0) ? 1u : 0u);
-            };
-            const int steps = min(4, (g.K - kb * kFp4StageK) / kFp4StepK);
-            if (steps == 4) {
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk) mma(kk);
-            } else {          // the end of a K that is no multiple of 256
-#pragma unroll
-              for (int kk = 0; kk < 3; ++kk)
-                if (kk < steps) mma(kk);
-            }
-            umma_commit_pair_mc(&empty_bar[stage]);
+          for (int c = 0; c < SF::chunks; ++c) {
+            tmem_cp_sf_pair(ta + 4 * c, fp4_sf_desc(ss + c * kFp4ChunkBytes));
+            tmem_cp_sf_pair(tw + 8 * c, fp4_sf_desc(ss + SF::bytes + c * kFp4ChunkBytes));
+            tmem_cp_sf_pair(tw + 8 * c + 4, fp4_sf_desc(ss + 2 * SF::bytes + c * kFp4ChunkBytes));
           }
+          const uint32_t a_lo = a_lo0 + stage * (C::stage_bytes >> 4);
+          const uint32_t w_lo = w_lo0 + stage * (C::stage_bytes >> 4);
+          auto mma = [&](int kk) {
+            umma_fp4<NV, true>(tmem_base, sdesc_of(a_lo + kk * 2), sdesc_of(w_lo + kk * 2),
+                               IDESC | fp4_select<NV>(kk), ta + 4 * fp4_step_chunk<NV>(kk),
+                               tw + 8 * fp4_step_chunk<NV>(kk), (kb > 0 || kk > 0) ? 1u : 0u);
+          };
+          const int steps = min(4, (g.K - kb * kFp4StageK) / kFp4StepK);
+          if (steps == 4) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) mma(kk);
+          } else {          // the end of a K that is no multiple of 256
+#pragma unroll
+            for (int kk = 0; kk < 3; ++kk)
+              if (kk < steps) mma(kk);
+          }
+          umma_commit_pair_mc(&empty_bar[stage]);
           if (++stage == STAGES) { stage = 0; phase ^= 1; }
         }
         if (ok) umma_commit_pair_mc(tfull_bar);
