@@ -20,8 +20,8 @@
 // those gaps where it is short (8,192 x 1,024 x 4,864 27 us).
 //   Tiles of 192 columns leave TMEM for two accumulators and hide the gaps, but
 // an MMA of N = 192 takes 123 cycles (142 NV), nearly what one of N = 256 takes (130):
-// 36.9 us against 33.2 (8,192 x 1,024 x 4,864) and 134 against 103 (K = 8,192, both
-// with stores from registers).  Pairs that share a's rows by multicast changed
+// 8,192 rows x 4,864, NV, K = 1,024 26.2 us against 27.4, 2,048 41.8 against 39.7, 8,192
+// 116 against 96.  Not worth a second tile.  Pairs that share a's rows by multicast changed
 // nothing.  Eight epilogue warps that hold 128 columns each, with room for 32 KB
 // more of boxes and four stages in place of five: 8,192 x 1,024 x 4,864 26 us plain but 58
 // gated (37 with 16 warps), and K = 8,192 104 in place of 96.
