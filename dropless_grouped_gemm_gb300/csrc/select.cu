@@ -24,7 +24,10 @@
 // Bound by instructions on long batches (65,536 x 256, sigmoid, bias, 8 groups:
 // 144 us with a search of the lane's values in every round, 91 now), by launch latency on
 // short ones.  Backward: a warp per token, the k gradients scattered into a row
-// in shared memory that leaves in 16-byte stores; bound by those writes.
+// in shared memory that leaves in 16-byte stores, the next token's pairs read
+// meanwhile; a softmax's exponentials are taken once and wait in that row (taken
+// again for the output: 48 us for 65,536 x 256, now 39).  Bound by latency and by
+// the writes (by sigmoid 25.7 us, 2.6 TB/s of them; 34 with more blocks than are resident).
 #include <cuda_bf16.h>
 
 #include <type_traits>
@@ -37,6 +40,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kRows = kThreads / 32;      // tokens of a block, one a warp
+constexpr int kBwdBlocks = 5;             // of the gradient's an SM, all resident
 constexpr unsigned kAll = 0xffffffffu;
 // bf16's lowest finite value: a mask's logit is there, at float32's lowest, or -inf
 constexpr float kMasked = -3.3895313892515355e38f;
@@ -524,56 +528,71 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
 // A pair with an id outside [0, E) takes no part; an expert chosen twice by a
 // token gets both terms, in the order of the pairs.
 template <class T, class TO, int VEC, bool DENSE>
-__global__ void __launch_bounds__(kThreads) select_bwd_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(kThreads, kBwdBlocks) select_bwd_kernel(const SelectArgs a) {
   extern __shared__ __align__(16) float rows[];       // [kRows][E padded to 4]
   const int lane = threadIdx.x & 31;
   float* acc = rows + (threadIdx.x >> 5) * ((a.E + 3) & ~3);
   for (int e = lane; e < a.E; e += 32) acc[e] = 0.f;
   __syncwarp();
   const int step = gridDim.x * kRows;
-  for (int t = blockIdx.x * kRows + (threadIdx.x >> 5); t < a.T; t += step) {
+  // lane j: pair j of a token, read while the token before is worked on
+  struct Pair {
+    int e;
+    float w, g;
+  };
+  auto pair_of = [&](int t) {
+    Pair p{-1, 0.f, 0.f};
+    if (lane < a.k && t < a.T) {
+      const long long o = static_cast<long long>(t) * a.k + lane;
+      p = Pair{a.idx[o], a.probs[o], a.dprobs[o]};
+    }
+    return p;
+  };
+  const int t0 = blockIdx.x * kRows + (threadIdx.x >> 5);
+  Pair ahead = pair_of(t0);
+  for (int t = t0; t < a.T; t += step) {
     const T* row = static_cast<const T*>(a.logits) + static_cast<long long>(t) * a.E;
     TO* out = static_cast<TO*>(a.dlogits) + static_cast<long long>(t) * a.E;
-    int e = -1;
-    float w = 0.f, g = 0.f;
-    if (lane < a.k) {
-      const long long o = static_cast<long long>(t) * a.k + lane;
-      e = a.idx[o];
-      if (e < 0 || e >= a.E) e = -1;
-      if (e >= 0) {
-        w = a.probs[o];
-        g = a.dprobs[o];
-      }
-    }
+    const Pair pair = ahead;
+    ahead = pair_of(t + step);
+    const int e = pair.e >= 0 && pair.e < a.E ? pair.e : -1;
+    const float w = e >= 0 ? pair.w : 0.f;
+    float g = e >= 0 ? pair.g : 0.f;
     const float dot = warp_add(w * g);
     g = a.renorm ? w * (g - dot / a.scale) : w * g;
     if (a.score == MOE_SCORE_SIGMOID && e >= 0) g *= 1.f / (1.f + expf(logit(row + e)));
     const unsigned twins = __match_any_sync(kAll, e);
-    if (e >= 0) {
-      const bool first = lane == __ffs(twins) - 1;
-      if (twins & (twins - 1)) {                      // chosen more than once
-        float s = 0.f;
-        for (unsigned r = twins; r != 0; r &= r - 1) s += __shfl_sync(twins, g, __ffs(r) - 1);
-        if (first) acc[e] = s;
-      } else {
-        acc[e] = g;
-      }
+    const bool first = e >= 0 && lane == __ffs(twins) - 1;
+    float mine = g;
+    if (e >= 0 && (twins & (twins - 1))) {            // chosen more than once
+      mine = 0.f;
+      for (unsigned r = twins; r != 0; r &= r - 1) mine += __shfl_sync(twins, g, __ffs(r) - 1);
     }
-    float m = -INFINITY, share = 0.f;
-    if constexpr (DENSE) {
+    if constexpr (!DENSE) {
+      if (first) acc[e] = mine;
+    } else {
       const float total = warp_add(e >= 0 ? g : 0.f);
-      float sum = 0.f;
+      float m = -INFINITY, sum = 0.f;
       for (int i = lane; i < a.E; i += 32) {
         const float z = logit(row + i);
         if (takes_part(z)) m = fmaxf(m, z);
       }
       m = warp_max(m);
+      // the exponentials in the row, -1 for a mask; then the gradients in their place
       for (int i = lane; i < a.E; i += 32) {
         const float z = logit(row + i);
-        if (takes_part(z)) sum += exp_below(z, m);
+        const float x = takes_part(z) ? exp_below(z, m) : -1.f;
+        if (x >= 0.f) sum += x;
+        acc[i] = x;
       }
       sum = warp_add(sum);
-      share = sum > 0.f ? total / sum : 0.f;
+      const float share = sum > 0.f ? total / sum : 0.f;
+      __syncwarp();
+      if (first && acc[e] >= 0.f) mine -= acc[e] * share;
+      __syncwarp();
+      for (int i = lane; i < a.E; i += 32) acc[i] = acc[i] >= 0.f ? -acc[i] * share : 0.f;
+      __syncwarp();
+      if (first) acc[e] = mine;
     }
     __syncwarp();
     for (int i = lane * VEC; i < a.E; i += 32 * VEC) {
@@ -583,13 +602,6 @@ __global__ void __launch_bounds__(kThreads) select_bwd_kernel(const SelectArgs a
         v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
       } else {
         v[0] = acc[i];
-      }
-      if constexpr (DENSE) {
-#pragma unroll
-        for (int x = 0; x < VEC; ++x) {
-          const float z = logit(row + i + x);
-          if (takes_part(z)) v[x] -= exp_below(z, m) * share;
-        }
       }
       if (a.accumulate) {
 #pragma unroll
@@ -606,7 +618,7 @@ __global__ void __launch_bounds__(kThreads) select_bwd_kernel(const SelectArgs a
       }
     }
     __syncwarp();
-    if (e >= 0) acc[e] = 0.f;
+    if (!DENSE && e >= 0) acc[e] = 0.f;
     __syncwarp();
   }
 }
@@ -622,14 +634,14 @@ cudaError_t with_lane(int E, F&& f) {
   return f(std::integral_constant<int, 32>{});
 }
 
-int blocks_of(int T, int num_sms) {
-  const long long want = (static_cast<long long>(T) + kRows - 1) / kRows;
-  return static_cast<int>(want < 8LL * num_sms ? want : 8LL * num_sms);
+int blocks_of(int T, int most) {
+  const int want = static_cast<int>((static_cast<long long>(T) + kRows - 1) / kRows);
+  return want < most ? want : most;
 }
 
 template <class T, int NV, bool SCORED>
 cudaError_t select_t(const SelectArgs& a, int num_sms, cudaStream_t s) {
-  const int blocks = blocks_of(a.T, num_sms);
+  const int blocks = blocks_of(a.T, 8 * num_sms);
   // lanes' experts in 8- and 16-byte loads: whole lanes, and rows that keep the alignment
   constexpr int bytes = NV * static_cast<int>(sizeof(T));
   constexpr int align = bytes < 16 ? bytes : 16;
@@ -646,7 +658,7 @@ cudaError_t select_t(const SelectArgs& a, int num_sms, cudaStream_t s) {
 
 template <class T, class TO>
 cudaError_t bwd_t(const SelectArgs& a, int num_sms, cudaStream_t s) {
-  const int blocks = blocks_of(a.T, num_sms);
+  const int blocks = blocks_of(a.T, kBwdBlocks * num_sms);
   const size_t smem = static_cast<size_t>(kRows) * ((a.E + 3) & ~3) * sizeof(float);
   const bool dense = a.score == MOE_SCORE_SOFTMAX && !a.renorm;
   const bool vec = a.E % 4 == 0 && reinterpret_cast<uintptr_t>(a.dlogits) % (4 * sizeof(TO)) == 0;
