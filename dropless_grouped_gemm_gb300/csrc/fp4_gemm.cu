@@ -65,12 +65,15 @@ struct GC {
       smem(MOE_MAX_EXPERTS) > smem(box_experts) ? smem(MOE_MAX_EXPERTS) : smem(box_experts);
 };
 
-// an arrival on a barrier of the cluster that orders no memory: the accumulator
-// has been read when tcgen05.wait::ld returns, and nothing else is handed over.
-// (With release semantics it waits for the warp's stores of the tile before: 1000
-// to 2000 cycles.)
-__device__ __forceinline__ void mbar_arrive_relaxed(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+// An arrival at the pair's first CTA that hands over TMEM alone.  TMEM's order is
+// the tcgen05 fences', before this arrival and after the wait for it, and its reads
+// are over when tcgen05.wait::ld returns; no shared or global memory is passed on,
+// so the release is the CTA's.  One at cluster scope waits, beyond that, for the
+// output stores that the SM has under way: 800 to 2000 cycles a tile (8,192 x 1,024
+// x 4,864 31.8 us with it, 27.4 so; 32,768 x 8,192 x 4,096 331, 323; by one thread of the CTA for
+// all its warps 32.5, 335).
+__device__ __forceinline__ void mbar_arrive_tmem(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
 }
 
@@ -404,7 +407,7 @@ __global__ void __launch_bounds__(GT, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          if (rank != 0) mbar_arrive_relaxed(tempty0);
+          if (rank != 0) mbar_arrive_tmem(tempty0);
           else mbar_arrive(tempty_bar);
         }
       };
