@@ -84,31 +84,40 @@ __device__ __forceinline__ void fp4_schedule(const int32_t* offsets, int E, int 
   }
   bool bad = false;
   int top = 0, carry = 0;
-  for (int base = 0; base <= E; base += 32) {
-    const int i = base + lane;
-    const int raw = i <= E ? offsets[i] : 0;
-    int m = max(min(max(raw, 0), M_cap), top);
+  for (int base = 0; base <= E; base += 128) {        // four loads in flight
+    int raw[4];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, m, o);
-      if (lane >= o) m = max(m, y);
+    for (int b = 0; b < 4; ++b) {
+      const int i = base + 32 * b + lane;
+      raw[b] = i <= E ? offsets[i] : 0;
     }
-    if (i <= E) {
-      if (m != raw || (i == 0 && m != 0)) bad = true;
-      s_off[i] = m;
-    }
-    // expert i - 1 ends at m
-    int prev = __shfl_up_sync(0xffffffffu, m, 1);
-    if (lane == 0) prev = top;
-    int c = (i >= 1 && i <= E) ? units(m - prev) : 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, c, o);
-      if (lane >= o) c += y;
+    for (int b = 0; b < 4; ++b) {
+      const int i = base + 32 * b + lane;
+      if (base + 32 * b > E) break;
+      int m = max(min(max(raw[b], 0), M_cap), top);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, m, o);
+        if (lane >= o) m = max(m, y);
+      }
+      if (i <= E) {
+        if (m != raw[b] || (i == 0 && m != 0)) bad = true;
+        s_off[i] = m;
+      }
+      // expert i - 1 ends at m
+      int prev = __shfl_up_sync(0xffffffffu, m, 1);
+      if (lane == 0) prev = top;
+      int c = (i >= 1 && i <= E) ? units(m - prev) : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, c, o);
+        if (lane >= o) c += y;
+      }
+      if (i <= E) s_ts[i] = carry + c;
+      top = __shfl_sync(0xffffffffu, m, 31);
+      carry += __shfl_sync(0xffffffffu, c, 31);
     }
-    if (i <= E) s_ts[i] = carry + c;
-    top = __shfl_sync(0xffffffffu, m, 31);
-    carry += __shfl_sync(0xffffffffu, c, 31);
   }
   if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0) set_err(err, MOE_DEV_BAD_OFFSETS);
 }
