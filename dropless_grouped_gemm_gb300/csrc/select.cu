@@ -45,6 +45,11 @@ constexpr unsigned kAll = 0xffffffffu;
 // bf16's lowest finite value: a mask's logit is there, at float32's lowest, or -inf
 constexpr float kMasked = -3.3895313892515355e38f;
 
+// below this a float32 sigmoid is subnormal (and from -88.8 on 0); from the second
+// one on a 64-bit one is 0, and counts as 0 here
+constexpr float kLowSigmoid = -87.f;
+constexpr float kNoSigmoid = -709.7827f;
+
 __device__ __forceinline__ bool takes_part(float z) { return z > kMasked; }   // (false for NaN)
 
 // signed keys in the order of the floats (-0 as +0); kNone: none
@@ -501,6 +506,11 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
     if (a.score == MOE_SCORE_SIGMOID) {
       if (on) w = 1.f / (1.f + expf(-zs));
       if (a.renorm) {
+        if (__any_sync(kAll, on && zs < kLowSigmoid)) {
+          // all below 0: numerator and sum times e^-m, m the largest logit
+          const float m0 = warp_max(on ? zs : -INFINITY);
+          if (m0 < 0.f) w = on && zs > kNoSigmoid ? expf(zs - m0) / (1.f + expf(zs)) : 0.f;
+        }
         const float tot = warp_add(w);
         w = tot > 0.f ? w / tot : 0.f;
       }

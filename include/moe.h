@@ -786,7 +786,8 @@ int moe_router_loss_bwd(const void* logits, int logits_type, const int32_t* topk
  *             the k chosen
  * An expert whose logit is NaN or at most bf16's lowest finite value (a mask),
  * or whose c is NaN or -inf, takes no part; where fewer than k are left, the
- * other picks are -1 with probability 0, and a sum of 0 gives probabilities 0.
+ * other picks are -1 with probability 0, and a sum of 0 gives probabilities 0
+ * (a sigmoid counts as 0 where 64 bits have none, at logits below -709.78).
  *   logits [T, E] float32 or bf16 (logits_type MOE_TYPE_*), aligned to their
  *   type; 1 <= k <= 32, k <= E / groups * top_groups; groups divides E, at most
  *   32; group_best <= E / groups; scale > 0 and finite; T <= 2^30.  One launch.
