@@ -230,12 +230,22 @@ __device__ __noinline__ int exact_choice(const SelectArgs& a, long long t, Exact
 // division two, of s <= 1), a softmax's s 22 u (expf two units, z - m u |z - m|
 // of an s that is as much smaller, the sum's chains of 8 + 2 + 5 additions, the
 // reciprocal and the product); c's addition rounds by u |c|, and a key's last bits
-// hide up to NV - 1 units of 2 u |c|.  Twice that for sums of two.
+// hide up to NV - 1 units of 2 u |c|.
 template <int NV>
-__device__ __forceinline__ bool in_doubt(int score, float hi, float lo, float times) {
+__device__ __forceinline__ bool in_doubt(int score, float hi, float lo) {
   const float own = score == MOE_SCORE_SIGMOID ? 12.f : 44.f;
-  const float tol = times * 5.9604644775390625e-8f * (own + 2.f * NV * fmaxf(fabsf(hi), fabsf(lo)));
+  const float tol = 5.9604644775390625e-8f * (own + 2.f * NV * fmaxf(fabsf(hi), fabsf(lo)));
   return !(hi - lo > tol);
+}
+
+// How far a float32 group score may be off: its terms' errors (own: half of
+// in_doubt's for each of two), and by the terms' sizes, which its own may be far
+// below, the keys' hidden bits, both additions and what is done with it here.
+template <int NV>
+__device__ __forceinline__ float group_slack(int score, float t1, float t2, int best) {
+  const float own = score == MOE_SCORE_SIGMOID ? 12.f : 44.f;
+  const float size = fabsf(t1) + ((best == 2 && t2 > -INFINITY) ? fabsf(t2) : 0.f);
+  return size < INFINITY ? 5.9604644775390625e-8f * (own + (2.f * NV + 2.f) * size) : 0.f;
 }
 
 // Whether an expert other than pick `at` (the last one chosen), and not equal to
@@ -342,7 +352,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
     bool doubt = false, keep = true;
     unsigned kept = kAll;                             // groups, a bit each
     if (limited) {
-      float score = -INFINITY;                        // lane's group's, or lane g: group g's
+      float score = -INFINITY, slack = 0.f;           // lane's group's, or lane g: group g's
       int mine = lane;
       if (lanes > 0) {
         // (values without the keys' last bits)
@@ -354,6 +364,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
           top2(t1, t2, b1, b2);
         }
         score = group_score(t1, t2, a.best);
+        if constexpr (SCORED) slack = group_slack<NV>(a.score, t1, t2, a.best);
         mine = lane / lanes;
       } else {
         for (int g = 0; g < a.groups; ++g) {
@@ -369,7 +380,10 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
             const float b1 = __shfl_xor_sync(kAll, t1, o), b2 = __shfl_xor_sync(kAll, t2, o);
             top2(t1, t2, b1, b2);
           }
-          if (lane == g) score = group_score(t1, t2, a.best);
+          if (lane == g) {
+            score = group_score(t1, t2, a.best);
+            if constexpr (SCORED) slack = group_slack<NV>(a.score, t1, t2, a.best);
+          }
         }
       }
       int before = 0;
@@ -380,15 +394,13 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
       }
       const bool in = mine < a.groups;
       keep = in && before < a.top_groups;
-      const float lo = value_of(__reduce_min_sync(kAll, keep ? key_of(score) : 0x7fffffff));
-      const int hk = __reduce_max_sync(kAll, in && !keep ? key_of(score) : kNone);
+      // the least that a kept group's score may be, the most that a dropped one's
+      const float lo = value_of(__reduce_min_sync(kAll, keep ? key_of(score - slack) : 0x7fffffff));
+      const int hk = __reduce_max_sync(kAll, in && !keep ? key_of(score + slack) : kNone);
       const float hi = value_of(hk);
-      if (hk != kNone && hi > -INFINITY) {
-        // scores without a bias, each group's largest: the largest logits, of
-        // which the keys hide the last bits of float32
-        if constexpr (SCORED) doubt |= in_doubt<NV>(a.score, lo, hi, 2.f);
-        else if constexpr (sizeof(T) == 4) doubt |= lo == hi;
-      }
+      // (scores without a bias, each group's largest: the largest logits, of which
+      // the keys hide the last bits of float32)
+      if (hk != kNone && hi > -INFINITY && (SCORED || sizeof(T) == 4)) doubt = !(lo > hi);
       if (lanes == 0) kept = __ballot_sync(kAll, keep);
       if (!SCORED || biased) {                        // (keys at a group's end become none, not in order)
         bool gap = false;
@@ -443,7 +455,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
     // bits that the keys hide (bf16 logits have none there)
     if (biased || sizeof(T) == 4) {
       auto near = [&](int hi, int lo) {
-        return biased ? in_doubt<NV>(a.score, value_of(hi), value_of(lo), 1.f) : hi == lo;
+        return biased ? in_doubt<NV>(a.score, value_of(hi), value_of(lo)) : hi == lo;
       };
       int nk = __shfl_down_sync(kAll, mykey, 1);
       const int ne = __shfl_down_sync(kAll, pick, 1);
