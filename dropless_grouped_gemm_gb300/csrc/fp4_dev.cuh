@@ -57,7 +57,7 @@ __device__ __forceinline__ uint32_t fp4_scale(uint32_t amax_bits, float t, float
     if (amax_bits >= 0x7f800000u) { inv = 0.f; return 0x7fu; }
     const uint32_t s = e4m3x2(__fdiv_rn(__uint_as_float(amax_bits), 6.f * t), 0.f) & 0xffu;
     const float d = e4m3_value(s) * t;
-    inv = d > 0.f ? __frcp_rn(d) : 0.f;
+    inv = d > 0.f ? fminf(__frcp_rn(d), 3.402823466e38f) : 0.f;    // (finite: 0 stays 0)
     return s;
   } else {
     if (amax_bits >= 0x7f800000u) { inv = 0.f; return 0xffu; }
@@ -88,26 +88,43 @@ __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
 }
 
 // A tensor scale as the quantisers of bf16 values use it.  With a power of two
-// (in 2^-100 .. 2^100, so that nothing under- or overflows) quotients need no
-// division: the quotient of an 8-bit significand and a 4-bit one (or 6, or their
-// product) either is one of the halves between two codes, or at least 1/256 away
-// from it, so rounding a float32 product with a reciprocal (2^-22 off at most)
-// to 11 or 12 bits gives the side, and the ties, of the exact quotient.
+// quotients need no division: the quotient of an 8-bit significand and a 4-bit one
+// (or 6, or their product) either is one of the halves between two codes, or at
+// least 1/256 away from it, so rounding a float32 product with a reciprocal (2^-22
+// off at most) to 11 or 12 bits gives the side, and the ties, of the exact
+// quotient.  Scales near the ends of float32's range, whose reciprocals would leave
+// it, are used times `shift`, a power of two, and so are their values
+// (fp4_shift): t is 2^-117 to 2^96 then, s t and its reciprocal are normal.
 struct Fp4Tensor {
-  float t, inv6, inv;
+  float t, inv6, inv, shift;
   bool exact;
 };
 __device__ __forceinline__ Fp4Tensor fp4_tensor(float t) {
   Fp4Tensor r;
+  r.shift = t < 0x1p-94f ? 0x1p32f : t > 0x1p94f ? 0x1p-32f : 1.f;
+  t *= r.shift;
   r.t = t;
   const uint32_t b = __float_as_uint(t);
-  r.exact = (b & 0x7fffffu) == 0u && b >= (27u << 23) && b <= (227u << 23);
+  r.exact = (b & 0x7fffffu) == 0u && b >= (10u << 23) && b <= (223u << 23);    // 2^-117 .. 2^96
   r.inv = __uint_as_float((254u << 23) - b);      // (of a power of two)
   r.inv6 = r.inv * (1.f / 6.f);
   return r;
 }
 
-// the scale byte and the multiplier of a block of bf16 values
+// bf16 values (words of pairs) times t.shift.  Exact, or past bf16's range, where
+// its last value saturates as well, or below it, where a code is 0.
+template <int N>
+__device__ __forceinline__ void fp4_shift(uint32_t (&p)[N], const Fp4Tensor& t) {
+  if (t.shift == 1.f) return;
+  auto shifted = [&](float v) {
+    const float f = v * t.shift;
+    return fabsf(v) < INFINITY && fabsf(f) > 0x1.fep127f ? copysignf(0x1.fep127f, f) : f;
+  };
+#pragma unroll
+  for (int i = 0; i < N; ++i) p[i] = pack_bf16x2(shifted(bf16_lo(p[i])), shifted(bf16_hi(p[i])));
+}
+
+// the scale byte and the multiplier of a block of bf16 values (shifted)
 template <bool NV>
 __device__ __forceinline__ uint32_t fp4_scale_bf16(uint32_t amax_bits, const Fp4Tensor& t,
                                                    float& inv) {

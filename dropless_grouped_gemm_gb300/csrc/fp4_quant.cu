@@ -96,7 +96,8 @@ __device__ __forceinline__ long long scales_at(const RowAt& r, int k0) {
 
 // A lane's 16 values (8 words) as codes and its scale byte (MX: the pair's)
 template <bool NV>
-__device__ __forceinline__ uint2 quant16(const uint32_t (&p)[8], const Fp4Tensor& t, uint32_t& byte) {
+__device__ __forceinline__ uint2 quant16(uint32_t (&p)[8], const Fp4Tensor& t, uint32_t& byte) {
+  if constexpr (NV) fp4_shift(p, t);
   uint32_t m = bf16_amax16(p);
   if constexpr (!NV) m = max(m, __shfl_xor_sync(kAll, m, 1));
   float inv;
@@ -280,6 +281,7 @@ __global__ void __launch_bounds__(kThreads)
       uint32_t p[32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) p[i] = __byte_perm(w[2 * i], w[2 * i + 1], h ? 0x7632 : 0x5410);
+      if constexpr (NV) fp4_shift(p, ts);
       uint32_t codes[8], scales = 0;
 #pragma unroll
       for (int b = 0; b < 4; ++b) {

@@ -888,8 +888,8 @@ int moe_grouped_linear_bwd(const moe_bf16* dout, const moe_bf16* z, const moe_bf
  *               E2M1(v / s), value = code s
  * Roundings are to nearest, ties to even, saturating; of bf16 values by a
  * power-of-two t (moe_fp4_tensor_scale's) exactly so, by another t and of
- * float32 values up to 2^-22 of a border.  A block that holds a NaN or an
- * infinity reads back as NaN.
+ * float32 values up to 2^-22 of a border.  t is positive and finite.  A block
+ * that holds a NaN or an infinity reads back as NaN.
  *   codes   [rows, K / 2]
  *   scales  chunks of 512 bytes: 128 rows x 4 consecutive blocks of K (NV 64
  *           values, MX 128), row r and block b of a chunk at byte (r % 32) * 16
@@ -942,7 +942,8 @@ int moe_fp4_dequantize(const uint8_t* q, const uint8_t* s, const int32_t* offset
  * MMAs ([TE] "최적화 1: grouped GEMM"; [CuTe] "핵심 아이디어 / 구조 / 동작 방식").
  * For the rows of each expert:
  *   z = t_a t_e a_e w_e^T + bias_e     (products of codes and block scales
- *                                      exact, sums float32)
+ *                                      exact, sums float32; so is t_a t_e,
+ *                                      which has to be finite)
  *   out = act(z) + residual            (float32, rounded once)
  *   a_q, a_s  [M_cap, K] as moe_fp4_quantize / _permute write them with these
  *             offsets; a_t [1] or NULL
@@ -952,7 +953,8 @@ int moe_fp4_dequantize(const uint8_t* q, const uint8_t* s, const int32_t* offset
  *   out  [M_cap, n_out] float32, bf16, or 4 bits (out_type MOE_TYPE_*): then
  *        codes in `out` and scales in out_s, as moe_fp4_quantize would write
  *        them of the float32 outputs, with tensor scale out_t [1] (NULL: 1;
- *        MX: NULL), n_out a multiple of 64: the next product's a
+ *        MX: NULL; from 2^-117 to 2^117, so that a block's scale times it is
+ *        a normal number), n_out a multiple of 64: the next product's a
  * Both operands and a 4-bit output are of one format.  K, N multiples of 64, at
  * most 2^23; pointers 16-byte aligned (t's to their type).  Rows outside every
  * expert are not written.  Reruns are bitwise identical.  One launch.
