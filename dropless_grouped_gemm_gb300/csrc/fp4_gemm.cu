@@ -14,10 +14,15 @@
 //
 // Measured: a stage's four MMAs take 0.280 us (MX: 9.1 PFLOP/s while they run) and
 // 0.288 us (NV, with twelve copies of scales into TMEM a stage where MX has six),
-// and 1.6 to 2.1 us pass between two tiles' MMAs (commit, TMEM to registers,
-// release in both CTAs).  Bound by the MMAs where K is long (32,768 x 8,192 x 4,096
-// over 8 experts, bf16 out: 326 us NV, 309 MX, 7.1 PFLOP/s, at the power cap), by
-// those gaps where it is short (8,192 x 1,024 x 4,864 27 us).
+// and 2.2 to 2.7 us pass between two tiles' MMAs (commit, TMEM to registers,
+// release in both CTAs).  Some 0.6 of that is the second CTA's release of the
+// accumulator: its arrival is on a barrier of the first CTA, so it releases at
+// cluster scope, and that waits for the output stores that the SM has under way.
+// Bound by the MMAs where K is long (32,768 x 8,192 x 4,096 over 8 experts, bf16
+// out: 330 us NV, 311 MX, 7.1 PFLOP/s, at the power cap), by those gaps where it is
+// short (8,192 x 1,024 x 4,864 32 us NV, 31 MX).
+//   Tried, and compared when that arrival still released at CTA scope, which does
+// not reach the thread that waits (320 us, 301; 27, 27):
 //   Tiles of 192 columns leave TMEM for two accumulators and hide the gaps, but
 // an MMA of N = 192 takes 123 cycles (142 NV), nearly what one of N = 256 takes (130):
 // 8,192 rows x 4,864, NV, K = 1,024 26.2 us against 27.4, 2,048 41.8 against 39.7, 8,192
@@ -64,18 +69,6 @@ struct GC {
   static constexpr size_t most =
       smem(MOE_MAX_EXPERTS) > smem(box_experts) ? smem(MOE_MAX_EXPERTS) : smem(box_experts);
 };
-
-// An arrival at the pair's first CTA that hands over TMEM alone.  TMEM's order is
-// the tcgen05 fences', before this arrival and after the wait for it, and its reads
-// are over when tcgen05.wait::ld returns; no shared or global memory is passed on,
-// so the release is the CTA's.  One at cluster scope waits, beyond that, for the
-// output stores that the SM has under way: 800 to 2000 cycles a tile (8,192 x 1,024
-// x 4,864 31.8 us with it, 27.4 so; 32,768 x 8,192 x 4,096 331, 323; by one thread of the CTA for
-// all its warps 32.5, 335).
-__device__ __forceinline__ void mbar_arrive_tmem(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
-               : "memory");
-}
 
 struct GTile {
   int e, row0, rows, n0;    // first row of this CTA's block, its valid rows, first column
@@ -407,7 +400,7 @@ __global__ void __launch_bounds__(GT, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          if (rank != 0) mbar_arrive_tmem(tempty0);
+          if (rank != 0) mbar_arrive_cluster(tempty0);    // (the waiter is in the other CTA)
           else mbar_arrive(tempty_bar);
         }
       };
