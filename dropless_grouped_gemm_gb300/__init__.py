@@ -188,6 +188,8 @@ def lib():
         L.moe_fp4_scale_bytes.argtypes = [i64, i32, i32, i32]
         L.moe_fp4_tensor_scale.restype = i32
         L.moe_fp4_tensor_scale.argtypes = [vp, i32, i64, vp, vp]
+        L.moe_fp4_tensor_scale_rows.restype = i32
+        L.moe_fp4_tensor_scale_rows.argtypes = [vp, vp, i32, i32, i32, vp, vp, vp]
         L.moe_fp4_quantize.restype = i32
         L.moe_fp4_quantize.argtypes = [vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp]
         L.moe_fp4_permute.restype = i32
@@ -1309,16 +1311,30 @@ def _fp4_width(K, name):
         raise MoeError(f"{name} must have a multiple of 64 columns, got {K}")
 
 
-def fp4_tensor_scale(src: torch.Tensor, per_expert: bool = False, t=None, stream=None):
+def fp4_tensor_scale(src: torch.Tensor, per_expert: bool = False, t=None, stream=None, offsets=None,
+                     err=None):
     """nvfp4's scale of a bf16 tensor (moe_fp4_tensor_scale): float32 [1], or
     with ``per_expert`` [E], one for each src[e]: the smallest power of two t
-    with max|v| <= 6 * 448 t."""
-    _need(src, torch.bfloat16, "src")
+    with max|v| <= 6 * 448 t.  ``offsets`` [E+1]: of src's [rows, K] the
+    experts' rows alone (moe_fp4_tensor_scale_rows); without them all of src
+    counts, rows that no call has written too."""
+    _need(src, torch.bfloat16, "src", None if offsets is None else 2)
+    if offsets is not None and per_expert:
+        raise MoeError("offsets and per_expert exclude each other")
     E = src.shape[0] if per_expert else 1
     n = src.numel() // max(E, 1)
     _buffers((t, torch.float32, "t", (E,)))
+    if offsets is not None:
+        experts = _fp4_offsets(offsets)
+        _fp4_width(src.shape[1], "src")
     if t is None:
         t = _empty(E, torch.float32, src.device, stream)
+    if offsets is not None:
+        err = _err_word(err, src.device, stream)
+        rc = lib().moe_fp4_tensor_scale_rows(_ptr(src), _ptr(offsets), experts, *src.shape, _ptr(t),
+                                             _ptr(err), _stream(stream))
+        _check(rc, "moe_fp4_tensor_scale_rows")
+        return t
     rc = lib().moe_fp4_tensor_scale(_ptr(src), E, n, _ptr(t), _stream(stream))
     _check(rc, "moe_fp4_tensor_scale")
     return t

@@ -1500,7 +1500,29 @@ int moe_fp4_tensor_scale(const moe_bf16* src, int E, long long n, float* t, void
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int launches = 0;
   ev_begin(st);
-  const cudaError_t e = moe::launch_fp4_tensor_scale(src, E, n, moe::Fp4Rows{}, 0, t, sms, st, &launches);
+  const cudaError_t e =
+      moe::launch_fp4_tensor_scale(src, E, n, moe::Fp4Rows{}, 0, t, nullptr, sms, st, &launches);
+  ev_end(st);
+  g_last_launches = launches;
+  return cuda_rc(e);
+}
+
+int moe_fp4_tensor_scale_rows(const moe_bf16* src, const int32_t* offsets, int E, int rows, int K,
+                              float* t, int32_t* err, void* stream) {
+  g_last_launches = 0;
+  g_split_extra = 0;
+  const int rc = check_fp4(E, rows, K, MOE_FP4_NV);
+  if (rc) return rc;
+  if (!t || (rows > 0 && (!src || !offsets || !err))) return MOE_E_NULL;
+  if (misaligned(src) || off_type(t, MOE_TYPE_F32)) return MOE_E_ALIGN;
+  const int sms = num_sms_current();
+  if (sms <= 0) return MOE_E_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int launches = 0;
+  ev_begin(st);
+  const cudaError_t e =
+      moe::launch_fp4_tensor_scale(src, 1, static_cast<long long>(rows) * K,
+                                   moe::Fp4Rows{offsets, E, rows, rows}, K, t, err, sms, st, &launches);
   ev_end(st);
   g_last_launches = launches;
   return cuda_rc(e);
@@ -1768,7 +1790,7 @@ int moe_fp4_linear_bwd(const moe_bf16* dout, const moe_bf16* z, const moe_bf16* 
     const cudaError_t e =
         top ? moe::launch_fp4_power(w.t, 1, s)
             : moe::launch_fp4_tensor_scale(gz, 1, static_cast<long long>(M_cap) * N,
-                                           moe::Fp4Rows{offsets, E, M_cap, M_cap}, N, w.t, sms, s, &n);
+                                           moe::Fp4Rows{offsets, E, M_cap, M_cap}, N, w.t, err, sms, s, &n);
     ev_end(s);
     if (e != cudaSuccess) return MOE_E_CUDA;
     launches += n;

@@ -74,9 +74,10 @@ cudaError_t launch_fp4_dequantize(const uint8_t* q, const uint8_t* s, const Fp4R
 
 // t[e] = the smallest power of two with max|v| <= 6 * 448 t over the finite
 // values of src[e] (n of each, a multiple of 8); 1 where they are all zero.  With
-// r.offsets (E 1, n = r.rows K) of the experts' rows alone
+// r.offsets (E 1, n = r.rows K) of the experts' rows alone (bad offsets: err)
 cudaError_t launch_fp4_tensor_scale(const uint16_t* src, int E, long long n, const Fp4Rows& r,
-                                    int K, float* t, int num_sms, cudaStream_t st, int* launches);
+                                    int K, float* t, int32_t* err, int num_sms, cudaStream_t st,
+                                    int* launches);
 // ... t [E] holding the largest magnitudes
 cudaError_t launch_fp4_power(float* t, int E, cudaStream_t st);
 

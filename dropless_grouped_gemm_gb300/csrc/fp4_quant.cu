@@ -368,25 +368,15 @@ __global__ void __launch_bounds__(kThreads)
 // L2 18.5 us).
 __global__ void __launch_bounds__(kThreads)
     amax_kernel(const uint4* __restrict__ src, long long n8, const Fp4Rows r, int row8,
-                uint32_t* __restrict__ top) {
+                uint32_t* __restrict__ top, int32_t* err) {
   const int e = blockIdx.y;
   const uint4* p = src + static_cast<long long>(e) * n8;
   __shared__ uint32_t s_top[kWarps];
   if (r.offsets != nullptr) {
-    __shared__ int s_lo, s_hi;
-    if (threadIdx.x < 32) {
-      int hi = 0;
-      for (int i = threadIdx.x; i <= r.E; i += 32)
-        hi = max(hi, min(r.offsets[i], static_cast<int>(r.rows)));
-      hi = __reduce_max_sync(kAll, hi);
-      if (threadIdx.x == 0) {
-        s_lo = max(min(r.offsets[0], static_cast<int>(r.rows)), 0);
-        s_hi = hi;
-      }
-    }
-    __syncthreads();
-    p = src + static_cast<long long>(s_lo) * row8;
-    n8 = static_cast<long long>(s_hi - s_lo) * row8;
+    extern __shared__ int s_off[];
+    load_offsets(r, s_off, err);
+    p = src + static_cast<long long>(s_off[0]) * row8;
+    n8 = static_cast<long long>(s_off[r.E] - s_off[0]) * row8;
   }
   uint32_t m = 0;
   const long long step = static_cast<long long>(gridDim.x) * kThreads;
@@ -485,7 +475,8 @@ cudaError_t launch_fp4_dequantize(const uint8_t* q, const uint8_t* s, const Fp4R
 }
 
 cudaError_t launch_fp4_tensor_scale(const uint16_t* src, int E, long long n, const Fp4Rows& r,
-                                    int K, float* t, int num_sms, cudaStream_t st, int* launches) {
+                                    int K, float* t, int32_t* err, int num_sms, cudaStream_t st,
+                                    int* launches) {
   *launches = 0;
   cudaError_t e = cudaMemsetAsync(t, 0, static_cast<size_t>(E) * sizeof(float), st);
   if (e != cudaSuccess) return e;
@@ -493,8 +484,8 @@ cudaError_t launch_fp4_tensor_scale(const uint16_t* src, int E, long long n, con
     const long long want = (n / 8 + 4 * kThreads - 1) / (4 * kThreads);
     const long long most = (8LL * num_sms + E - 1) / E;
     const dim3 grid(static_cast<unsigned>(want < most ? want : most), E);
-    amax_kernel<<<grid, kThreads, 0, st>>>(reinterpret_cast<const uint4*>(src), n / 8, r, K / 8,
-                                           reinterpret_cast<uint32_t*>(t));
+    amax_kernel<<<grid, kThreads, off_bytes(r), st>>>(reinterpret_cast<const uint4*>(src), n / 8, r,
+                                                      K / 8, reinterpret_cast<uint32_t*>(t), err);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     ++*launches;

@@ -905,7 +905,11 @@ int moe_grouped_linear_bwd(const moe_bf16* dout, const moe_bf16* z, const moe_bf
  * moe_fp4_tensor_scale  t [E]: for src [E, n] bf16, of each e the smallest
  *                       power of two with max|v| <= 6 * 448 t over its finite
  *                       values (1 where there are none above 0).  n a multiple
- *                       of 64.  Two launches.
+ *                       of 64.  All of src is read: a buffer with rows outside
+ *                       every expert, which no call writes, takes the next one.
+ *                       Two launches.
+ * moe_fp4_tensor_scale_rows  t [1] of the experts' rows alone: src [rows, K],
+ *                       offsets [E+1].  Two launches.
  * moe_fp4_quantize      src [rows, K] bf16 -> q, s.  offsets [E+1] (rows outside
  *                       every expert are not written), or NULL: E experts of
  *                       rows / E rows.  t [1] or NULL (MX: NULL).  One launch.
@@ -925,6 +929,8 @@ int moe_grouped_linear_bwd(const moe_bf16* dout, const moe_bf16* z, const moe_bf
  */
 size_t moe_fp4_scale_bytes(long long rows, int E, int K, int format);
 int moe_fp4_tensor_scale(const moe_bf16* src, int E, long long n, float* t, void* stream);
+int moe_fp4_tensor_scale_rows(const moe_bf16* src, const int32_t* offsets, int E, int rows, int K,
+                              float* t, int32_t* err, void* stream);
 int moe_fp4_quantize(const moe_bf16* src, const int32_t* offsets, int E, int rows, int K,
                      int format, const float* t, uint8_t* q, uint8_t* s, int32_t* err,
                      void* stream);
