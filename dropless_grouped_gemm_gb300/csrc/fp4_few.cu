@@ -555,7 +555,8 @@ cudaError_t few_t(const CUtensorMap& tw, const CUtensorMap& tx, const Fp4GemmArg
 // 260 ns, 350 with more than 16 tokens; ending a tile 1.5 us, joining a split 2.5;
 // where no other tile reads a tile's weights, their share of 6.6 TB/s at least.
 // The pairs' kernel: 4 us, a stage 300 ns, a tile's end 1.9 us, and the same
-// share.  Measured, us, this kernel / the pairs': dense 64 x 4096 x 4096 8.7 /
+// share.  (Fitted before the release of the pairs' accumulator took 0.6 us more, from a
+// pair's second tile on.)  Measured, us, this kernel / the pairs': dense 64 x 4096 x 4096 8.7 /
 // 10.1, 128 rows 9.6 / 10.7, 256 rows 11.5 / 10.7, 512 rows 16.7 / 10.8, 1024 rows
 // 28.7 / 12.3, 256 x 7168 x 2048 11.5 / 13.9; 57 experts with 128 rows, 2048 x 7168
 // 77.2 / 90.3, 7168 x 4096 142 / 153, with 2000 rows, 2048 x 7168 83.7 / 96.4; 8

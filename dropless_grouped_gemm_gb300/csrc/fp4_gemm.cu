@@ -19,7 +19,7 @@
 // accumulator: its arrival is on a barrier of the first CTA, so it releases at
 // cluster scope, and that waits for the output stores that the SM has under way.
 // Bound by the MMAs where K is long (32,768 x 8,192 x 4,096 over 8 experts, bf16
-// out: 330 us NV, 311 MX, 7.1 PFLOP/s, at the power cap), by those gaps where it is
+// out: 330 us NV, 311 MX, 6.7 and 7.1 PFLOP/s, at the power cap), by those gaps where it is
 // short (8,192 x 1,024 x 4,864 32 us NV, 31 MX).
 //   Tried, and compared when that arrival still released at CTA scope, which does
 // not reach the thread that waits (320 us, 301; 27, 27):

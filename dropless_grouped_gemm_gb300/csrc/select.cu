@@ -24,8 +24,8 @@
 // by a network of minima and maxima.  Each of the k rounds then is one maximum
 // over the warp, one ballot, and a shift of the owner's keys: 18 instructions.
 // Bound by instructions on long batches (65,536 x 256, sigmoid, bias, 8 groups:
-// 144 us with a search of the lane's values in every round, 91 now), by launch latency on
-// short ones.  Backward: a warp per token, the k gradients scattered into a row
+// 144 us with a search of the lane's values in every round, 91 with the sort; by a batch's
+// rows in doubt 90 to 112 now), by launch latency on short ones.  Backward: a warp per token, the k gradients scattered into a row
 // in shared memory that leaves in 16-byte stores, the next token's pairs read
 // meanwhile; a softmax's exponentials are taken once and wait in that row (taken
 // again for the output: 48 us for 65,536 x 256, now 39).  Bound by latency and by
